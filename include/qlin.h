@@ -366,6 +366,118 @@ int qlin_int4_scale_zero_grad(const qlin_qweight *w, const uint16_t *x, int64_t 
                               const uint16_t *dy, float *dscale, float *dzero,
                               hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit rows: int8 codes[rows][d] and one fp32 scale per row, the row
+ * standing for codes * scale.  One format for activations kept for the
+ * backward pass, for the operands of the 8-bit product and for weights held
+ * in 8 bits (a row is then an output channel).  With every step taken on the
+ * exact real values,
+ *     a = max_k |x[m][k]|,  scale[m] = RN32(a / 127),
+ *     codes[m][k] = round_half_even(127 x[m][k] / a)      (-127 .. 127),
+ * and a row of zeros has scale 0 and codes 0.  A row that holds NaN or an
+ * infinity has scale NaN and codes 0: whatever is computed from it is NaN for
+ * that row and for no other.  The functions of this part are asynchronous and
+ * report nothing from the device.  [QLoRA "Background: what is
+ * quantization?": absmax scaling of a block, here one row]
+ * ---------------------------------------------------------------------- */
+
+/* Element type of an input that may come in either. */
+typedef enum {
+  QLIN_BF16 = 1,
+  QLIN_F32 = 2
+} qlin_dtype;
+
+/*
+ * Rows to 8 bits.
+ *   x       bf16 or fp32 (dtype) [rows][d];  1 <= rows, 1 <= d <= 131072
+ *   codes   int8[rows][d];  scale fp32[rows]  (outputs)
+ *   values  bf16[rows][d] (output, may be NULL): RN16(codes * scale), what a
+ *           layer computes with when its backward pass reads the codes
+ * Asynchronous on `stream`.
+ */
+int qlin_quantize_q8(const void *x, int32_t dtype, int64_t rows, int64_t d, int8_t *codes,
+                     float *scale, uint16_t *values, hipStream_t stream);
+
+/* out = bf16(codes * scale), [rows][d]; sizes as for qlin_quantize_q8. */
+int qlin_dequant_q8(const int8_t *codes, const float *scale, int64_t rows, int64_t d,
+                    uint16_t *out, hipStream_t stream);
+
+/*
+ * Root-mean-square norm of x + residual, given out as 8-bit rows:
+ *     h = x + residual,  rstd[m] = 1 / sqrt(mean_k h^2 + eps),
+ *     y = h rstd gamma,  (codes, scale) = 8-bit rows of y.
+ *   x         bf16[M][d];  1 <= M, 1 <= d <= 131072
+ *   residual  bf16[M][d] or NULL (h = x; then h must be NULL too)
+ *   gamma     bf16[d];  eps finite, >= 0 (a row of zeros with eps = 0 has
+ *             rstd infinite and is a non-finite row)
+ *   h         bf16[M][d] (output): the sum rounded once; y is formed from the
+ *             sum before that rounding
+ *   codes, scale  the 8-bit rows of y (outputs)
+ *   rstd      fp32[M] (output, may be NULL), for qlin_rmsnorm_bwd
+ *   values    bf16[M][d] (output, may be NULL): RN16(codes * scale)
+ * A row whose sum of squares leaves fp32's range counts as non-finite.
+ * Outputs must not overlap inputs.  Asynchronous on `stream`.
+ */
+int qlin_rmsnorm_q8(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t M,
+                    int64_t d, float eps, uint16_t *h, int8_t *codes, float *scale, float *rstd,
+                    uint16_t *values, hipStream_t stream);
+
+/*
+ * Gradient of the norm (the 8-bit rounding of y passed straight through):
+ *     xh = h rstd,  g = dy gamma,
+ *     dx = rstd (g - xh mean_k(g xh)) + dh,   dgamma[k] = sum_m dy xh
+ *   h, dy   bf16[M][d];  gamma bf16[d];  rstd fp32[M] (from qlin_rmsnorm_q8;
+ *           h is its x where it had no residual)
+ *   dh      bf16[M][d] or NULL: gradient that reaches h by another way (the
+ *           residual stream)
+ *   dx      bf16[M][d] (output): the gradient of x and of the residual
+ *   dgamma  fp32[d] (output), summed in a fixed order
+ *   workspace, ws_bytes  >= qlin_rmsnorm_workspace_bytes(M, d) (0 for invalid
+ *           sizes); no initial contents needed
+ * Outputs must not overlap inputs.  Asynchronous on `stream`.
+ */
+size_t qlin_rmsnorm_workspace_bytes(int64_t M, int64_t d);
+int qlin_rmsnorm_bwd(const uint16_t *h, const uint16_t *gamma, const float *rstd,
+                     const uint16_t *dy, const uint16_t *dh, int64_t M, int64_t d, uint16_t *dx,
+                     float *dgamma, void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Product of 8-bit rows: y[m][n] = x_scale[m] w_scale[n] sum_k xq[m][k] wq[n][k].
+ *   xq, x_scale  8-bit rows [M][K] (tokens);  1 <= M
+ *   wq, w_scale  8-bit rows [N][K] (output channels);  1 <= N;  K % 16 == 0,
+ *                16 <= K <= 131056 (any int8 codes then sum inside int32)
+ *   y            bf16[M][N] (output): the integer sum is exact; one rounding
+ *                to fp32 of it, one for each scale, one to bf16
+ *   workspace, ws_bytes  >= qlin_w8a8_workspace_bytes(M, N, K) (0 for invalid
+ *                sizes); zero-filled once before its first use, as for
+ *                qlin_workspace_bytes
+ * Asynchronous on `stream`.
+ */
+size_t qlin_w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int qlin_w8a8_fwd(const int8_t *xq, const float *x_scale, int64_t M, const int8_t *wq,
+                  const float *w_scale, int64_t N, int64_t K, uint16_t *y, void *workspace,
+                  size_t ws_bytes, hipStream_t stream);
+
+/*
+ * qlin_bwd from an 8-bit checkpoint: the layer's input is given as 8-bit rows
+ * (qlin_quantize_q8, or the rows qlin_rmsnorm_q8 gave) instead of bf16, so
+ * that M (d_in + 4) bytes are kept between the passes instead of 2 M d_in.
+ *     du = s dY B,  dB = s dY^T u,  dA = du^T pool(codes * scale),
+ *     dX = dY dequant(Wq) + expand(du A)
+ *   xq, x_scale  8-bit rows [M][d_in]
+ *   u            fp32[M][r] from qlin_fwd's u_out (required)
+ *   the rest, and the outputs dx (NULL skips it), dA, dB, as for qlin_bwd
+ *   workspace, ws_bytes  >= qlin_bwd_q8_workspace_bytes(w, M, r, pool) (0 for
+ *                invalid arguments); zero-filled once before its first use, as
+ *                for qlin_workspace_bytes
+ * Asynchronous on `stream`.
+ */
+size_t qlin_bwd_q8_workspace_bytes(const qlin_qweight *w, int64_t M, int32_t r, int32_t pool);
+int qlin_bwd_q8(const qlin_qweight *w, const int8_t *xq, const float *x_scale, int64_t M,
+                const uint16_t *A, const uint16_t *B, int32_t r, float s, int32_t pool,
+                const uint16_t *dy, const float *u, uint16_t *dx, uint16_t *dA, uint16_t *dB,
+                void *workspace, size_t ws_bytes, hipStream_t stream);
+
 /*
  * Test helper: writes the dequantized weight W_bf16 (bf16[d_out][d_in]) using
  * the same in-register lookup-table decode as the fused kernels.  Never

@@ -14,14 +14,16 @@ from typing import Optional
 
 import numpy as np
 
-from ._lib import (EXPORTS, LIB_PATH, QLIN_FMT_INT4_GROUP, QLIN_FMT_NF, QLIN_FMT_NF4, QlinError,
-                   QWeightStruct, check, lib)
+from ._lib import (EXPORTS, LIB_PATH, QLIN_BF16, QLIN_F32, QLIN_FMT_INT4_GROUP, QLIN_FMT_NF,
+                   QLIN_FMT_NF4, QlinError, QWeightStruct, check, lib)
 
 __all__ = [
     "QWeight", "QlinError", "qlin_nf4_codebook", "qlin_quantize_nf4", "qlin_nf_codebook",
     "qlin_quantize_nf",
     "qlin_quantize_int4_group", "qlin_workspace_bytes", "qlin_fwd", "qlin_fwd_noalloc", "qlin_bwd",
-    "qlin_dequant_bf16", "qlin_qa_merge", "qlin_int4_scale_zero_grad", "qlin_profile_next_launch", "EXPORTS", "LIB_PATH",
+    "qlin_dequant_bf16", "qlin_qa_merge", "qlin_int4_scale_zero_grad", "qlin_profile_next_launch",
+    "Q8Rows", "qlin_quantize_q8", "qlin_dequant_q8", "qlin_rmsnorm_q8", "qlin_rmsnorm_bwd", "qlin_w8a8_fwd",
+    "qlin_bwd_q8", "EXPORTS", "LIB_PATH",
 ]
 
 
@@ -311,6 +313,210 @@ def qlin_dequant_bf16(w: QWeight):
     check(lib().qlin_dequant_bf16(ctypes.byref(s_), out.data_ptr(), _stream(w.device)),
           "qlin_dequant_bf16")
     return out
+
+
+# ------------------------------------------------------------- 8-bit rows
+
+@dataclasses.dataclass
+class Q8Rows:
+    """Rows in 8 bits: row m stands for codes[m] * scale[m]."""
+    codes: object                 # int8 [rows][d]
+    scale: object                 # fp32 [rows]
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scale.numel()
+
+
+def _need_q8(q: Q8Rows, shape, name):
+    torch = _torch()
+    _need(q.codes, torch.int8, shape, name + ".codes")
+    _need(q.scale, torch.float32, shape[:1], name + ".scale")
+
+
+_WS_STREAM = {}
+
+
+def _stream_workspace(device, stream: int, nbytes: int):
+    """A zero-filled workspace of at least ``nbytes`` for calls on one stream of
+    one device (grown on demand), so that calls in flight on different streams
+    never share one."""
+    torch = _torch()
+    key = (device.index, stream)
+    ws = _WS_STREAM.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        _WS_STREAM[key] = ws
+    return ws
+
+
+def qlin_quantize_q8(x, codes=None, scale=None, values=None) -> Q8Rows:
+    """Rows of x (bf16 or fp32, [rows][d]) in 8 bits, one scale per row.
+    ``values`` (bf16 [rows][d]) receives codes * scale when given."""
+    torch = _torch()
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x: expected a bfloat16 or float32 matrix, got {x.dtype} {tuple(x.shape)}")
+    rows, d = x.shape
+    dev = x.device
+    _need(x, x.dtype, (rows, d), "x")
+    if codes is None:
+        codes = torch.empty((rows, d), dtype=torch.int8, device=dev)
+    else:
+        _need(codes, torch.int8, (rows, d), "codes")
+    if scale is None:
+        scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+    else:
+        _need(scale, torch.float32, (rows,), "scale")
+    if values is not None:
+        _need(values, torch.bfloat16, (rows, d), "values")
+    check(lib().qlin_quantize_q8(x.data_ptr(), QLIN_BF16 if x.dtype == torch.bfloat16 else QLIN_F32, rows, d,
+                                 codes.data_ptr(), scale.data_ptr(), _ptr(values), _stream(dev)),
+          "qlin_quantize_q8")
+    return Q8Rows(codes, scale)
+
+
+def qlin_dequant_q8(q: Q8Rows, out=None):
+    """bf16(codes * scale), [rows][d]."""
+    torch = _torch()
+    rows, d = q.codes.shape
+    _need_q8(q, (rows, d), "q")
+    if out is None:
+        out = torch.empty((rows, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out, torch.bfloat16, (rows, d), "out")
+    check(lib().qlin_dequant_q8(q.codes.data_ptr(), q.scale.data_ptr(), rows, d, out.data_ptr(),
+                                _stream(q.device)), "qlin_dequant_q8")
+    return out
+
+
+def qlin_rmsnorm_q8(x, gamma, eps: float, residual=None, want_values: bool = False, h=None, codes=None,
+                    scale=None, rstd=None, values=None):
+    """Root-mean-square norm of x + residual as 8-bit rows.  Returns (h, q,
+    rstd, values): h = bf16(x + residual) (None without a residual), q the
+    8-bit rows of h rstd gamma, values = bf16(q.codes * q.scale) or None."""
+    torch = _torch()
+    M, d = x.shape
+    dev = x.device
+    _need(x, torch.bfloat16, (M, d), "x")
+    _need(gamma, torch.bfloat16, (d,), "gamma")
+    if residual is not None:
+        _need(residual, torch.bfloat16, (M, d), "residual")
+        if h is None:
+            h = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _need(h, torch.bfloat16, (M, d), "h")
+    if codes is None:
+        codes = torch.empty((M, d), dtype=torch.int8, device=dev)
+    else:
+        _need(codes, torch.int8, (M, d), "codes")
+    if scale is None:
+        scale = torch.empty((M,), dtype=torch.float32, device=dev)
+    else:
+        _need(scale, torch.float32, (M,), "scale")
+    if rstd is None:
+        rstd = torch.empty((M,), dtype=torch.float32, device=dev)
+    else:
+        _need(rstd, torch.float32, (M,), "rstd")
+    if values is not None:
+        _need(values, torch.bfloat16, (M, d), "values")
+    elif want_values:
+        values = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
+    check(lib().qlin_rmsnorm_q8(x.data_ptr(), _ptr(residual), gamma.data_ptr(), M, d, float(eps), _ptr(h),
+                                codes.data_ptr(), scale.data_ptr(), rstd.data_ptr(), _ptr(values),
+                                _stream(dev)), "qlin_rmsnorm_q8")
+    return h, Q8Rows(codes, scale), rstd, values
+
+
+def qlin_rmsnorm_bwd(h, gamma, rstd, dy, dh=None, dx=None, dgamma=None, ws=None):
+    """Gradient of the norm: returns (dx, dgamma).  h is the norm's sum (its x
+    where it had no residual); dh, when given, is added to dx."""
+    torch = _torch()
+    M, d = h.shape
+    dev = h.device
+    _need(h, torch.bfloat16, (M, d), "h")
+    _need(gamma, torch.bfloat16, (d,), "gamma")
+    _need(rstd, torch.float32, (M,), "rstd")
+    _need(dy, torch.bfloat16, (M, d), "dy")
+    if dh is not None:
+        _need(dh, torch.bfloat16, (M, d), "dh")
+    if dx is None:
+        dx = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(dx, torch.bfloat16, (M, d), "dx")
+    if dgamma is None:
+        dgamma = torch.empty((d,), dtype=torch.float32, device=dev)
+    else:
+        _need(dgamma, torch.float32, (d,), "dgamma")
+    st = _stream(dev)
+    if ws is None:
+        ws = _stream_workspace(dev, st, lib().qlin_rmsnorm_workspace_bytes(M, d))
+    check(lib().qlin_rmsnorm_bwd(h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), dy.data_ptr(), _ptr(dh),
+                                 M, d, dx.data_ptr(), dgamma.data_ptr(), ws.data_ptr(), ws.numel(), st),
+          "qlin_rmsnorm_bwd")
+    return dx, dgamma
+
+
+def qlin_w8a8_fwd(x: Q8Rows, w: Q8Rows, y=None, ws=None):
+    """y[m][n] = bf16(x.scale[m] w.scale[n] sum_k x.codes[m][k] w.codes[n][k])."""
+    torch = _torch()
+    M, K = x.codes.shape
+    N = w.codes.shape[0]
+    dev = x.device
+    _need_q8(x, (M, K), "x")
+    _need_q8(w, (N, K), "w")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(y, torch.bfloat16, (M, N), "y")
+    st = _stream(dev)
+    if ws is None:
+        ws = _stream_workspace(dev, st, lib().qlin_w8a8_workspace_bytes(M, N, K))
+    check(lib().qlin_w8a8_fwd(x.codes.data_ptr(), x.scale.data_ptr(), M, w.codes.data_ptr(),
+                              w.scale.data_ptr(), N, K, y.data_ptr(), ws.data_ptr(), ws.numel(), st),
+          "qlin_w8a8_fwd")
+    return y
+
+
+def qlin_bwd_q8(w: QWeight, x: Q8Rows, A, B, r: int, s: float, dy, u, pool: int = 1, need_dx: bool = True,
+                dx=None, dA=None, dB=None, ws=None):
+    """qlin_bwd with the layer's input as an 8-bit checkpoint (``x``) and u from
+    the forward pass.  Returns (dx, dA, dB); dx is None unless wanted."""
+    torch = _torch()
+    M = x.codes.shape[0]
+    dev = x.device
+    _need_q8(x, (M, w.d_in), "x")
+    _need(dy, torch.bfloat16, (M, w.d_out), "dy")
+    _need(A, torch.bfloat16, (r, w.d_in // pool), "A")
+    _need(B, torch.bfloat16, (w.d_out, r), "B")
+    _need(u, torch.float32, (M, r), "u")
+    if not need_dx:
+        dx = None
+    elif dx is None:
+        dx = torch.empty((M, w.d_in), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(dx, torch.bfloat16, (M, w.d_in), "dx")
+    if dA is None:
+        dA = torch.empty((r, w.d_in // pool), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(dA, torch.bfloat16, (r, w.d_in // pool), "dA")
+    if dB is None:
+        dB = torch.empty((w.d_out, r), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(dB, torch.bfloat16, (w.d_out, r), "dB")
+    s_ = w.struct()
+    st = _stream(dev)
+    if ws is None:
+        nbytes = lib().qlin_bwd_q8_workspace_bytes(ctypes.byref(s_), M, r, pool)
+        if nbytes == 0:
+            raise QlinError(2, "qlin_bwd_q8_workspace_bytes")
+        ws = _stream_workspace(dev, st, nbytes)
+    check(lib().qlin_bwd_q8(ctypes.byref(s_), x.codes.data_ptr(), x.scale.data_ptr(), M, A.data_ptr(),
+                            B.data_ptr(), r, float(s), pool, dy.data_ptr(), u.data_ptr(), _ptr(dx),
+                            dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.numel(), st), "qlin_bwd_q8")
+    return dx, dA, dB
 
 
 def qlin_profile_next_launch(kernel: Optional[str], start=None, stop=None) -> None:

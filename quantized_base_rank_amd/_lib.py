@@ -12,6 +12,8 @@ QLIN_OK = 0
 QLIN_FMT_NF4 = 1
 QLIN_FMT_INT4_GROUP = 2
 QLIN_FMT_NF = 3
+QLIN_BF16 = 1
+QLIN_F32 = 2
 
 #: every symbol include/qlin.h declares
 EXPORTS = (
@@ -29,6 +31,15 @@ EXPORTS = (
     "qlin_int4_scale_zero_grad",
     "qlin_lq_workspace_bytes",
     "qlin_lq_nf4",
+    "qlin_quantize_q8",
+    "qlin_dequant_q8",
+    "qlin_rmsnorm_q8",
+    "qlin_rmsnorm_workspace_bytes",
+    "qlin_rmsnorm_bwd",
+    "qlin_w8a8_workspace_bytes",
+    "qlin_w8a8_fwd",
+    "qlin_bwd_q8_workspace_bytes",
+    "qlin_bwd_q8",
     "qlin_profile_next_launch",
     "qlin_status_string",
 )
@@ -84,6 +95,16 @@ def lib() -> ctypes.CDLL:
         "qlin_lq_workspace_bytes": (sz, [i64, i64, i32]),
         "qlin_lq_nf4": (ctypes.c_int, [vp, i64, i64, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, sz,
                                        vp]),
+        "qlin_quantize_q8": (ctypes.c_int, [vp, i32, i64, i64, vp, vp, vp, vp]),
+        "qlin_dequant_q8": (ctypes.c_int, [vp, vp, i64, i64, vp, vp]),
+        "qlin_rmsnorm_q8": (ctypes.c_int, [vp, vp, vp, i64, i64, f32, vp, vp, vp, vp, vp, vp]),
+        "qlin_rmsnorm_workspace_bytes": (sz, [i64, i64]),
+        "qlin_rmsnorm_bwd": (ctypes.c_int, [vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
+        "qlin_w8a8_workspace_bytes": (sz, [i64, i64, i64]),
+        "qlin_w8a8_fwd": (ctypes.c_int, [vp, vp, i64, vp, vp, i64, i64, vp, vp, sz, vp]),
+        "qlin_bwd_q8_workspace_bytes": (sz, [qp, i64, i32, i32]),
+        "qlin_bwd_q8": (ctypes.c_int,
+                        [qp, vp, vp, i64, vp, vp, i32, f32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
         "qlin_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     }
     for name, (res, args) in sig.items():

@@ -861,6 +861,216 @@ int qlin_int4_scale_zero_grad(const qlin_qweight* w, const uint16_t* x, int64_t 
                            [&] { return launch_int4_scale_zero_grad(a, stream); }));
 }
 
+// --------------------------------------------------------------- 8-bit rows
+
+namespace {
+
+constexpr int64_t kMaxRowLen = 131072;   // columns of an 8-bit row
+constexpr int64_t kMaxProductK = 131056; // 128 * 128 * K stays below 2^31
+
+int check_rows(int64_t rows, int64_t d) {
+  if (rows < 1 || rows > (int64_t{1} << 31) || d < 1 || d > kMaxRowLen) return QLIN_E_SHAPE;
+  return QLIN_OK;
+}
+
+// Workspace of qlin_bwd_q8, after the counter region.
+struct BwdQ8Plan {
+  bool few = false;  // <= 16 tokens: du and dB in one launch, dX streamed
+  bool fits = true;
+  int nt_splits = 1, tn2_splits = 1, ds_splits = 1;
+  size_t off_du = 0, off_Bt = 0, off_At = 0, off_z = 0, off_partial = 0, off_tc = 0, total = 0;
+};
+
+BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t pool) {
+  BwdQ8Plan p;
+  const Plan q = make_plan(w, M, r, pool);
+  const int64_t N = w->d_out, K = w->d_in, G = K / pool;
+  p.few = M <= kSmallM && dx_stream_fits(N, K, fmt_of(w));
+  p.nt_splits = q.nt_splits_du;
+  p.tn2_splits = q.tn2_splits_dB;
+  p.ds_splits = q.ds_splits;
+  int64_t counters, partial;
+  if (p.few) {
+    counters = std::max<int64_t>(1, p.ds_splits > 1 ? dx_stream_panels(K) : 0);
+    partial = std::max<int64_t>(adapter_few_partial_floats(N), dx_stream_partial_floats(N, K, fmt_of(w)));
+  } else {
+    counters = std::max<int64_t>(p.nt_splits > 1 ? nt_tiles(M) : 0, p.tn2_splits > 1 ? tn2_tiles(N) : 0);
+    partial = std::max<int64_t>(nt_partial_floats(M, p.nt_splits), tn2_partial_floats(N, r, p.tn2_splits));
+  }
+  p.fits = counters <= kCounterWords;
+  size_t off = kCounterBytes;
+  p.off_du = off;      off = align256(off + static_cast<size_t>(M) * r * sizeof(float));
+  p.off_Bt = off;      off = align256(off + (p.few ? 0 : static_cast<size_t>(N) * r * sizeof(uint16_t)));
+  p.off_At = off;      off = align256(off + (p.few ? 0 : static_cast<size_t>(G) * r * sizeof(uint16_t)));
+  p.off_z = off;       off = align256(off + (p.few ? 0 : 2 * static_cast<size_t>(M) * tn2_jp(r) * sizeof(uint16_t)));
+  p.off_partial = off; off = align256(off + static_cast<size_t>(partial) * sizeof(float));
+  p.off_tc = off;      off += transcode_bytes(w);
+  p.total = off;
+  return p;
+}
+
+}  // namespace
+
+int qlin_quantize_q8(const void* x, int32_t dtype, int64_t rows, int64_t d, int8_t* codes, float* scale,
+                     uint16_t* values, hipStream_t stream) {
+  if (x == nullptr || codes == nullptr || scale == nullptr) return QLIN_E_NULL;
+  if (dtype != QLIN_BF16 && dtype != QLIN_F32) return QLIN_E_UNSUPPORTED;
+  const int st = check_rows(rows, d);
+  if (st != QLIN_OK) return st;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scale) || !aligned16(values)) return QLIN_E_ALIGN;
+  Q8RowsArgs a{};
+  a.x = x; a.rows = rows; a.d = d; a.codes = codes; a.scale = scale; a.values = values;
+  return hip_status(hooked("k_quant_q8", stream, [&] { return launch_quant_q8(a, dtype == QLIN_F32, stream); }));
+}
+
+int qlin_dequant_q8(const int8_t* codes, const float* scale, int64_t rows, int64_t d, uint16_t* out,
+                    hipStream_t stream) {
+  if (codes == nullptr || scale == nullptr || out == nullptr) return QLIN_E_NULL;
+  const int st = check_rows(rows, d);
+  if (st != QLIN_OK) return st;
+  if (!aligned16(codes) || !aligned16(scale) || !aligned16(out)) return QLIN_E_ALIGN;
+  return hip_status(launch_dequant_q8(codes, scale, rows, d, out, stream));
+}
+
+int qlin_rmsnorm_q8(const uint16_t* x, const uint16_t* residual, const uint16_t* gamma, int64_t M, int64_t d,
+                    float eps, uint16_t* h, int8_t* codes, float* scale, float* rstd, uint16_t* values,
+                    hipStream_t stream) {
+  if (x == nullptr || gamma == nullptr || codes == nullptr || scale == nullptr) return QLIN_E_NULL;
+  if (residual != nullptr && h == nullptr) return QLIN_E_NULL;
+  if (residual == nullptr && h != nullptr) return QLIN_E_UNSUPPORTED;
+  const int st = check_rows(M, d);
+  if (st != QLIN_OK) return st;
+  if (!std::isfinite(eps) || eps < 0.0f) return QLIN_E_SHAPE;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(h) || !aligned16(codes) ||
+      !aligned16(scale) || !aligned16(rstd) || !aligned16(values))
+    return QLIN_E_ALIGN;
+  RmsNormArgs a{};
+  a.x = x; a.res = residual; a.gamma = gamma; a.M = M; a.d = d; a.eps = eps; a.h = h; a.codes = codes;
+  a.scale = scale; a.rstd = rstd; a.values = values;
+  return hip_status(hooked("k_rmsnorm_q8", stream, [&] { return launch_rmsnorm_q8(a, stream); }));
+}
+
+size_t qlin_rmsnorm_workspace_bytes(int64_t M, int64_t d) {
+  if (check_rows(M, d) != QLIN_OK) return 0;
+  // (the counter region stays untouched, so that one workspace may serve
+  // this and the calls that keep counters in it)
+  return kCounterBytes + align256(static_cast<size_t>(rmsnorm_bwd_partial_floats(M, d)) * sizeof(float));
+}
+
+int qlin_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd, const uint16_t* dy,
+                     const uint16_t* dh, int64_t M, int64_t d, uint16_t* dx, float* dgamma, void* workspace,
+                     size_t ws_bytes, hipStream_t stream) {
+  if (h == nullptr || gamma == nullptr || rstd == nullptr || dy == nullptr || dx == nullptr || dgamma == nullptr)
+    return QLIN_E_NULL;
+  const int st = check_rows(M, d);
+  if (st != QLIN_OK) return st;
+  if (!aligned16(h) || !aligned16(gamma) || !aligned16(rstd) || !aligned16(dy) || !aligned16(dh) ||
+      !aligned16(dx) || !aligned16(dgamma))
+    return QLIN_E_ALIGN;
+  if (workspace == nullptr || ws_bytes < qlin_rmsnorm_workspace_bytes(M, d)) return QLIN_E_WORKSPACE;
+  if (!aligned16(workspace)) return QLIN_E_ALIGN;
+  RmsNormBwdArgs a{};
+  a.h = h; a.gamma = gamma; a.rstd = rstd; a.dy = dy; a.dh = dh; a.M = M; a.d = d; a.dx = dx; a.dgamma = dgamma;
+  a.partial = ws_at<float>(workspace, kCounterBytes);
+  return hip_status(hooked("k_rmsnorm_bwd", stream, [&] { return launch_rmsnorm_bwd(a, stream); }));
+}
+
+size_t qlin_w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || M > (int64_t{1} << 31) || N < 1 || N > (int64_t{1} << 31)) return 0;
+  if (K < 16 || K % 16 != 0 || K > kMaxProductK) return 0;
+  return kCounterBytes;
+}
+
+int qlin_w8a8_fwd(const int8_t* xq, const float* x_scale, int64_t M, const int8_t* wq, const float* w_scale,
+                  int64_t N, int64_t K, uint16_t* y, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  if (xq == nullptr || x_scale == nullptr || wq == nullptr || w_scale == nullptr || y == nullptr)
+    return QLIN_E_NULL;
+  const size_t need = qlin_w8a8_workspace_bytes(M, N, K);
+  if (need == 0) return QLIN_E_SHAPE;
+  if (!aligned16(xq) || !aligned16(x_scale) || !aligned16(wq) || !aligned16(w_scale) || !aligned16(y))
+    return QLIN_E_ALIGN;
+  if (workspace == nullptr || ws_bytes < need) return QLIN_E_WORKSPACE;
+  if (!aligned16(workspace)) return QLIN_E_ALIGN;
+  W8A8Args a{};
+  a.xq = xq; a.xs = x_scale; a.M = M; a.wq = wq; a.ws = w_scale; a.N = N; a.K = K; a.y = y;
+  return hip_status(hooked("k_w8a8", stream, [&] { return launch_w8a8(a, stream); }));
+}
+
+size_t qlin_bwd_q8_workspace_bytes(const qlin_qweight* w, int64_t M, int32_t r, int32_t pool) {
+  if (check_layer(w, M, r, 0.0f, pool) != QLIN_OK) return 0;
+  const BwdQ8Plan p = make_bwd_q8_plan(w, M, r, pool);
+  return p.fits ? p.total : 0;
+}
+
+int qlin_bwd_q8(const qlin_qweight* w, const int8_t* xq, const float* x_scale, int64_t M, const uint16_t* A,
+                const uint16_t* B, int32_t r, float s, int32_t pool, const uint16_t* dy, const float* u,
+                uint16_t* dx, uint16_t* dA, uint16_t* dB, void* workspace, size_t ws_bytes,
+                hipStream_t stream) {
+  int st = check_layer(w, M, r, s, pool);
+  if (st != QLIN_OK) return st;
+  if (xq == nullptr || x_scale == nullptr || A == nullptr || B == nullptr || dy == nullptr || u == nullptr ||
+      dA == nullptr || dB == nullptr)
+    return QLIN_E_NULL;
+  if (!aligned16(xq) || !aligned16(x_scale) || !aligned16(A) || !aligned16(B) || !aligned16(dy) ||
+      !aligned16(u) || !aligned16(dx) || !aligned16(dA) || !aligned16(dB))
+    return QLIN_E_ALIGN;
+  const BwdQ8Plan p = make_bwd_q8_plan(w, M, r, pool);
+  if (!p.fits) return QLIN_E_SHAPE;
+  if (workspace == nullptr || ws_bytes < p.total) return QLIN_E_WORKSPACE;
+  if (!aligned16(workspace)) return QLIN_E_ALIGN;
+
+  const int64_t N = w->d_out, K = w->d_in, G = K / pool;
+  const int fmt = fmt_of(w);
+  float* partial = ws_at<float>(workspace, p.off_partial);
+  uint32_t* counters = ws_at<uint32_t>(workspace, 0);
+  float* du = ws_at<float>(workspace, p.off_du);
+  if (p.few) {
+    AdapterFewArgs f{};
+    f.dy = dy; f.M = M; f.N = N; f.B = B; f.u = u; f.r = r; f.s = s;
+    f.du = du; f.dB = dB; f.shares = adapter_few_shares(N);
+    f.partial = partial; f.counters = counters;
+    QLIN_TRY(hooked("k_du_few", stream, [&] { return launch_du_few(f, stream); }));
+  } else {
+    uint16_t* Bt = ws_at<uint16_t>(workspace, p.off_Bt);
+    QLIN_TRY(hooked("k_transpose16", stream, [&] { return launch_transpose16(B, N, r, Bt, stream); }));
+    NtArgs n{};
+    n.X = dy; n.ldx = N; n.Y = Bt; n.ldy = N; n.C = du; n.ldc = r;
+    n.M = M; n.K = N; n.J = r; n.splits = p.nt_splits; n.alpha = s;
+    n.partial = partial; n.counters = counters;
+    QLIN_TRY(hooked("k_nt_skinny", stream, [&] { return launch_nt_skinny(n, stream); }));
+    uint16_t* zh = ws_at<uint16_t>(workspace, p.off_z);
+    uint16_t* zl = zh + M * tn2_jp(r);
+    QLIN_TRY(hooked("k_split_hl", stream, [&] { return launch_split_hl(u, M, r, r, zh, zl, stream); }));
+    Tn2Args t{};
+    t.X = dy; t.ldx = N; t.Zh = zh; t.Zl = zl; t.C = dB; t.ldc = r;
+    t.M = M; t.P = N; t.J = r; t.splits = p.tn2_splits; t.out_transposed = 0; t.alpha = s;
+    t.partial = partial; t.counters = counters;
+    QLIN_TRY(hooked("k_tn2", stream, [&] { return launch_tn2(t, stream); }));
+  }
+  DaQ8Args d{};
+  d.xq = xq; d.xs = x_scale; d.du = du; d.M = M; d.K = K; d.r = r; d.pool = pool; d.dA = dA;
+  QLIN_TRY(hooked("k_da_q8", stream, [&] { return launch_da_q8(d, stream); }));
+  if (dx == nullptr) return QLIN_OK;
+
+  WeightView v;
+  st = layer_view(w, ws_at<uint8_t>(workspace, p.off_tc), stream, &v);
+  if (st != QLIN_OK) return st;
+  const int pool_shift = __builtin_ctz(static_cast<unsigned>(pool));
+  if (p.few) {
+    DxStreamArgs a{};
+    a.w = v; a.dy = dy; a.M = M; a.A = A; a.du = du; a.r = r; a.pool_shift = pool_shift;
+    a.adapter = s != 0.0f ? 1 : 0;
+    a.dx = dx; a.x = nullptr; a.dA = nullptr;
+    a.splits = p.ds_splits; a.partial = partial; a.counters = counters;
+    return hip_status(hooked("k_gemv_dx_stream", stream, [&] { return launch_gemv_dx_stream(a, fmt, stream); }));
+  }
+  uint16_t* At = ws_at<uint16_t>(workspace, p.off_At);
+  QLIN_TRY(hooked("k_transpose16", stream, [&] { return launch_transpose16(A, r, G, At, stream); }));
+  DxArgs a{};
+  a.w = v; a.dy = dy; a.M = M; a.At = At; a.du = du; a.r = r; a.pool = pool; a.pool_shift = pool_shift; a.dx = dx;
+  return hip_status(hooked("k_dx_gemm", stream, [&] { return launch_dx_gemm(a, fmt, stream); }));
+}
+
 int qlin_profile_next_launch(const char* kernel, hipEvent_t start, hipEvent_t stop) {
   ProfileHook& h = profile_hook();
   std::lock_guard<std::mutex> g(h.m);

@@ -59,6 +59,67 @@ hipError_t launch_transcode_nf(const uint8_t* codes, const void* absmax, const f
 hipError_t launch_qa_merge(const uint16_t* zero, const uint16_t* A, const uint16_t* B, int64_t N,
                            int64_t G, int r, float s, uint16_t* out, hipStream_t stream);
 
+// ------------------------------------------------------------- 8-bit rows
+struct Q8RowsArgs {  // rows of x (bf16 or fp32) to int8 codes and one scale each
+  const void* x;
+  int64_t rows, d;
+  int8_t* codes;
+  float* scale;
+  uint16_t* values;  // bf16(codes * scale), or nullptr
+};
+hipError_t launch_quant_q8(const Q8RowsArgs& a, bool f32, hipStream_t stream);
+hipError_t launch_dequant_q8(const int8_t* codes, const float* scale, int64_t rows, int64_t d,
+                             uint16_t* out, hipStream_t stream);
+
+struct RmsNormArgs {  // h = x + res; (codes, scale) = 8-bit rows of h rstd gamma
+  const uint16_t* x;
+  const uint16_t* res;    // or nullptr
+  const uint16_t* gamma;
+  int64_t M, d;
+  float eps;
+  uint16_t* h;            // nullptr without a residual
+  int8_t* codes;
+  float* scale;
+  float* rstd;            // or nullptr
+  uint16_t* values;       // or nullptr
+};
+hipError_t launch_rmsnorm_q8(const RmsNormArgs& a, hipStream_t stream);
+
+struct RmsNormBwdArgs {
+  const uint16_t* h;
+  const uint16_t* gamma;
+  const float* rstd;
+  const uint16_t* dy;
+  const uint16_t* dh;     // or nullptr
+  int64_t M, d;
+  uint16_t* dx;
+  float* dgamma;
+  float* partial;         // rmsnorm_bwd_partial_floats(M, d)
+};
+int64_t rmsnorm_bwd_partial_floats(int64_t M, int64_t d);
+hipError_t launch_rmsnorm_bwd(const RmsNormBwdArgs& a, hipStream_t stream);
+
+struct W8A8Args {  // y[m][n] = xs[m] ws[n] sum_k xq[m][k] wq[n][k]
+  const int8_t* xq;
+  const float* xs;
+  int64_t M;
+  const int8_t* wq;
+  const float* ws;
+  int64_t N, K;           // K % 16 == 0, K <= 131056
+  uint16_t* y;            // [M][N]
+};
+hipError_t launch_w8a8(const W8A8Args& a, hipStream_t stream);
+
+struct DaQ8Args {  // dA[j][g] = sum_m du[m][j] xs[m] sum_{k in g} xq[m][k], g of 1 or 32 columns
+  const int8_t* xq;       // [M][K], K % 64 == 0
+  const float* xs;
+  const float* du;        // [M][r]
+  int64_t M, K;
+  int32_t r, pool;        // pool 1 or 32
+  uint16_t* dA;           // [r][K / pool]
+};
+hipError_t launch_da_q8(const DaQ8Args& a, hipStream_t stream);
+
 // ------------------------------------------------------------ adapter ops
 struct NtArgs {  // C[m][j] = alpha * sum_k X[m][k] Y[j][k]
   const uint16_t* X;  int64_t ldx;
