@@ -3,6 +3,8 @@
 
 #include "device_common.hpp"
 
+#include <type_traits>
+
 namespace qlin {
 
 // Running maximum of |v| that keeps a NaN once it has met one (fmaxf drops
@@ -55,6 +57,92 @@ __device__ __forceinline__ float q8_scale(float mx) {
 __device__ __forceinline__ int q8_code_exact(float v, float mx) {
   if (!finite_f32(mx) || mx == 0.0f) return 0;
   return static_cast<int>(rint(127.0 * static_cast<double>(v) / static_cast<double>(mx)));
+}
+
+// ------------------------------------------------------ rows in registers
+// A row of at least eight elements is spread over T threads in vectors of
+// eight: thread t holds vectors t, t + T, ...  Rows of any width and
+// alignment go through the same branch-free 16-byte accesses (this target
+// allows them at any address): a vector that would pass the row's end is
+// moved back onto its last eight elements, so some of its elements are held
+// twice, with the same values; they are stored twice alike and left out of
+// sums (Vec::dup).
+typedef u32x4 u32x4u __attribute__((aligned(2)));
+typedef u32x2 u32x2u __attribute__((aligned(1)));
+
+struct Vec {
+  int k;    // first element
+  int dup;  // elements k .. k + dup - 1 belong to an earlier vector (8: a vector past the row)
+  bool in;  // holds elements of its own
+};
+__device__ __forceinline__ Vec row_vec(int v, int d) {
+  const int k = 8 * v < d - 8 ? 8 * v : d - 8;
+  const int dup = 8 * v - k;
+  return Vec{k, dup < 8 ? dup : 8, dup < 8};
+}
+__device__ __forceinline__ u32x4 load8(const uint16_t* p) { return *reinterpret_cast<const u32x4u*>(p); }
+__device__ __forceinline__ void store8(uint16_t* p, u32x4 v) { *reinterpret_cast<u32x4u*>(p) = v; }
+__device__ __forceinline__ void store_codes8(int8_t* p, u32x2 v) { *reinterpret_cast<u32x2u*>(p) = v; }
+__device__ __forceinline__ float elem8(u32x4 v, int e) { return (e & 1) ? bf16_hi(v[e >> 1]) : bf16_lo(v[e >> 1]); }
+
+// Adding 1.5 * 2^23 rounds a value of less than 2^22 to the nearest integer
+// (ties to even) and leaves that integer, in two's complement, in the low
+// bits: the low byte is the code.
+__device__ __forceinline__ uint32_t round_bits(float p) { return __float_as_uint(p + 12582912.0f); }
+// low bytes of four words, in order
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return perm(perm(d, c, 0x0C0C0400u), perm(b, a, 0x0C0C0400u), 0x05040100u);
+}
+__device__ __forceinline__ float code_of(uint32_t word, int e) {
+  return static_cast<float>(static_cast<int8_t>(word >> (8 * e)));
+}
+
+// bf16(code * scale) of eight codes.
+__device__ __forceinline__ u32x4 values8(u32x2 c, float scale) {
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = pack_bf16x2(code_of(c[j >> 1], 2 * (j & 1)) * scale, code_of(c[j >> 1], 2 * (j & 1) + 1) * scale);
+  return o;
+}
+
+// A row's factors: y * pre * inv = 127 y / mx.  Rows below 2^-100 are first
+// scaled by 2^64 (exact), so that inv stays inside fp32's range; rows that
+// are zero or not finite have inv = 0 (codes 0, once their elements are made
+// finite by the caller).
+struct RowScale {
+  float scale, pre, inv;
+};
+__device__ __forceinline__ RowScale row_scale(float mx) {
+  RowScale r;
+  r.scale = q8_scale(mx);
+  r.pre = mx < 0x1p-100f ? 0x1p64f : 1.0f;
+  r.inv = finite_f32(mx) && mx > 0.0f ? 127.0f / (mx * r.pre) : 0.0f;
+  return r;
+}
+
+// Sizes of a row kernel's instantiations: threads per row, vectors a thread.
+// One wave per row up to 1024 columns (several rows share a workgroup and
+// nothing needs a barrier), then as few waves as hold the row in two vectors
+// a thread, four beyond 16384 columns.  Rows below eight columns or past
+// kRowMax take the kernels that walk a row element by element.
+constexpr int kRowMin = 8, kRowMax = 32768;
+template <typename F>
+hipError_t by_row_width(int64_t d, F f) {
+  if (d <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  if (d <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  if (d <= 2048) return f(std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{});
+  if (d <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  if (d <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  if (d <= 16384) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+}
+// Rows that share a workgroup: only rows of one wave, which need no barrier.
+constexpr int rows_per_group(int threads) { return threads == 64 ? 4 : 1; }
+// Workgroups for `rows` rows, `per` of them each; a longer queue is walked.
+inline uint32_t row_grid(int64_t rows, int per) {
+  const int64_t n = (rows + per - 1) / per;
+  return static_cast<uint32_t>(n < (1 << 20) ? n : (1 << 20));
 }
 
 }  // namespace qlin
