@@ -38,7 +38,10 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(device) -> int:
     torch = _torch()
-    return torch.cuda.current_stream(device).cuda_stream
+    try:
+        return torch._C._cuda_getCurrentRawStream(device.index)  # 1.8 us less than the stream object
+    except AttributeError:
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _need(t, dtype, shape, name):
@@ -405,7 +408,7 @@ def qlin_rmsnorm_q8(x, gamma, eps: float, residual=None, want_values: bool = Fal
     if residual is not None:
         _need(residual, torch.bfloat16, (M, d), "residual")
         if h is None:
-            h = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
+            h = torch.empty_like(x)
         else:
             _need(h, torch.bfloat16, (M, d), "h")
     if codes is None:
@@ -423,7 +426,7 @@ def qlin_rmsnorm_q8(x, gamma, eps: float, residual=None, want_values: bool = Fal
     if values is not None:
         _need(values, torch.bfloat16, (M, d), "values")
     elif want_values:
-        values = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
+        values = torch.empty_like(x)
     check(lib().qlin_rmsnorm_q8(x.data_ptr(), _ptr(residual), gamma.data_ptr(), M, d, float(eps), _ptr(h),
                                 codes.data_ptr(), scale.data_ptr(), rstd.data_ptr(), _ptr(values),
                                 _stream(dev)), "qlin_rmsnorm_q8")
@@ -443,7 +446,7 @@ def qlin_rmsnorm_bwd(h, gamma, rstd, dy, dh=None, dx=None, dgamma=None, ws=None)
     if dh is not None:
         _need(dh, torch.bfloat16, (M, d), "dh")
     if dx is None:
-        dx = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
+        dx = torch.empty_like(h)
     else:
         _need(dx, torch.bfloat16, (M, d), "dx")
     if dgamma is None:

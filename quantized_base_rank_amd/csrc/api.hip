@@ -975,10 +975,34 @@ int qlin_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd
   return hip_status(hooked("k_rmsnorm_bwd", stream, [&] { return launch_rmsnorm_bwd(a, stream); }));
 }
 
+namespace {
+
+constexpr int64_t kFewProductM = 64;  // weight-streaming product up to this many tokens
+
+struct ProductPlan {
+  bool few = false, fits = true;
+  int splits = 1;
+  int64_t words = 0;  // int32 sums of the shares
+};
+
+ProductPlan make_product_plan(int64_t M, int64_t N, int64_t K) {
+  ProductPlan p;
+  p.few = M <= kFewProductM;
+  if (p.few) {
+    p.splits = w8a8_few_splits(N, K);
+    p.words = w8a8_few_partial_words(M, N, K);
+    p.fits = p.splits == 1 || w8a8_few_tiles(N) <= kCounterWords;
+  }
+  return p;
+}
+
+}  // namespace
+
 size_t qlin_w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || M > (int64_t{1} << 31) || N < 1 || N > (int64_t{1} << 31)) return 0;
   if (K < 16 || K % 16 != 0 || K > kMaxProductK) return 0;
-  return kCounterBytes;
+  const ProductPlan p = make_product_plan(M, N, K);
+  return p.fits ? kCounterBytes + align256(static_cast<size_t>(p.words) * sizeof(int32_t)) : 0;
 }
 
 int qlin_w8a8_fwd(const int8_t* xq, const float* x_scale, int64_t M, const int8_t* wq, const float* w_scale,
@@ -991,9 +1015,14 @@ int qlin_w8a8_fwd(const int8_t* xq, const float* x_scale, int64_t M, const int8_
     return QLIN_E_ALIGN;
   if (workspace == nullptr || ws_bytes < need) return QLIN_E_WORKSPACE;
   if (!aligned16(workspace)) return QLIN_E_ALIGN;
+  const ProductPlan p = make_product_plan(M, N, K);
   W8A8Args a{};
   a.xq = xq; a.xs = x_scale; a.M = M; a.wq = wq; a.ws = w_scale; a.N = N; a.K = K; a.y = y;
-  return hip_status(hooked("k_w8a8", stream, [&] { return launch_w8a8(a, stream); }));
+  a.splits = p.splits;
+  a.partial = ws_at<int32_t>(workspace, kCounterBytes);
+  a.counters = ws_at<uint32_t>(workspace, 0);
+  if (p.few) return hip_status(hooked("k_w8a8_few", stream, [&] { return launch_w8a8_few(a, stream); }));
+  return hip_status(hooked("k_w8a8_gemm", stream, [&] { return launch_w8a8_gemm(a, stream); }));
 }
 
 size_t qlin_bwd_q8_workspace_bytes(const qlin_qweight* w, int64_t M, int32_t r, int32_t pool) {

@@ -107,8 +107,16 @@ struct W8A8Args {  // y[m][n] = xs[m] ws[n] sum_k xq[m][k] wq[n][k]
   const float* ws;
   int64_t N, K;           // K % 16 == 0, K <= 131056
   uint16_t* y;            // [M][N]
+  int32_t splits;         // shares of K
+  int32_t* partial;       // int32 sums of the shares
+  uint32_t* counters;     // one per tile
 };
-hipError_t launch_w8a8(const W8A8Args& a, hipStream_t stream);
+hipError_t launch_w8a8_gemm(const W8A8Args& a, hipStream_t stream);  // any M
+int w8a8_gemm_tiles(int64_t M, int64_t N);
+hipError_t launch_w8a8_few(const W8A8Args& a, hipStream_t stream);   // M <= 64
+int w8a8_few_tiles(int64_t N);
+int w8a8_few_splits(int64_t N, int64_t K);
+int64_t w8a8_few_partial_words(int64_t M, int64_t N, int64_t K);
 
 struct DaQ8Args {  // dA[j][g] = sum_m du[m][j] xs[m] sum_{k in g} xq[m][k], g of 1 or 32 columns
   const int8_t* xq;       // [M][K], K % 64 == 0
