@@ -991,7 +991,7 @@ ProductPlan make_product_plan(int64_t M, int64_t N, int64_t K) {
   if (p.few) {
     p.splits = w8a8_few_splits(N, K);
     p.words = w8a8_few_partial_words(M, N, K);
-    p.fits = p.splits == 1 || w8a8_few_tiles(N) <= kCounterWords;
+    p.fits = p.splits == 1 || w8a8_few_tiles(N, K) <= kCounterWords;
   }
   return p;
 }

@@ -114,7 +114,7 @@ struct W8A8Args {  // y[m][n] = xs[m] ws[n] sum_k xq[m][k] wq[n][k]
 hipError_t launch_w8a8_gemm(const W8A8Args& a, hipStream_t stream);  // any M
 int w8a8_gemm_tiles(int64_t M, int64_t N);
 hipError_t launch_w8a8_few(const W8A8Args& a, hipStream_t stream);   // M <= 64
-int w8a8_few_tiles(int64_t N);
+int w8a8_few_tiles(int64_t N, int64_t K);
 int w8a8_few_splits(int64_t N, int64_t K);
 int64_t w8a8_few_partial_words(int64_t M, int64_t N, int64_t K);
 

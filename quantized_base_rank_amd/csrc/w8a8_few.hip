@@ -2,14 +2,16 @@
 // HBM straight into the operands of the 8-bit matrix instructions.
 //   y[m][n] = xs[m] ws[n] sum_k xq[m][k] wq[n][k],  exact in int32
 //
-// A workgroup of 8 waves owns 16 RT channels and a share of K; its waves
-// divide the share's 64-byte slices, each walking a contiguous run with the
-// loads of the next kAhead slices in flight in a register ring.  Per slice a
-// wave loads RT weight operands (lane (r, g): 16 bytes from 16 g of row r,
-// so 64 bytes of each of 16 rows) and MT token operands, which come from the
-// cache.  The waves' int32 sums meet in LDS (integer addition: any order
-// gives the same sum); shares of K publish theirs and the last workgroup of a
-// tile (atomic ticket) adds them.
+// A workgroup of 8 waves owns 16 RT channels and a share of K, walked in
+// chunks of kChunk bytes.  The chunk of all token rows is copied to LDS (two
+// buffers, direct-to-LDS loads one chunk ahead): read from cache by every
+// wave, the token operands cost as many load instructions as the weights (16
+// tokens by 8192 x 28672: 59 us, against 46 through LDS).  Each wave takes a
+// contiguous eighth of the chunk for all rows, in 64-byte slices: a weight
+// operand is 16 bytes from 16 g of row r for lane (r, g), loaded two chunks
+// ahead into a register ring.  The waves' int32 sums meet in LDS (integer
+// addition: any order gives the same sum); shares of K publish theirs and the
+// last workgroup of a tile (atomic ticket) adds them.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "q8_common.hpp"
@@ -22,11 +24,19 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFewWaves = 8;
 constexpr int kSlice = 64;  // bytes of K per matrix instruction
-constexpr int kAhead = 6;   // slices in flight per wave
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// Bytes of K per chunk: 32 or 64 KB of LDS per buffer.
+constexpr int few_chunk(int mt) { return mt <= 2 ? 2048 : 1024; }
 
 template <int RT, int MT>
 __global__ __launch_bounds__(64 * kFewWaves, 2) void k_w8a8_few(W8A8Args a) {
-  constexpr int kRows = 16 * RT, kTok = 16 * MT;
+  constexpr int kRows = 16 * RT, kTok = 16 * MT, kChunk = few_chunk(MT);
+  constexpr int kSl = kChunk / kSlice / kFewWaves;         // slices per wave and chunk
+  constexpr int kDma = kTok * kChunk / 1024 / kFewWaves;   // token loads per wave and chunk
+  // one array per buffer: a read of one is not held for loads into the other
+  __shared__ __attribute__((aligned(16))) uint8_t s_x0[kTok * kChunk];
+  __shared__ __attribute__((aligned(16))) uint8_t s_x1[kTok * kChunk];
   __shared__ int32_t s_sum[kTok][kRows + 4];
   __shared__ uint32_t s_ticket;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -34,61 +44,90 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void k_w8a8_few(W8A8Args a) {
   const int l16 = lane & 15, g = lane >> 4;
   const int S = a.splits;
   const int tile = static_cast<int>(blockIdx.x) / S, share = static_cast<int>(blockIdx.x) % S;
-  const int64_t M = a.M, N = a.N, K = a.K, n0 = static_cast<int64_t>(tile) * kRows;
-  const int slices = static_cast<int>((K + kSlice - 1) / kSlice);
-  // the slices of this wave
-  const int per = (slices + S * kFewWaves - 1) / (S * kFewWaves);
-  const int b0 = (share * kFewWaves + wave) * per;
-  const int s_begin = b0 < slices ? b0 : slices, s_end = b0 + per < slices ? b0 + per : slices;
+  const int64_t M = a.M, N = a.N, n0 = static_cast<int64_t>(tile) * kRows;
+  const int K = static_cast<int>(a.K);
+  const int chunks = (K + kChunk - 1) / kChunk, per = (chunks + S - 1) / S;
+  const int c_begin = share * per < chunks ? share * per : chunks;
+  const int c_end = c_begin + per < chunks ? c_begin + per : chunks;
 
-  for (int i = tid; i < kTok * (kRows + 4); i += 64 * kFewWaves) (&s_sum[0][0])[i] = 0;
-
-  // Rows past the matrix lie outside the resource (zeros).  A weight piece
-  // past K holds the next row's codes, against a token piece that is zero.
+  // Rows past the matrices lie outside the resources (zeros), and whole
+  // slices past K too.  A weight piece past K holds the next row's codes,
+  // against a token piece that is zero.
   const int64_t rows = N - n0 < kRows ? N - n0 : kRows;
   const rsrc_t wr = uniform_rsrc(a.wq + n0 * K, static_cast<uint32_t>(rows * K));
   const rsrc_t xr = uniform_rsrc(a.xq, static_cast<uint32_t>(M * K));
-  uint32_t wo[RT], xo[MT], xo_tail[MT];
+  uint32_t wo[RT];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) wo[t] = static_cast<uint32_t>((16 * t + l16) * K + 16 * g);
-  const bool past = (slices - 1) * kSlice + 16 * g >= K;
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int64_t m = 16 * t + l16 < M ? 16 * t + l16 : M - 1;
-    xo[t] = static_cast<uint32_t>(m * K + 16 * g);
-    xo_tail[t] = xo[t] | (past ? 0x80000000u : 0u);
-  }
+  for (int t = 0; t < RT; ++t) wo[t] = static_cast<uint32_t>((16 * t + l16) * K + 16 * g + wave * kSl * kSlice);
 
-  i32x4 wv[kAhead][RT], xv[kAhead][MT], acc[RT][MT];
+  // Token rows of a chunk: [token][kChunk / 16 pieces], piece p at
+  // p ^ (token % 16), so that 16 tokens' reads of one piece take 16 distinct
+  // bank groups.  Load i of wave w fills 1 KB: part (8 i + w) % (kChunk / 1024)
+  // of token (8 i + w) / (kChunk / 1024).
+  auto load_tokens = [&](int c, uint8_t* buf) {
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) {
+      const int ii = i * kFewWaves + wave;
+      const int tok = ii / (kChunk / 1024), part = ii % (kChunk / 1024);
+      const int k = c * kChunk + part * 1024 + ((lane ^ (tok & 15)) << 4);
+      const uint32_t vo = c < c_end && k < K ? static_cast<uint32_t>(tok * K + k) : 0x80000000u;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_ptr_t)(buf + ii * 1024), 16, vo, 0, 0, 0);
+    }
+  };
+  i32x4 wv[2][kSl][RT], acc[RT][MT];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[r][m] = i32x4{};
-  auto load = [&](int sl, i32x4 (&w)[RT], i32x4 (&x)[MT]) {
-    // (a slice past the run lies outside the resources)
-    const int so = sl < s_end ? sl * kSlice : 0x7FFFFFFF;
-    const bool last = sl == slices - 1;
+  auto load_weights = [&](int c, int i, i32x4 (&w)[RT]) {
+    const int k = c * kChunk + i * kSlice;
+    const int so = c < c_end && k + wave * kSl * kSlice < K ? k : 0x7FFFFFFF;
 #pragma unroll
     for (int t = 0; t < RT; ++t)
       w[t] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[t], so, 0));
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-      x[t] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, last ? xo_tail[t] : xo[t], so, 0));
   };
+  load_tokens(c_begin, s_x0);
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(s_begin + i, wv[i], xv[i]);
-  for (int sl = s_begin; sl < s_end; sl += kAhead) {
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kSl; ++i) load_weights(c_begin + c, i, wv[c][i]);
+  for (int i = tid; i < kTok * (kRows + 4); i += 64 * kFewWaves) (&s_sum[0][0])[i] = 0;
+
+  // Chunk c: its token rows and this wave's weights have landed once at most
+  // the weights of chunk c + 1 are in flight; past the barrier the other
+  // buffer is free for the token rows of chunk c + 1.
+  for (int c0 = c_begin; c0 < c_end; c0 += 2) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+    for (int p = 0; p < 2; ++p) {
+      const int c = c0 + p;
+      uint8_t* const cur = p == 0 ? s_x0 : s_x1;
+      uint8_t* const nxt = p == 0 ? s_x1 : s_x0;
+      static_assert(kSl * RT <= 16, "the waits below");
+      if constexpr (kSl * RT == 2) __asm__ volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      else if constexpr (kSl * RT == 4) __asm__ volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      else if constexpr (kSl * RT == 8) __asm__ volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      else __asm__ volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      static_assert(kSl * RT == 2 || kSl * RT == 4 || kSl * RT == 8 || kSl * RT == 16, "a wait for each");
+      load_tokens(c + 1, nxt);
+#pragma unroll
+      for (int i = 0; i < kSl; ++i) {
+        i32x4 xv[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          acc[r][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[i][r], xv[i][m], acc[r][m], 0, 0, 0);
-      load(sl + kAhead + i, wv[i], xv[i]);
-      __builtin_amdgcn_sched_barrier(0);
+          xv[m] = *reinterpret_cast<const i32x4*>(cur + (16 * m + l16) * kChunk +
+                                                  ((((wave * kSl + i) * 4 + g) ^ l16) << 4));
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            acc[r][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[p][i][r], xv[m], acc[r][m], 0, 0, 0);
+        load_weights(c + 2, i, wv[p][i]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
+  // (the loads issued past the share land before the workgroup ends)
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // lane (l16, g) holds channel 16 r + 4 g + v of token 16 m + l16
   __syncthreads();
@@ -119,36 +158,63 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void k_w8a8_few(W8A8Args a) {
   }
 }
 
-// 32 channels per workgroup where that leaves at least one per compute unit.
-int few_rt(int64_t N) { return (N + 31) / 32 >= 256 ? 2 : 1; }
+// Share of the compute units' time that `groups` workgroups fill, in whole
+// rounds of one per unit.
+double few_fill(int64_t groups) { return static_cast<double>(groups) / (256.0 * static_cast<double>((groups + 255) / 256)); }
+
+// 16-row tiles per workgroup.  More rows use each token operand more often
+// but leave fewer workgroups.  Four where K has four chunks for each of the
+// shares that fill the card (16 tokens by 8192 x 28672: 50 us, against 54 and
+// 56 with two and one), else two where that fills the rounds about as well as
+// one does (32003 x 4096: 31 against 35; 11008 x 4096, 344 groups: 16 against
+// 14).
+int few_rt(int64_t N, int64_t K) {
+  const int64_t t4 = (N + 63) / 64, shares = t4 < 256 ? 256 / t4 : 1;
+  if (K >= shares * 4 * 2048 && t4 * shares >= 128) return 4;
+  const int64_t t2 = (N + 31) / 32, t1 = (N + 15) / 16;
+  return t2 >= 256 && few_fill(t2) > few_fill(t1) - 0.1 ? 2 : 1;
+}
 int few_mt(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 
 }  // namespace
 
-int w8a8_few_tiles(int64_t N) { return static_cast<int>((N + 16 * few_rt(N) - 1) / (16 * few_rt(N))); }
-// Shares of K: about one workgroup per compute unit, each wave at least two
-// slices.
+int w8a8_few_tiles(int64_t N, int64_t K) {
+  return static_cast<int>((N + 16 * few_rt(N, K) - 1) / (16 * few_rt(N, K)));
+}
+// Shares of K: about one workgroup per compute unit, each a chunk or
+// more.
 int w8a8_few_splits(int64_t N, int64_t K) {
-  const int64_t tiles = w8a8_few_tiles(N), slices = (K + kSlice - 1) / kSlice;
+  const int64_t tiles = w8a8_few_tiles(N, K), chunks = (K + 2047) / 2048;
   int64_t s = 256 / tiles;
-  if (s > slices / (2 * kFewWaves)) s = slices / (2 * kFewWaves);
+  if (s > chunks) s = chunks;
   return static_cast<int>(s < 1 ? 1 : s);
 }
 int64_t w8a8_few_partial_words(int64_t M, int64_t N, int64_t K) {
   const int64_t s = w8a8_few_splits(N, K);
-  return s > 1 ? s * w8a8_few_tiles(N) * 16 * few_rt(N) * 16 * few_mt(M) : 0;
+  return s > 1 ? s * w8a8_few_tiles(N, K) * 16 * few_rt(N, K) * 16 * few_mt(M) : 0;
 }
 
-hipError_t launch_w8a8_few(const W8A8Args& a, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(w8a8_few_tiles(a.N) * a.splits)), block(64 * kFewWaves);
-  const int rt = few_rt(a.N), mt = few_mt(a.M);
-  if (rt == 2 && mt == 1) hipLaunchKernelGGL((k_w8a8_few<2, 1>), grid, block, 0, stream, a);
-  else if (rt == 2 && mt == 2) hipLaunchKernelGGL((k_w8a8_few<2, 2>), grid, block, 0, stream, a);
-  else if (rt == 2) hipLaunchKernelGGL((k_w8a8_few<2, 4>), grid, block, 0, stream, a);
-  else if (mt == 1) hipLaunchKernelGGL((k_w8a8_few<1, 1>), grid, block, 0, stream, a);
-  else if (mt == 2) hipLaunchKernelGGL((k_w8a8_few<1, 2>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((k_w8a8_few<1, 4>), grid, block, 0, stream, a);
+namespace {
+
+template <int RT>
+hipError_t launch_few_rt(const W8A8Args& a, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(w8a8_few_tiles(a.N, a.K) * a.splits)), block(64 * kFewWaves);
+  switch (few_mt(a.M)) {
+    case 1: hipLaunchKernelGGL((k_w8a8_few<RT, 1>), grid, block, 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((k_w8a8_few<RT, 2>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_w8a8_few<RT, 4>), grid, block, 0, stream, a); break;
+  }
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_w8a8_few(const W8A8Args& a, hipStream_t stream) {
+  switch (few_rt(a.N, a.K)) {
+    case 1: return launch_few_rt<1>(a, stream);
+    case 2: return launch_few_rt<2>(a, stream);
+    default: return launch_few_rt<4>(a, stream);
+  }
 }
 
 }  // namespace qlin
