@@ -877,8 +877,8 @@ int check_rows(int64_t rows, int64_t d) {
 struct BwdQ8Plan {
   bool few = false;  // <= 16 tokens: du and dB in one launch, dX streamed
   bool fits = true;
-  int nt_splits = 1, tn2_splits = 1, ds_splits = 1;
-  size_t off_du = 0, off_Bt = 0, off_At = 0, off_z = 0, off_partial = 0, off_tc = 0, total = 0;
+  int nt_splits = 1, tn2_splits = 1, ds_splits = 1, da_splits = 1;
+  size_t off_du = 0, off_Bt = 0, off_At = 0, off_z = 0, off_dz = 0, off_partial = 0, off_tc = 0, total = 0;
 };
 
 BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t pool) {
@@ -897,12 +897,16 @@ BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t 
     counters = std::max<int64_t>(p.nt_splits > 1 ? nt_tiles(M) : 0, p.tn2_splits > 1 ? tn2_tiles(N) : 0);
     partial = std::max<int64_t>(nt_partial_floats(M, p.nt_splits), tn2_partial_floats(N, r, p.tn2_splits));
   }
+  p.da_splits = da_q8_splits(M, K, r);
+  if (p.da_splits > 1) counters = std::max<int64_t>(counters, da_q8_strips(K, r));
+  partial = std::max<int64_t>(partial, da_q8_partial_floats(M, K, r));
   p.fits = counters <= kCounterWords;
   size_t off = kCounterBytes;
   p.off_du = off;      off = align256(off + static_cast<size_t>(M) * r * sizeof(float));
   p.off_Bt = off;      off = align256(off + (p.few ? 0 : static_cast<size_t>(N) * r * sizeof(uint16_t)));
   p.off_At = off;      off = align256(off + (p.few ? 0 : static_cast<size_t>(G) * r * sizeof(uint16_t)));
   p.off_z = off;       off = align256(off + (p.few ? 0 : 2 * static_cast<size_t>(M) * tn2_jp(r) * sizeof(uint16_t)));
+  p.off_dz = off;      off = align256(off + static_cast<size_t>(da_q8_z_bytes(M, r)));
   p.off_partial = off; off = align256(off + static_cast<size_t>(partial) * sizeof(float));
   p.off_tc = off;      off += transcode_bytes(w);
   p.total = off;
@@ -1078,6 +1082,7 @@ int qlin_bwd_q8(const qlin_qweight* w, const int8_t* xq, const float* x_scale, i
   }
   DaQ8Args d{};
   d.xq = xq; d.xs = x_scale; d.du = du; d.M = M; d.K = K; d.r = r; d.pool = pool; d.dA = dA;
+  d.splits = p.da_splits; d.partial = partial; d.counters = counters; d.z = ws_at<u32x4>(workspace, p.off_dz);
   QLIN_TRY(hooked("k_da_q8", stream, [&] { return launch_da_q8(d, stream); }));
   if (dx == nullptr) return QLIN_OK;
 

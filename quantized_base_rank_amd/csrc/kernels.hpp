@@ -125,7 +125,15 @@ struct DaQ8Args {  // dA[j][g] = sum_m du[m][j] xs[m] sum_{k in g} xq[m][k], g o
   int64_t M, K;
   int32_t r, pool;        // pool 1 or 32
   uint16_t* dA;           // [r][K / pool]
+  int32_t splits;         // da_q8_splits(M, K, r)
+  float* partial;         // da_q8_partial_floats(M, K, r)
+  uint32_t* counters;     // da_q8_strips(K, r)
+  const u32x4* z;         // da_q8_z_bytes(M, r): scratch for z's planes
 };
+int da_q8_strips(int64_t K, int r);
+int da_q8_splits(int64_t M, int64_t K, int r);
+int64_t da_q8_partial_floats(int64_t M, int64_t K, int r);
+int64_t da_q8_z_bytes(int64_t M, int r);
 hipError_t launch_da_q8(const DaQ8Args& a, hipStream_t stream);
 
 // ------------------------------------------------------------ adapter ops
