@@ -95,6 +95,7 @@ struct RmsNormBwdArgs {
   uint16_t* dx;
   float* dgamma;
   float* partial;         // rmsnorm_bwd_partial_floats(M, d)
+  int64_t per;            // rows per share of dgamma (set by the launcher)
 };
 int64_t rmsnorm_bwd_partial_floats(int64_t M, int64_t d);
 hipError_t launch_rmsnorm_bwd(const RmsNormBwdArgs& a, hipStream_t stream);

@@ -123,7 +123,105 @@ __global__ __launch_bounds__(256) void k_rmsnorm_q8_wide(RmsNormArgs a) {
   }
 }
 
-__global__ __launch_bounds__(256) void k_rmsnorm_dx(RmsNormBwdArgs a) {
+// Gradient, one pass over h, dy (and dh): a workgroup walks a run of rows, one
+// at a time, with the next row's loads in flight during this row's sum, and
+// keeps its share of dgamma in registers (each thread's columns are the same
+// in every row).  Shares of dgamma go to the workspace; k_rmsnorm_dgamma adds
+// them in order.  HBM-bound: 8 bytes per element with dh.
+template <int T, int NV, bool DH>
+__global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_bwd(RmsNormBwdArgs a) {
+  constexpr int kRows = rows_per_group(T);
+  __shared__ float s_red[2][T / 64];
+  const int t = threadIdx.x % T, sub = threadIdx.x / T, d = static_cast<int>(a.d);
+  const int64_t share = static_cast<int64_t>(blockIdx.x) * kRows + sub;
+  const int64_t m0 = share * a.per, m1 = m0 + a.per < a.M ? m0 + a.per : a.M;
+  u32x4 gv[NV];
+  float dg[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    gv[i] = load8(a.gamma + row_vec(t + T * i, d).k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg[i][e] = 0.0f;
+  }
+  // (1024 threads leave 128 registers each: no room for the next row)
+  constexpr int kAhead = T < 1024 ? 1 : 0;
+  u32x4 hv[1 + kAhead][NV], yv[1 + kAhead][NV], ev[1 + kAhead][NV];
+  float rs[1 + kAhead];
+  auto load = [&](int64_t m, int p) {
+    const int64_t row = (m < m1 ? m : a.M - 1) * a.d;  // (past the run: any row, unused)
+    rs[p] = a.rstd[m < m1 ? m : a.M - 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = row_vec(t + T * i, d).k;
+      hv[p][i] = load8(a.h + row + k);
+      yv[p][i] = load8(a.dy + row + k);
+      if (DH) ev[p][i] = load8(a.dh + row + k);
+    }
+  };
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  if (kAhead != 0) load(m0, 0);
+  for (int64_t mm = m0; mm < m1; mm += 2) {
+#pragma unroll
+    for (int turn = 0; turn < 2; ++turn) {
+      const int p = kAhead != 0 ? turn : 0;
+      const int64_t m = mm + turn;
+      if (m >= m1) break;
+      load(m + kAhead, kAhead != 0 ? 1 - p : 0);
+      const float rstd = rs[p];
+      float c = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int dup = row_vec(t + T * i, d).dup;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float xh = elem8(hv[p][i], e) * rstd, dy = elem8(yv[p][i], e);
+          dg[i][e] = __builtin_fmaf(dy, xh, dg[i][e]);
+          c = __builtin_fmaf(e >= dup ? dy * elem8(gv[i], e) : 0.0f, xh, c);
+        }
+      }
+      // (two buffers take turns, so one barrier a row)
+      c = warp_sum(c);
+      if (T > 64) {
+        if ((t & 63) == 0) s_red[turn][t >> 6] = c;
+        __syncthreads();
+        c = s_red[turn][0];
+#pragma unroll
+        for (int w = 1; w < T / 64; ++w) c += s_red[turn][w];
+      }
+      c *= inv_d;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Vec q = row_vec(t + T * i, d);
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int e = 2 * j + z;
+            const float xh = elem8(hv[p][i], e) * rstd;
+            v[z] = rstd * (elem8(yv[p][i], e) * elem8(gv[i], e) - xh * c);
+            if (DH) v[z] += elem8(ev[p][i], e);
+          }
+          o[j] = pack_bf16x2(v[0], v[1]);
+        }
+        if (q.in) store8(a.dx + m * a.d + q.k, o);
+      }
+    }
+  }
+  if (m0 >= a.M) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const Vec q = row_vec(t + T * i, d);
+    if (!q.in) continue;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a.partial[share * a.d + q.k + e] = dg[i][e];
+  }
+}
+
+// Rows too short or too wide for the kernel above: dx row by row, dgamma's
+// shares column by column.
+__global__ __launch_bounds__(256) void k_rmsnorm_dx_wide(RmsNormBwdArgs a) {
   __shared__ float s_red[4];
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     const int64_t row = m * a.d;
@@ -140,27 +238,44 @@ __global__ __launch_bounds__(256) void k_rmsnorm_dx(RmsNormBwdArgs a) {
     }
   }
 }
-
-constexpr int kDgShares = 64;
-
-// Columns' sums over a share of the tokens, then the shares' sum in order.
-__global__ __launch_bounds__(256) void k_rmsnorm_dgamma_part(RmsNormBwdArgs a) {
+__global__ __launch_bounds__(256) void k_rmsnorm_dgamma_wide(RmsNormBwdArgs a) {
   const int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (k >= a.d) return;
-  const int64_t per = (a.M + kDgShares - 1) / kDgShares;
-  const int64_t m1 = (blockIdx.y + 1) * per < a.M ? (blockIdx.y + 1) * per : a.M;
+  const int64_t m0 = blockIdx.y * a.per, m1 = m0 + a.per < a.M ? m0 + a.per : a.M;
   float t = 0.0f;
-  for (int64_t m = blockIdx.y * per; m < m1; ++m)
+  for (int64_t m = m0; m < m1; ++m)
     t += bf16_to_f32(a.dy[m * a.d + k]) * (bf16_to_f32(a.h[m * a.d + k]) * a.rstd[m]);
   a.partial[blockIdx.y * a.d + k] = t;
 }
-__global__ __launch_bounds__(256) void k_rmsnorm_dgamma_sum(RmsNormBwdArgs a) {
-  const int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (k >= a.d) return;
+
+// dgamma: 64 columns a workgroup, sixteen waves each adding every sixteenth
+// share, their sums added in wave order.
+__global__ __launch_bounds__(1024) void k_rmsnorm_dgamma(RmsNormBwdArgs a, int shares) {
+  __shared__ float s_t[16][64];
+  const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t k = static_cast<int64_t>(blockIdx.x) * 64 + c;
   float t = 0.0f;
-  for (int s = 0; s < kDgShares; ++s) t += a.partial[s * a.d + k];
+  if (k < a.d) {
+#pragma unroll 8
+    for (int s = w; s < shares; s += 16) t += a.partial[s * a.d + k];
+  }
+  s_t[w][c] = t;
+  __syncthreads();
+  if (w != 0 || k >= a.d) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) t += s_t[i][c];
   a.dgamma[k] = t;
 }
+
+// Rows per share: 256 shares (one workgroup per compute unit of 1024 threads,
+// four of 256 ...), at least two rows each so that a short batch does not
+// write more partial sums than it reads rows.
+constexpr int64_t kBwdShares = 256;
+int64_t bwd_rows(int64_t M) {
+  const int64_t per = (M + kBwdShares - 1) / kBwdShares;
+  return per < 2 ? 2 : per;
+}
+int64_t bwd_shares(int64_t M) { return (M + bwd_rows(M) - 1) / bwd_rows(M); }
 
 }  // namespace
 
@@ -180,13 +295,32 @@ hipError_t launch_rmsnorm_q8(const RmsNormArgs& a, hipStream_t stream) {
   });
 }
 
-int64_t rmsnorm_bwd_partial_floats(int64_t, int64_t d) { return kDgShares * d; }
+int64_t rmsnorm_bwd_partial_floats(int64_t M, int64_t d) { return bwd_shares(M) * d; }
 
-hipError_t launch_rmsnorm_bwd(const RmsNormBwdArgs& a, hipStream_t stream) {
-  const uint32_t cols = static_cast<uint32_t>((a.d + 255) / 256);
-  hipLaunchKernelGGL(k_rmsnorm_dx, dim3(row_grid(a.M, 1)), dim3(256), 0, stream, a);
-  hipLaunchKernelGGL(k_rmsnorm_dgamma_part, dim3(cols, kDgShares), dim3(256), 0, stream, a);
-  hipLaunchKernelGGL(k_rmsnorm_dgamma_sum, dim3(cols), dim3(256), 0, stream, a);
+hipError_t launch_rmsnorm_bwd(const RmsNormBwdArgs& args, hipStream_t stream) {
+  RmsNormBwdArgs a = args;
+  a.per = bwd_rows(a.M);
+  const int64_t shares = bwd_shares(a.M);
+  hipError_t e;
+  if (a.d < kRowMin || a.d > kRowMax) {
+    hipLaunchKernelGGL(k_rmsnorm_dx_wide, dim3(row_grid(a.M, 1)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(k_rmsnorm_dgamma_wide, dim3(static_cast<uint32_t>((a.d + 255) / 256), static_cast<uint32_t>(shares)),
+                       dim3(256), 0, stream, a);
+    e = hipGetLastError();
+  } else {
+    e = by_row_width(a.d, [&](auto t, auto nv) {
+      constexpr int T = decltype(t)::value, NV = decltype(nv)::value, R = rows_per_group(T);
+      const dim3 grid(static_cast<uint32_t>((shares + R - 1) / R)), block(T * R);
+      if (a.dh != nullptr)
+        hipLaunchKernelGGL((k_rmsnorm_bwd<T, NV, true>), grid, block, 0, stream, a);
+      else
+        hipLaunchKernelGGL((k_rmsnorm_bwd<T, NV, false>), grid, block, 0, stream, a);
+      return hipGetLastError();
+    });
+  }
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_rmsnorm_dgamma, dim3(static_cast<uint32_t>((a.d + 63) / 64)), dim3(1024), 0, stream, a,
+                     static_cast<int>(shares));
   return hipGetLastError();
 }
 

@@ -157,14 +157,14 @@ __global__ __launch_bounds__(256, 1) void k_w8a8_gemm(W8A8Args a) {
     const int64_t m = mw + 32 * j + l32;
     xs[j] = m < M ? a.xs[m] : 0.0f;
   }
+  // (channels past N read as zero)
+  const rsrc_t wsr = uniform_rsrc(a.ws + nw, static_cast<uint32_t>(nw < N ? (N - nw < 128 ? N - nw : 128) * 4 : 0));
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int c = 32 * i + 8 * q + 4 * h;
-      float ws[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) ws[v] = nw + c + v < N ? a.ws[nw + c + v] : 0.0f;
+      const f32x4 ws = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(wsr, static_cast<uint32_t>(c * 4), 0, 0));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int m = 32 * j + l32;
@@ -175,15 +175,14 @@ __global__ __launch_bounds__(256, 1) void k_w8a8_gemm(W8A8Args a) {
             u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
       }
     }
-  const bool wide = (N & 7) == 0;
   for (int it = 0; it < 32; ++it) {
     const int m = 4 * it + (lane >> 4), pc = lane & 15;
     const u32x4 v = *reinterpret_cast<const u32x4*>(out + m * 256 + ((pc ^ (m & 15)) << 4));
     const int64_t n = nw + 8 * pc;
     if (mw + m >= M || n >= N) continue;
     uint16_t* const dst = a.y + (mw + m) * N + n;
-    if (wide) {
-      *reinterpret_cast<u32x4*>(dst) = v;
+    if (n + 8 <= N) {
+      store8(dst, v);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
