@@ -445,7 +445,9 @@ int qlin_rmsnorm_bwd(const uint16_t *h, const uint16_t *gamma, const float *rstd
  * Product of 8-bit rows: y[m][n] = x_scale[m] w_scale[n] sum_k xq[m][k] wq[n][k].
  *   xq, x_scale  8-bit rows [M][K] (tokens);  1 <= M
  *   wq, w_scale  8-bit rows [N][K] (output channels);  1 <= N;  K % 16 == 0,
- *                16 <= K <= 131056 (any int8 codes then sum inside int32)
+ *                16 <= K <= 131056 (any int8 codes then sum inside int32);
+ *                QLIN_E_SHAPE for outputs of more than 2^22 of the kernels'
+ *                tiles (at the least 16 channels for M <= 64, 64 x 256 above)
  *   y            bf16[M][N] (output): the integer sum is exact; one rounding
  *                to fp32 of it, one for each scale, one to bf16
  *   workspace, ws_bytes  >= qlin_w8a8_workspace_bytes(M, N, K) (0 for invalid

@@ -981,11 +981,12 @@ int qlin_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd
 
 namespace {
 
+constexpr int64_t kMaxTiles = int64_t{1} << 22;  // a launch of 512 threads each stays below 2^32
 constexpr int64_t kFewProductM = 64;  // weight-streaming product up to this many tokens
 
 struct ProductPlan {
   bool few = false, fits = true;
-  int splits = 1;
+  int j = 4, splits = 1;
   int64_t words = 0;  // int32 sums of the shares
 };
 
@@ -995,7 +996,13 @@ ProductPlan make_product_plan(int64_t M, int64_t N, int64_t K) {
   if (p.few) {
     p.splits = w8a8_few_splits(N, K);
     p.words = w8a8_few_partial_words(M, N, K);
-    p.fits = p.splits == 1 || w8a8_few_tiles(N, K) <= kCounterWords;
+    p.fits = w8a8_few_tiles(N, K) <= (p.splits == 1 ? kMaxTiles : kCounterWords);
+  } else {
+    const W8A8Shape s = w8a8_gemm_shape(M, N, K);
+    p.j = s.j;
+    p.splits = s.splits;
+    p.words = w8a8_gemm_partial_words(M, N, s);
+    p.fits = w8a8_gemm_tiles(M, N, p.j) <= kMaxTiles;
   }
   return p;
 }
@@ -1026,7 +1033,7 @@ int qlin_w8a8_fwd(const int8_t* xq, const float* x_scale, int64_t M, const int8_
   a.partial = ws_at<int32_t>(workspace, kCounterBytes);
   a.counters = ws_at<uint32_t>(workspace, 0);
   if (p.few) return hip_status(hooked("k_w8a8_few", stream, [&] { return launch_w8a8_few(a, stream); }));
-  return hip_status(hooked("k_w8a8_gemm", stream, [&] { return launch_w8a8_gemm(a, stream); }));
+  return hip_status(hooked("k_w8a8_gemm", stream, [&] { return launch_w8a8_gemm(a, p.j, stream); }));
 }
 
 size_t qlin_bwd_q8_workspace_bytes(const qlin_qweight* w, int64_t M, int32_t r, int32_t pool) {

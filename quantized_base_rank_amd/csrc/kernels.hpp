@@ -110,12 +110,17 @@ struct W8A8Args {  // y[m][n] = xs[m] ws[n] sum_k xq[m][k] wq[n][k]
   uint16_t* y;            // [M][N]
   int32_t splits;         // shares of K
   int32_t* partial;       // int32 sums of the shares
-  uint32_t* counters;     // one per tile
+  uint32_t* counters;     // one per tile (few tokens)
 };
-hipError_t launch_w8a8_gemm(const W8A8Args& a, hipStream_t stream);  // any M
-int w8a8_gemm_tiles(int64_t M, int64_t N);
+struct W8A8Shape {        // tile of the matrix kernel: 64 j tokens; shares of K
+  int j = 4, splits = 1;
+};
+W8A8Shape w8a8_gemm_shape(int64_t M, int64_t N, int64_t K);
+int64_t w8a8_gemm_tiles(int64_t M, int64_t N, int j);
+int64_t w8a8_gemm_partial_words(int64_t M, int64_t N, W8A8Shape s);
+hipError_t launch_w8a8_gemm(const W8A8Args& a, int j, hipStream_t stream);  // any M
 hipError_t launch_w8a8_few(const W8A8Args& a, hipStream_t stream);   // M <= 64
-int w8a8_few_tiles(int64_t N, int64_t K);
+int64_t w8a8_few_tiles(int64_t N, int64_t K);
 int w8a8_few_splits(int64_t N, int64_t K);
 int64_t w8a8_few_partial_words(int64_t M, int64_t N, int64_t K);
 

@@ -178,8 +178,8 @@ int few_mt(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 
 }  // namespace
 
-int w8a8_few_tiles(int64_t N, int64_t K) {
-  return static_cast<int>((N + 16 * few_rt(N, K) - 1) / (16 * few_rt(N, K)));
+int64_t w8a8_few_tiles(int64_t N, int64_t K) {
+  return (N + 16 * few_rt(N, K) - 1) / (16 * few_rt(N, K));
 }
 // Shares of K: about one workgroup per compute unit, each a chunk or
 // more.
