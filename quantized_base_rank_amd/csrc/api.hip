@@ -877,36 +877,29 @@ int check_rows(int64_t rows, int64_t d) {
 struct BwdQ8Plan {
   bool few = false;  // <= 16 tokens: du and dB in one launch, dX streamed
   bool fits = true;
-  int nt_splits = 1, tn2_splits = 1, ds_splits = 1, da_splits = 1;
-  size_t off_du = 0, off_Bt = 0, off_At = 0, off_z = 0, off_dz = 0, off_partial = 0, off_tc = 0, total = 0;
+  int ds_splits = 1;
+  size_t off_du = 0, off_At = 0, off_partial = 0, off_tc = 0, total = 0;
 };
 
 BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t pool) {
   BwdQ8Plan p;
-  const Plan q = make_plan(w, M, r, pool);
   const int64_t N = w->d_out, K = w->d_in, G = K / pool;
   p.few = M <= kSmallM && dx_stream_fits(N, K, fmt_of(w));
-  p.nt_splits = q.nt_splits_du;
-  p.tn2_splits = q.tn2_splits_dB;
-  p.ds_splits = q.ds_splits;
-  int64_t counters, partial;
+  p.ds_splits = dx_stream_splits(N, K, fmt_of(w));
+  int64_t counters = tokens_splits(M, K, r) > 1 ? tokens_strips(K, r) : 0;
+  int64_t partial = tokens_partial_floats(M, K, r);
   if (p.few) {
-    counters = std::max<int64_t>(1, p.ds_splits > 1 ? dx_stream_panels(K) : 0);
-    partial = std::max<int64_t>(adapter_few_partial_floats(N), dx_stream_partial_floats(N, K, fmt_of(w)));
+    counters = std::max<int64_t>({counters, 1, p.ds_splits > 1 ? dx_stream_panels(K) : 0});
+    partial = std::max<int64_t>({partial, adapter_few_partial_floats(N), dx_stream_partial_floats(N, K, fmt_of(w))});
   } else {
-    counters = std::max<int64_t>(p.nt_splits > 1 ? nt_tiles(M) : 0, p.tn2_splits > 1 ? tn2_tiles(N) : 0);
-    partial = std::max<int64_t>(nt_partial_floats(M, p.nt_splits), tn2_partial_floats(N, r, p.tn2_splits));
+    counters = std::max<int64_t>({counters, tokens_splits(M, N, r) > 1 ? tokens_strips(N, r) : 0,
+                                  du_splits(M, N) > 1 ? du_tiles(M) : 0});
+    partial = std::max<int64_t>({partial, tokens_partial_floats(M, N, r), du_partial_floats(M, N, r)});
   }
-  p.da_splits = da_q8_splits(M, K, r);
-  if (p.da_splits > 1) counters = std::max<int64_t>(counters, da_q8_strips(K, r));
-  partial = std::max<int64_t>(partial, da_q8_partial_floats(M, K, r));
   p.fits = counters <= kCounterWords;
   size_t off = kCounterBytes;
   p.off_du = off;      off = align256(off + static_cast<size_t>(M) * r * sizeof(float));
-  p.off_Bt = off;      off = align256(off + (p.few ? 0 : static_cast<size_t>(N) * r * sizeof(uint16_t)));
   p.off_At = off;      off = align256(off + (p.few ? 0 : static_cast<size_t>(G) * r * sizeof(uint16_t)));
-  p.off_z = off;       off = align256(off + (p.few ? 0 : 2 * static_cast<size_t>(M) * tn2_jp(r) * sizeof(uint16_t)));
-  p.off_dz = off;      off = align256(off + static_cast<size_t>(da_q8_z_bytes(M, r)));
   p.off_partial = off; off = align256(off + static_cast<size_t>(partial) * sizeof(float));
   p.off_tc = off;      off += transcode_bytes(w);
   p.total = off;
@@ -1071,26 +1064,19 @@ int qlin_bwd_q8(const qlin_qweight* w, const int8_t* xq, const float* x_scale, i
     f.partial = partial; f.counters = counters;
     QLIN_TRY(hooked("k_du_few", stream, [&] { return launch_du_few(f, stream); }));
   } else {
-    uint16_t* Bt = ws_at<uint16_t>(workspace, p.off_Bt);
-    QLIN_TRY(hooked("k_transpose16", stream, [&] { return launch_transpose16(B, N, r, Bt, stream); }));
-    NtArgs n{};
-    n.X = dy; n.ldx = N; n.Y = Bt; n.ldy = N; n.C = du; n.ldc = r;
-    n.M = M; n.K = N; n.J = r; n.splits = p.nt_splits; n.alpha = s;
-    n.partial = partial; n.counters = counters;
-    QLIN_TRY(hooked("k_nt_skinny", stream, [&] { return launch_nt_skinny(n, stream); }));
-    uint16_t* zh = ws_at<uint16_t>(workspace, p.off_z);
-    uint16_t* zl = zh + M * tn2_jp(r);
-    QLIN_TRY(hooked("k_split_hl", stream, [&] { return launch_split_hl(u, M, r, r, zh, zl, stream); }));
-    Tn2Args t{};
-    t.X = dy; t.ldx = N; t.Zh = zh; t.Zl = zl; t.C = dB; t.ldc = r;
-    t.M = M; t.P = N; t.J = r; t.splits = p.tn2_splits; t.out_transposed = 0; t.alpha = s;
-    t.partial = partial; t.counters = counters;
-    QLIN_TRY(hooked("k_tn2", stream, [&] { return launch_tn2(t, stream); }));
+    DuArgs f{};
+    f.dy = dy; f.B = B; f.M = M; f.N = N; f.r = r; f.s = s; f.du = du;
+    f.splits = du_splits(M, N); f.partial = partial; f.counters = counters;
+    QLIN_TRY(hooked("k_du_stream", stream, [&] { return launch_du_stream(f, stream); }));
+    TokensArgs t{};
+    t.X = dy; t.Z = u; t.M = M; t.P = N; t.r = r; t.pool = 1; t.alpha = s; t.C = dB;
+    t.splits = tokens_splits(M, N, r); t.partial = partial; t.counters = counters;
+    QLIN_TRY(hooked("k_tokens", stream, [&] { return launch_tokens(t, false, stream); }));
   }
-  DaQ8Args d{};
-  d.xq = xq; d.xs = x_scale; d.du = du; d.M = M; d.K = K; d.r = r; d.pool = pool; d.dA = dA;
-  d.splits = p.da_splits; d.partial = partial; d.counters = counters; d.z = ws_at<u32x4>(workspace, p.off_dz);
-  QLIN_TRY(hooked("k_da_q8", stream, [&] { return launch_da_q8(d, stream); }));
+  TokensArgs d{};
+  d.X = xq; d.xs = x_scale; d.Z = du; d.M = M; d.P = K; d.r = r; d.pool = pool; d.alpha = 1.0f; d.C = dA;
+  d.splits = tokens_splits(M, K, r); d.partial = partial; d.counters = counters;
+  QLIN_TRY(hooked("k_tokens", stream, [&] { return launch_tokens(d, true, stream); }));
   if (dx == nullptr) return QLIN_OK;
 
   WeightView v;

@@ -124,23 +124,41 @@ int64_t w8a8_few_tiles(int64_t N, int64_t K);
 int w8a8_few_splits(int64_t N, int64_t K);
 int64_t w8a8_few_partial_words(int64_t M, int64_t N, int64_t K);
 
-struct DaQ8Args {  // dA[j][g] = sum_m du[m][j] xs[m] sum_{k in g} xq[m][k], g of 1 or 32 columns
-  const int8_t* xq;       // [M][K], K % 64 == 0
-  const float* xs;
-  const float* du;        // [M][r]
-  int64_t M, K;
-  int32_t r, pool;        // pool 1 or 32
-  uint16_t* dA;           // [r][K / pool]
-  int32_t splits;         // da_q8_splits(M, K, r)
-  float* partial;         // da_q8_partial_floats(M, K, r)
-  uint32_t* counters;     // da_q8_strips(K, r)
-  const u32x4* z;         // da_q8_z_bytes(M, r): scratch for z's planes
+// Sums over the tokens: C = alpha Z^T X, Z fp32 [M][r], X 8-bit rows with
+// scales xs (C = dA [r][P / pool], groups of `pool` columns summed) or bf16
+// rows (C = dB [P][r])
+struct TokensArgs {
+  const void* X;          // [M][P], P % 64 == 0 (codes) or P % 16 == 0 (bf16)
+  const float* xs;        // [M] (codes)
+  const float* Z;
+  int64_t M, P;
+  int32_t r, pool;        // pool 1 or 32 (codes)
+  float alpha;
+  uint16_t* C;
+  int32_t splits;         // tokens_splits(M, P, r)
+  float* partial;         // tokens_partial_floats(M, P, r)
+  uint32_t* counters;     // tokens_strips(P, r)
 };
-int da_q8_strips(int64_t K, int r);
-int da_q8_splits(int64_t M, int64_t K, int r);
-int64_t da_q8_partial_floats(int64_t M, int64_t K, int r);
-int64_t da_q8_z_bytes(int64_t M, int r);
-hipError_t launch_da_q8(const DaQ8Args& a, hipStream_t stream);
+int64_t tokens_strips(int64_t P, int r);
+int tokens_splits(int64_t M, int64_t P, int r);
+int64_t tokens_partial_floats(int64_t M, int64_t P, int r);
+hipError_t launch_tokens(const TokensArgs& a, bool q8, hipStream_t stream);
+
+struct DuArgs {  // du[m][j] = s sum_n dY[m][n] B[n][j]
+  const uint16_t* dy;     // [M][N], N % 16 == 0
+  const uint16_t* B;      // [N][r]
+  int64_t M, N;
+  int32_t r;
+  float s;
+  float* du;              // [M][r]
+  int32_t splits;         // du_splits(M, N)
+  float* partial;         // du_partial_floats(M, N, r)
+  uint32_t* counters;     // du_tiles(M)
+};
+int64_t du_tiles(int64_t M);
+int du_splits(int64_t M, int64_t N);
+int64_t du_partial_floats(int64_t M, int64_t N, int r);
+hipError_t launch_du_stream(const DuArgs& a, hipStream_t stream);
 
 // ------------------------------------------------------------ adapter ops
 struct NtArgs {  // C[m][j] = alpha * sum_k X[m][k] Y[j][k]
