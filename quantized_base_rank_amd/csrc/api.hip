@@ -875,33 +875,40 @@ int check_rows(int64_t rows, int64_t d) {
 
 // Workspace of qlin_bwd_q8, after the counter region.
 struct BwdQ8Plan {
-  bool few = false;  // <= 16 tokens: du and dB in one launch, dX streamed
+  bool dx_stream = false;  // <= 16 tokens: dX streamed
   bool fits = true;
-  int ds_splits = 1;
-  size_t off_du = 0, off_At = 0, off_partial = 0, off_tc = 0, total = 0;
+  int du_splits = 1, dB_splits = 1, dA_splits = 1, ds_splits = 1;
+  int64_t dB_counters = 0;  // dB's and dA's tickets are taken in one launch: dA's follow dB's
+  size_t off_du = 0, off_zu = 0, off_zdu = 0, off_At = 0, off_partial = 0, off_partial_dA = 0, off_tc = 0, total = 0;
 };
+
+// Tokens the products' launches and offsets are made for.
+constexpr int64_t kMaxBwdTokens = int64_t{1} << 24;
 
 BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t pool) {
   BwdQ8Plan p;
   const int64_t N = w->d_out, K = w->d_in, G = K / pool;
-  p.few = M <= kSmallM && dx_stream_fits(N, K, fmt_of(w));
-  p.ds_splits = dx_stream_splits(N, K, fmt_of(w));
-  int64_t counters = tokens_splits(M, K, r) > 1 ? tokens_strips(K, r) : 0;
-  int64_t partial = tokens_partial_floats(M, K, r);
-  if (p.few) {
-    counters = std::max<int64_t>({counters, 1, p.ds_splits > 1 ? dx_stream_panels(K) : 0});
-    partial = std::max<int64_t>({partial, adapter_few_partial_floats(N), dx_stream_partial_floats(N, K, fmt_of(w))});
-  } else {
-    counters = std::max<int64_t>({counters, tokens_splits(M, N, r) > 1 ? tokens_strips(N, r) : 0,
-                                  du_splits(M, N) > 1 ? du_tiles(M) : 0});
-    partial = std::max<int64_t>({partial, tokens_partial_floats(M, N, r), du_partial_floats(M, N, r)});
-  }
-  p.fits = counters <= kCounterWords;
+  const int fmt = fmt_of(w);
+  p.dx_stream = M <= kSmallM && dx_stream_fits(N, K, fmt);
+  p.ds_splits = dx_stream_splits(N, K, fmt);
+  p.du_splits = du_splits(M, N);
+  p.dB_splits = tokens_splits(M, N, r);
+  p.dA_splits = tokens_splits(M, K, r);
+  p.dB_counters = p.dB_splits > 1 ? tokens_strips(N) : 0;
+  const int64_t counters = std::max<int64_t>({p.dB_counters + (p.dA_splits > 1 ? tokens_strips(K) : 0),
+                                              p.du_splits > 1 ? du_tiles(M) : 0,
+                                              p.dx_stream && p.ds_splits > 1 ? dx_stream_panels(K) : 0});
+  p.fits = counters <= kCounterWords && M <= kMaxBwdTokens && 64 * N * 2 < (int64_t{1} << 31);
+  const int64_t partial = std::max<int64_t>({du_partial_floats(M, N, r), tokens_partial_floats(M, N, r),
+                                             p.dx_stream ? dx_stream_partial_floats(N, K, fmt) : 0});
   size_t off = kCounterBytes;
-  p.off_du = off;      off = align256(off + static_cast<size_t>(M) * r * sizeof(float));
-  p.off_At = off;      off = align256(off + (p.few ? 0 : static_cast<size_t>(G) * r * sizeof(uint16_t)));
-  p.off_partial = off; off = align256(off + static_cast<size_t>(partial) * sizeof(float));
-  p.off_tc = off;      off += transcode_bytes(w);
+  p.off_du = off;         off = align256(off + static_cast<size_t>(M) * r * sizeof(float));
+  p.off_zu = off;         off = align256(off + static_cast<size_t>(plane_bytes(M, r)));
+  p.off_zdu = off;        off = align256(off + static_cast<size_t>(plane_bytes(M, r)));
+  p.off_At = off;         off = align256(off + (p.dx_stream ? 0 : static_cast<size_t>(G) * r * sizeof(uint16_t)));
+  p.off_partial = off;    off = align256(off + static_cast<size_t>(partial) * sizeof(float));
+  p.off_partial_dA = off; off = align256(off + static_cast<size_t>(tokens_partial_floats(M, K, r)) * sizeof(float));
+  p.off_tc = off;         off += transcode_bytes(w);
   p.total = off;
   return p;
 }
@@ -1057,33 +1064,24 @@ int qlin_bwd_q8(const qlin_qweight* w, const int8_t* xq, const float* x_scale, i
   float* partial = ws_at<float>(workspace, p.off_partial);
   uint32_t* counters = ws_at<uint32_t>(workspace, 0);
   float* du = ws_at<float>(workspace, p.off_du);
-  if (p.few) {
-    AdapterFewArgs f{};
-    f.dy = dy; f.M = M; f.N = N; f.B = B; f.u = u; f.r = r; f.s = s;
-    f.du = du; f.dB = dB; f.shares = adapter_few_shares(N);
-    f.partial = partial; f.counters = counters;
-    QLIN_TRY(hooked("k_du_few", stream, [&] { return launch_du_few(f, stream); }));
-  } else {
-    DuArgs f{};
-    f.dy = dy; f.B = B; f.M = M; f.N = N; f.r = r; f.s = s; f.du = du;
-    f.splits = du_splits(M, N); f.partial = partial; f.counters = counters;
-    QLIN_TRY(hooked("k_du_stream", stream, [&] { return launch_du_stream(f, stream); }));
-    TokensArgs t{};
-    t.X = dy; t.Z = u; t.M = M; t.P = N; t.r = r; t.pool = 1; t.alpha = s; t.C = dB;
-    t.splits = tokens_splits(M, N, r); t.partial = partial; t.counters = counters;
-    QLIN_TRY(hooked("k_tokens", stream, [&] { return launch_tokens(t, false, stream); }));
-  }
-  TokensArgs d{};
-  d.X = xq; d.xs = x_scale; d.Z = du; d.M = M; d.P = K; d.r = r; d.pool = pool; d.alpha = 1.0f; d.C = dA;
-  d.splits = tokens_splits(M, K, r); d.partial = partial; d.counters = counters;
-  QLIN_TRY(hooked("k_tokens", stream, [&] { return launch_tokens(d, true, stream); }));
+  DuArgs f{};
+  f.dy = dy; f.B = B; f.u = u; f.xs = x_scale; f.M = M; f.N = N; f.r = r; f.s = s; f.du = du;
+  f.u_planes = ws_at<u32x4>(workspace, p.off_zu); f.du_planes = ws_at<u32x4>(workspace, p.off_zdu);
+  f.splits = p.du_splits; f.partial = partial; f.counters = counters;
+  QLIN_TRY(hooked("k_du", stream, [&] { return launch_du(f, stream); }));
+  TokensArgs tb{}, ta{};
+  tb.X = dy; tb.Z = f.u_planes; tb.M = M; tb.P = N; tb.r = r; tb.pool = 1; tb.alpha = s; tb.C = dB;
+  tb.splits = p.dB_splits; tb.partial = partial; tb.counters = counters;
+  ta.X = xq; ta.Z = f.du_planes; ta.M = M; ta.P = K; ta.r = r; ta.pool = pool; ta.alpha = 1.0f; ta.C = dA;
+  ta.splits = p.dA_splits; ta.partial = ws_at<float>(workspace, p.off_partial_dA); ta.counters = counters + p.dB_counters;
+  QLIN_TRY(hooked("k_tokens", stream, [&] { return launch_tokens(tb, ta, stream); }));
   if (dx == nullptr) return QLIN_OK;
 
   WeightView v;
   st = layer_view(w, ws_at<uint8_t>(workspace, p.off_tc), stream, &v);
   if (st != QLIN_OK) return st;
   const int pool_shift = __builtin_ctz(static_cast<unsigned>(pool));
-  if (p.few) {
+  if (p.dx_stream) {
     DxStreamArgs a{};
     a.w = v; a.dy = dy; a.M = M; a.A = A; a.du = du; a.r = r; a.pool_shift = pool_shift;
     a.adapter = s != 0.0f ? 1 : 0;

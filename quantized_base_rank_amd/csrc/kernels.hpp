@@ -124,41 +124,47 @@ int64_t w8a8_few_tiles(int64_t N, int64_t K);
 int w8a8_few_splits(int64_t N, int64_t K);
 int64_t w8a8_few_partial_words(int64_t M, int64_t N, int64_t K);
 
-// Sums over the tokens: C = alpha Z^T X, Z fp32 [M][r], X 8-bit rows with
-// scales xs (C = dA [r][P / pool], groups of `pool` columns summed) or bf16
-// rows (C = dB [P][r])
+// Sums over the tokens: C = alpha Z^T X, Z [M][r] as bf16 hi/lo planes in
+// operand order (plane_bytes(M, r)); X bf16 rows (C = dB [P][r]) or codes
+// (C = dA [r][P / pool], groups of `pool` columns summed)
 struct TokensArgs {
   const void* X;          // [M][P], P % 64 == 0 (codes) or P % 16 == 0 (bf16)
-  const float* xs;        // [M] (codes)
-  const float* Z;
+  const u32x4* Z;
   int64_t M, P;
   int32_t r, pool;        // pool 1 or 32 (codes)
   float alpha;
   uint16_t* C;
   int32_t splits;         // tokens_splits(M, P, r)
+  int32_t blocks;         // (set by the launcher)
   float* partial;         // tokens_partial_floats(M, P, r)
-  uint32_t* counters;     // tokens_strips(P, r)
+  uint32_t* counters;     // tokens_strips(P)
 };
-int64_t tokens_strips(int64_t P, int r);
+int64_t tokens_strips(int64_t P);
 int tokens_splits(int64_t M, int64_t P, int r);
 int64_t tokens_partial_floats(int64_t M, int64_t P, int r);
-hipError_t launch_tokens(const TokensArgs& a, bool q8, hipStream_t stream);
+int64_t plane_bytes(int64_t M, int r);
+hipError_t launch_tokens(TokensArgs dB, const TokensArgs& dA, hipStream_t stream);
 
-struct DuArgs {  // du[m][j] = s sum_n dY[m][n] B[n][j]
+struct DuArgs {  // du[m][j] = s sum_n dY[m][n] B[n][j]; planes of u and of du xs
   const uint16_t* dy;     // [M][N], N % 16 == 0
   const uint16_t* B;      // [N][r]
+  const float* u;         // [M][r]
+  const float* xs;        // [M]
   int64_t M, N;
   int32_t r;
   float s;
   float* du;              // [M][r]
+  u32x4* u_planes;
+  u32x4* du_planes;
   int32_t splits;         // du_splits(M, N)
+  int32_t tiles;          // (set by the launcher)
   float* partial;         // du_partial_floats(M, N, r)
   uint32_t* counters;     // du_tiles(M)
 };
 int64_t du_tiles(int64_t M);
 int du_splits(int64_t M, int64_t N);
 int64_t du_partial_floats(int64_t M, int64_t N, int r);
-hipError_t launch_du_stream(const DuArgs& a, hipStream_t stream);
+hipError_t launch_du(DuArgs a, hipStream_t stream);
 
 // ------------------------------------------------------------ adapter ops
 struct NtArgs {  // C[m][j] = alpha * sum_k X[m][k] Y[j][k]
