@@ -66,12 +66,20 @@ __device__ __forceinline__ bool join_shares(float* partial, uint32_t* counters, 
   if (wave >= 4) return true;
 #pragma unroll
   for (int t = 0; t < G; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int sp = 0; sp < S; ++sp) {
-    f32x4 v[G];
+  // (several shares' loads in flight: one after the other they cost over a
+  // microsecond each)
+  constexpr int kBatch = G >= 8 ? 2 : 16 / G;
+  for (int sp0 = 0; sp0 < S; sp0 += kBatch) {
+    f32x4 v[kBatch][G];
 #pragma unroll
-    for (int t = 0; t < G; ++t) v[t] = ld_sys16(pr, off(sp, t));
+    for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-    for (int t = 0; t < G; ++t) o[t] += v[t];
+      for (int t = 0; t < G; ++t) v[b][t] = ld_sys16(pr, off(sp0 + b < S ? sp0 + b : S - 1, t));
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (sp0 + b < S)
+#pragma unroll
+        for (int t = 0; t < G; ++t) o[t] += v[b][t];
   }
   return true;
 }
@@ -115,7 +123,7 @@ constexpr int tokens_waves(int jt) { return jt <= 2 ? 8 : 4; }
 
 template <bool Q8, int JT>
 __device__ __forceinline__ void tokens_block(const TokensArgs& a, int block, f32x4* s_acc, uint32_t* s_ticket) {
-  constexpr int kWaves = tokens_waves(JT), kRing = 4;
+  constexpr int kWaves = tokens_waves(JT), kRing = Q8 ? 8 : 4;
   constexpr int kEl = Q8 ? 1 : 2, kW = kEl;  // words of a lane's piece of a row
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -249,16 +257,16 @@ __device__ __forceinline__ void tokens_block(const TokensArgs& a, int block, f32
   }
 }
 
-// dB's blocks, then dA's.
+// dA's blocks, the longer ones, then dB's.
 template <int JT>
 __global__ __launch_bounds__(64 * tokens_waves(JT), tokens_waves(JT) / 4) void k_tokens(TokensArgs b, TokensArgs a) {
   __shared__ __attribute__((aligned(16))) f32x4 s_acc[tokens_waves(JT) * kFW * 4 * 64];
   __shared__ uint32_t s_ticket;
-  const int block = static_cast<int>(blockIdx.x), nb = b.blocks;
-  if (block < nb)
-    tokens_block<false, JT>(b, block, s_acc, &s_ticket);
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < a.blocks)
+    tokens_block<true, JT>(a, block, s_acc, &s_ticket);
   else
-    tokens_block<true, JT>(a, block - nb, s_acc, &s_ticket);
+    tokens_block<false, JT>(b, block - a.blocks, s_acc, &s_ticket);
 }
 
 // ------------------------------------------------- sums over the output features
@@ -270,10 +278,12 @@ __global__ __launch_bounds__(64 * tokens_waves(JT), tokens_waves(JT) / 4) void k
 // back inside the row where it would pass r (those columns are then formed
 // twice, alike).  The finished tile also leaves as planes of du xs.
 // Blocks past du's lay out u's planes, four steps each.
+constexpr int du_waves(int fw) { return fw <= 4 ? 8 : 4; }
+
 template <int FW>
-__global__ __launch_bounds__(256, 1) void k_du(DuArgs a) {
-  constexpr int kRing = FW == 8 ? 3 : 4, kW = FW >= 2 ? FW / 2 : 1;
-  __shared__ __attribute__((aligned(16))) f32x4 s_acc[4 * FW * 4 * 64];
+__global__ __launch_bounds__(64 * du_waves(FW), du_waves(FW) / 4) void k_du(DuArgs a) {
+  constexpr int kWaves = du_waves(FW), kThreads = 64 * kWaves, kRing = FW >= 4 ? 3 : 4, kW = FW >= 2 ? FW / 2 : 1;
+  __shared__ __attribute__((aligned(16))) f32x4 s_acc[kWaves * FW * 4 * 64];
   __shared__ uint32_t s_ticket;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -283,7 +293,7 @@ __global__ __launch_bounds__(256, 1) void k_du(DuArgs a) {
   const int du_blocks = a.tiles * S;
   if (static_cast<int>(blockIdx.x) >= du_blocks) {
     const int64_t m0 = static_cast<int64_t>(static_cast<int>(blockIdx.x) - du_blocks) * 64;
-    for (int i = tid; i < 4 * jt * 64; i += 256) {
+    for (int i = tid; i < 4 * jt * 64; i += kThreads) {
       const int ln = i & 63, tile = i / 64 % jt, st = i / 64 / jt;
       const int j = 32 * tile + (ln & 31);
       const int64_t m = m0 + 16 * st + 8 * (ln >> 5);
@@ -297,8 +307,8 @@ __global__ __launch_bounds__(256, 1) void k_du(DuArgs a) {
   }
   const int tile = static_cast<int>(blockIdx.x) / S, share = static_cast<int>(blockIdx.x) % S;
   const int64_t m0 = static_cast<int64_t>(tile) * 64;
-  const int slices = static_cast<int>((N + 31) / 32), per = (slices + 4 * S - 1) / (4 * S);
-  const int b0 = (share * 4 + wave) * per;
+  const int slices = static_cast<int>((N + 31) / 32), per = (slices + kWaves * S - 1) / (kWaves * S);
+  const int b0 = (share * kWaves + wave) * per;
   const int s0 = b0 < slices ? b0 : slices, s1 = b0 + per < slices ? b0 + per : slices;
   const int64_t rows = M - m0 < 64 ? M - m0 : 64;
   const rsrc_t yr = uniform_rsrc(a.dy + m0 * N, static_cast<uint32_t>(rows * N * 2));
@@ -365,16 +375,16 @@ __global__ __launch_bounds__(256, 1) void k_du(DuArgs a) {
   }
   // lane (l, g) holds token 16 q + 4 g + v of column c0 + t; wave w ends with q = w
   f32x4 o[FW];
-  join_waves<4, FW>(s_acc, wave, lane, acc, o);
+  join_waves<kWaves, FW>(s_acc, wave, lane, acc, o);
   if (S > 1 && !join_shares<FW>(a.partial, a.counters, tile, share, S, wave, lane, o, &s_ticket)) return;
   // the tile as fp32 rows of 32 jt + 1 words, columns past r and tokens past M zero
   float* const s_du = reinterpret_cast<float*>(s_acc);
   const int stride = 32 * jt + 1;
   __syncthreads();
-  for (int i = tid; i < 64 * stride; i += 256) s_du[i] = 0.0f;
+  for (int i = tid; i < 64 * stride; i += kThreads) s_du[i] = 0.0f;
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
+  for (int v = 0; wave < 4 && v < 4; ++v) {
     const int mr = 16 * wave + 4 * g + v;
     const int64_t m = m0 + mr;
     if (m >= M || FW * l16 >= r) continue;
@@ -387,7 +397,7 @@ __global__ __launch_bounds__(256, 1) void k_du(DuArgs a) {
     }
   }
   __syncthreads();
-  for (int i = tid; i < 4 * jt * 64; i += 256) {
+  for (int i = tid; i < 4 * jt * 64; i += kThreads) {
     const int ln = i & 63, tj = i / 64 % jt, st = i / 64 / jt;
     if (m0 + 16 * st >= M) continue;
     float z[8];
@@ -417,9 +427,9 @@ int64_t tokens_partial_floats(int64_t M, int64_t P, int r) {
 }
 int64_t plane_bytes(int64_t M, int r) { return (M + kStep - 1) / kStep * ((r + 31) / 32) * 2048; }
 
-hipError_t launch_tokens(TokensArgs b, const TokensArgs& a, hipStream_t stream) {
-  b.blocks = static_cast<int32_t>(tokens_strips(b.P) * b.splits);
-  const uint32_t grid = static_cast<uint32_t>(b.blocks + tokens_strips(a.P) * a.splits);
+hipError_t launch_tokens(const TokensArgs& b, TokensArgs a, hipStream_t stream) {
+  a.blocks = static_cast<int32_t>(tokens_strips(a.P) * a.splits);
+  const uint32_t grid = static_cast<uint32_t>(a.blocks + tokens_strips(b.P) * b.splits);
   switch ((a.r + 31) / 32) {
     case 1: hipLaunchKernelGGL(k_tokens<1>, dim3(grid), dim3(64 * tokens_waves(1)), 0, stream, b, a); break;
     case 2: hipLaunchKernelGGL(k_tokens<2>, dim3(grid), dim3(64 * tokens_waves(2)), 0, stream, b, a); break;
@@ -443,12 +453,12 @@ int64_t du_partial_floats(int64_t M, int64_t N, int r) {
 
 hipError_t launch_du(DuArgs a, hipStream_t stream) {
   a.tiles = static_cast<int32_t>(du_tiles(a.M));
-  const dim3 grid(static_cast<uint32_t>(a.tiles * a.splits + a.tiles)), block(256);
+  const dim3 grid(static_cast<uint32_t>(a.tiles * a.splits + a.tiles));
   switch (du_fw(a.r)) {
-    case 1: hipLaunchKernelGGL(k_du<1>, grid, block, 0, stream, a); break;
-    case 2: hipLaunchKernelGGL(k_du<2>, grid, block, 0, stream, a); break;
-    case 4: hipLaunchKernelGGL(k_du<4>, grid, block, 0, stream, a); break;
-    default: hipLaunchKernelGGL(k_du<8>, grid, block, 0, stream, a); break;
+    case 1: hipLaunchKernelGGL(k_du<1>, grid, dim3(64 * du_waves(1)), 0, stream, a); break;
+    case 2: hipLaunchKernelGGL(k_du<2>, grid, dim3(64 * du_waves(2)), 0, stream, a); break;
+    case 4: hipLaunchKernelGGL(k_du<4>, grid, dim3(64 * du_waves(4)), 0, stream, a); break;
+    default: hipLaunchKernelGGL(k_du<8>, grid, dim3(64 * du_waves(8)), 0, stream, a); break;
   }
   return hipGetLastError();
 }

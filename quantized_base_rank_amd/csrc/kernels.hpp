@@ -143,7 +143,7 @@ int64_t tokens_strips(int64_t P);
 int tokens_splits(int64_t M, int64_t P, int r);
 int64_t tokens_partial_floats(int64_t M, int64_t P, int r);
 int64_t plane_bytes(int64_t M, int r);
-hipError_t launch_tokens(TokensArgs dB, const TokensArgs& dA, hipStream_t stream);
+hipError_t launch_tokens(const TokensArgs& dB, TokensArgs dA, hipStream_t stream);
 
 struct DuArgs {  // du[m][j] = s sum_n dY[m][n] B[n][j]; planes of u and of du xs
   const uint16_t* dy;     // [M][N], N % 16 == 0
