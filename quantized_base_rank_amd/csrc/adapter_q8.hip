@@ -47,6 +47,27 @@ __device__ __forceinline__ void join_waves(f32x4* s_acc, int wave, int lane, con
   }
 }
 
+// o = the S shares' published values, added in share order, several shares'
+// loads in flight (one after the other they cost over a microsecond each).
+template <int G, typename Off>
+__device__ __forceinline__ void add_shares(rsrc_t pr, int S, Off off, f32x4 (&o)[G]) {
+  constexpr int kBatch = G >= 8 ? 2 : 16 / G;
+#pragma unroll
+  for (int t = 0; t < G; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int sp0 = 0; sp0 < S; sp0 += kBatch) {
+    f32x4 v[kBatch][G];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int t = 0; t < G; ++t) v[b][t] = ld_sys16(pr, off(sp0 + b < S ? sp0 + b : S - 1, t));
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (sp0 + b < S)
+#pragma unroll
+        for (int t = 0; t < G; ++t) o[t] += v[b][t];
+  }
+}
+
 // Publishes the G lane values of a workgroup's first four waves as share
 // `share` of `S`; true in the last workgroup of `tile`, whose o then holds the
 // shares' sum.
@@ -63,24 +84,7 @@ __device__ __forceinline__ bool join_shares(float* partial, uint32_t* counters, 
     for (int t = 0; t < G; ++t) st_sys16(pr, off(share, t), o[t]);
   if (publish_and_ticket(counters + tile, s_ticket) != static_cast<uint32_t>(S - 1)) return false;
   if (threadIdx.x == 0) counters[tile] = 0u;
-  if (wave >= 4) return true;
-#pragma unroll
-  for (int t = 0; t < G; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // (several shares' loads in flight: one after the other they cost over a
-  // microsecond each)
-  constexpr int kBatch = G >= 8 ? 2 : 16 / G;
-  for (int sp0 = 0; sp0 < S; sp0 += kBatch) {
-    f32x4 v[kBatch][G];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-      for (int t = 0; t < G; ++t) v[b][t] = ld_sys16(pr, off(sp0 + b < S ? sp0 + b : S - 1, t));
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (sp0 + b < S)
-#pragma unroll
-        for (int t = 0; t < G; ++t) o[t] += v[b][t];
-  }
+  if (wave < 4) add_shares<G>(pr, S, off, o);
   return true;
 }
 
@@ -271,54 +275,45 @@ __global__ __launch_bounds__(64 * tokens_waves(JT), tokens_waves(JT) / 4) void k
 
 // ------------------------------------------------- sums over the output features
 
-// du = s dY B: a workgroup takes 64 tokens (four 16-row operands of the
+// du = s dY B: a workgroup of 4 waves takes 16 RT tokens (RT operands of the
 // 16x16x32 instruction, lane (l, g): 8 consecutive n from 8 g of row l, so 64
 // bytes of each row a load) and a share of the n; B's rows are paired in
 // registers, lane l holding columns c0 .. c0 + FW - 1 with c0 = FW l, moved
 // back inside the row where it would pass r (those columns are then formed
-// twice, alike).  The finished tile also leaves as planes of du xs.
-// Blocks past du's lay out u's planes, four steps each.
-constexpr int du_waves(int fw) { return fw <= 4 ? 8 : 4; }
+// twice, alike).  The first share of a tile also lays u's planes out, the last
+// one to finish those of du xs.  Fewer tokens a workgroup read B more often,
+// more of them need more shares, whose join (write-through stores, ticket,
+// reload) is a chain of some 6 us: at 4096 x 8192, rank 64, RT = 1, 2, 4 on
+// 256 workgroups take 34, 29 and 32 us, on 512 38, 33 and 37.
+constexpr int kDuWaves = 4;
 
-template <int FW>
-__global__ __launch_bounds__(64 * du_waves(FW), du_waves(FW) / 4) void k_du(DuArgs a) {
-  constexpr int kWaves = du_waves(FW), kThreads = 64 * kWaves, kRing = FW >= 4 ? 3 : 4, kW = FW >= 2 ? FW / 2 : 1;
-  __shared__ __attribute__((aligned(16))) f32x4 s_acc[kWaves * FW * 4 * 64];
+template <int FW, int RT>
+__global__ __launch_bounds__(64 * kDuWaves, FW == 8 ? 1 : 2) void k_du(DuArgs a) {
+  constexpr int kThreads = 64 * kDuWaves, kRing = FW == 8 ? 3 : 4, kW = FW >= 2 ? FW / 2 : 1, kTok = 16 * RT;
+  constexpr int kItems = FW * RT, kMine = (kItems + kDuWaves - 1) / kDuWaves;
+  __shared__ __attribute__((aligned(16))) f32x4 s_acc[kDuWaves * kItems * 64];
+  float* const s_du = reinterpret_cast<float*>(s_acc);  // (once the waves' sums are joined)
+  static_assert(kTok * (16 * FW + 16 + 1) <= kDuWaves * kItems * 256, "32 jt <= 16 FW + 16 columns");
   __shared__ uint32_t s_ticket;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int S = a.splits, r = a.r, jt = (r + 31) / 32;
   const int64_t M = a.M, N = a.N;
-  const int du_blocks = a.tiles * S;
-  if (static_cast<int>(blockIdx.x) >= du_blocks) {
-    const int64_t m0 = static_cast<int64_t>(static_cast<int>(blockIdx.x) - du_blocks) * 64;
-    for (int i = tid; i < 4 * jt * 64; i += kThreads) {
-      const int ln = i & 63, tile = i / 64 % jt, st = i / 64 / jt;
-      const int j = 32 * tile + (ln & 31);
-      const int64_t m = m0 + 16 * st + 8 * (ln >> 5);
-      if (m0 + 16 * st >= M) continue;
-      float z[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = j < r && m + e < M ? a.u[(m + e) * r + j] : 0.0f;
-      store_planes(a.u_planes, m0 / kStep + st, jt, tile, ln, z);
-    }
-    return;
-  }
   const int tile = static_cast<int>(blockIdx.x) / S, share = static_cast<int>(blockIdx.x) % S;
-  const int64_t m0 = static_cast<int64_t>(tile) * 64;
-  const int slices = static_cast<int>((N + 31) / 32), per = (slices + kWaves * S - 1) / (kWaves * S);
-  const int b0 = (share * kWaves + wave) * per;
+  const int64_t m0 = static_cast<int64_t>(tile) * kTok;
+  const int slices = static_cast<int>((N + 31) / 32), per = (slices + kDuWaves * S - 1) / (kDuWaves * S);
+  const int b0 = (share * kDuWaves + wave) * per;
   const int s0 = b0 < slices ? b0 : slices, s1 = b0 + per < slices ? b0 + per : slices;
-  const int64_t rows = M - m0 < 64 ? M - m0 : 64;
+  const int64_t rows = M - m0 < kTok ? M - m0 : kTok;
   const rsrc_t yr = uniform_rsrc(a.dy + m0 * N, static_cast<uint32_t>(rows * N * 2));
   const int c0 = FW * l16 + FW <= r ? FW * l16 : r - FW;
-  uint32_t yo[4];
+  uint32_t yo[RT];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) yo[t] = static_cast<uint32_t>(((16 * t + l16) * N + 8 * g) * 2);
+  for (int t = 0; t < RT; ++t) yo[t] = static_cast<uint32_t>(((16 * t + l16) * N + 8 * g) * 2);
   typedef uint32_t words_t __attribute__((ext_vector_type(kW == 1 ? 2 : kW)));
   struct Slice {
-    u32x4 y[4];
+    u32x4 y[RT];
     words_t b[8];
   };
   Slice ring[kRing];
@@ -330,7 +325,7 @@ __global__ __launch_bounds__(64 * du_waves(FW), du_waves(FW) / 4) void k_du(DuAr
     const bool ok = in && n < N;
     const int so = in ? sl * 64 : 0;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) v.y[t] = __builtin_amdgcn_raw_buffer_load_b128(yr, ok ? yo[t] : 0x80000000u, so, 0);
+    for (int t = 0; t < RT; ++t) v.y[t] = __builtin_amdgcn_raw_buffer_load_b128(yr, ok ? yo[t] : 0x80000000u, so, 0);
     const uint16_t* const bp = a.B + (n < N ? n : 0) * r + c0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -345,13 +340,24 @@ __global__ __launch_bounds__(64 * du_waves(FW), du_waves(FW) / 4) void k_du(DuAr
       }
     }
   };
-  f32x4 acc[FW][4];  // [column of the lane][16 tokens]
+  f32x4 acc[FW][RT];  // [column of the lane][16 tokens]
 #pragma unroll
   for (int t = 0; t < FW; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[t][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < RT; ++q) acc[t][q] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) load(s0 + i, ring[i]);
+  if (share == 0)
+    for (int i = tid; i < RT * jt * 64; i += kThreads) {
+      const int ln = i & 63, tj = i / 64 % jt, st = i / 64 / jt;
+      const int j = 32 * tj + (ln & 31);
+      const int64_t m = m0 + 16 * st + 8 * (ln >> 5);
+      if (m0 + 16 * st >= M) continue;
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = j < r && m + e < M ? a.u[(m + e) * r + j] : 0.0f;
+      store_planes(a.u_planes, m0 / kStep + st, jt, tj, ln, z);
+    }
   for (int sl = s0; sl < s1; sl += kRing) {
 #pragma unroll
     for (int i = 0; i < kRing; ++i) {
@@ -368,36 +374,58 @@ __global__ __launch_bounds__(64 * du_waves(FW), du_waves(FW) / 4) void k_du(DuAr
           b[e] = ok ? w : 0u;
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[t][q] = mfma16(v.y[q], b, acc[t][q]);
+        for (int q = 0; q < RT; ++q) acc[t][q] = mfma16(v.y[q], b, acc[t][q]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // lane (l, g) holds token 16 q + 4 g + v of column c0 + t; wave w ends with q = w
-  f32x4 o[FW];
-  join_waves<kWaves, FW>(s_acc, wave, lane, acc, o);
-  if (S > 1 && !join_shares<FW>(a.partial, a.counters, tile, share, S, wave, lane, o, &s_ticket)) return;
+  // Lane (l, g) holds token 16 q + 4 g + v of column c0 + t: item t RT + q.
+  // The waves' sums, in wave order; wave w ends with items w, w + 8, ...
+#pragma unroll
+  for (int t = 0; t < FW; ++t)
+#pragma unroll
+    for (int q = 0; q < RT; ++q) s_acc[(wave * kItems + t * RT + q) * 64 + lane] = acc[t][q];
+  __syncthreads();
+  f32x4 o[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int item = wave + kDuWaves * i < kItems ? wave + kDuWaves * i : kItems - 1;
+    o[i] = s_acc[item * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < kDuWaves; ++w) o[i] += s_acc[(w * kItems + item) * 64 + lane];
+  }
+  if (S > 1) {
+    constexpr uint32_t kShare = kDuWaves * kMine * 1024u;
+    const rsrc_t pr = make_rsrc(reinterpret_cast<const uint8_t*>(a.partial) + static_cast<int64_t>(tile) * S * kShare);
+    auto off = [&](int sp, int i) { return static_cast<uint32_t>(sp) * kShare + static_cast<uint32_t>((wave * kMine + i) * 1024 + lane * 16); };
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) st_sys16(pr, off(share, i), o[i]);
+    if (publish_and_ticket(a.counters + tile, &s_ticket) != static_cast<uint32_t>(S - 1)) return;
+    if (tid == 0) a.counters[tile] = 0u;
+    add_shares<kMine>(pr, S, off, o);
+  }
   // the tile as fp32 rows of 32 jt + 1 words, columns past r and tokens past M zero
-  float* const s_du = reinterpret_cast<float*>(s_acc);
   const int stride = 32 * jt + 1;
   __syncthreads();
-  for (int i = tid; i < 64 * stride; i += kThreads) s_du[i] = 0.0f;
+  for (int i = tid; i < kTok * stride; i += kThreads) s_du[i] = 0.0f;
   __syncthreads();
 #pragma unroll
-  for (int v = 0; wave < 4 && v < 4; ++v) {
-    const int mr = 16 * wave + 4 * g + v;
-    const int64_t m = m0 + mr;
-    if (m >= M || FW * l16 >= r) continue;
-    const float xs = a.xs[m];
+  for (int i = 0; i < kMine; ++i) {
+    const int item = wave + kDuWaves * i;
+    if (item >= kItems) continue;
+    const int t = item / RT, q = item % RT;
 #pragma unroll
-    for (int t = 0; t < FW; ++t) {
-      const float du = a.s * o[t][v];
+    for (int v = 0; v < 4; ++v) {
+      const int mr = 16 * q + 4 * g + v;
+      const int64_t m = m0 + mr;
+      if (m >= M || FW * l16 >= r) continue;
+      const float du = a.s * o[i][v];
       a.du[m * r + c0 + t] = du;
-      s_du[mr * stride + c0 + t] = du * xs;
+      s_du[mr * stride + c0 + t] = du * a.xs[m];
     }
   }
   __syncthreads();
-  for (int i = tid; i < 4 * jt * 64; i += kThreads) {
+  for (int i = tid; i < RT * jt * 64; i += kThreads) {
     const int ln = i & 63, tj = i / 64 % jt, st = i / 64 / jt;
     if (m0 + 16 * st >= M) continue;
     float z[8];
@@ -408,6 +436,7 @@ __global__ __launch_bounds__(64 * du_waves(FW), du_waves(FW) / 4) void k_du(DuAr
 }
 
 int du_fw(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
+int du_rt(int64_t M) { return M < 16384 ? 2 : 4; }
 
 }  // namespace
 
@@ -439,28 +468,36 @@ hipError_t launch_tokens(const TokensArgs& b, TokensArgs a, hipStream_t stream) 
   return hipGetLastError();
 }
 
-int64_t du_tiles(int64_t M) { return (M + 63) / 64; }
+int64_t du_tiles(int64_t M) { return (M + 16 * du_rt(M) - 1) / (16 * du_rt(M)); }
+// Shares of the n: about one workgroup per compute unit, each wave at least 16
+// slices (fewer would not pay for the join).
 int du_splits(int64_t M, int64_t N) {
   int64_t s = 256 / du_tiles(M);
-  const int64_t slices = (N + 31) / 32;
-  if (s > slices / 8) s = slices / 8;
+  const int64_t most = (N + 31) / 32 / (4 * kDuWaves);
+  if (s > most) s = most;
   return static_cast<int>(s < 1 ? 1 : s);
 }
 int64_t du_partial_floats(int64_t M, int64_t N, int r) {
-  const int64_t s = du_splits(M, N);
-  return s > 1 ? s * du_tiles(M) * 4 * du_fw(r) * 256 : 0;
+  const int64_t s = du_splits(M, N), items = du_fw(r) * du_rt(M);
+  return s > 1 ? s * du_tiles(M) * kDuWaves * ((items + kDuWaves - 1) / kDuWaves) * 256 : 0;
 }
 
-hipError_t launch_du(DuArgs a, hipStream_t stream) {
-  a.tiles = static_cast<int32_t>(du_tiles(a.M));
-  const dim3 grid(static_cast<uint32_t>(a.tiles * a.splits + a.tiles));
+namespace {
+template <int RT>
+hipError_t launch_du_rt(const DuArgs& a, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(du_tiles(a.M) * a.splits)), block(64 * kDuWaves);
   switch (du_fw(a.r)) {
-    case 1: hipLaunchKernelGGL(k_du<1>, grid, dim3(64 * du_waves(1)), 0, stream, a); break;
-    case 2: hipLaunchKernelGGL(k_du<2>, grid, dim3(64 * du_waves(2)), 0, stream, a); break;
-    case 4: hipLaunchKernelGGL(k_du<4>, grid, dim3(64 * du_waves(4)), 0, stream, a); break;
-    default: hipLaunchKernelGGL(k_du<8>, grid, dim3(64 * du_waves(8)), 0, stream, a); break;
+    case 1: hipLaunchKernelGGL((k_du<1, RT>), grid, block, 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((k_du<2, RT>), grid, block, 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((k_du<4, RT>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_du<8, RT>), grid, block, 0, stream, a); break;
   }
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_du(const DuArgs& a, hipStream_t stream) {
+  return du_rt(a.M) == 2 ? launch_du_rt<2>(a, stream) : launch_du_rt<4>(a, stream);
 }
 
 }  // namespace qlin

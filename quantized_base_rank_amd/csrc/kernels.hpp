@@ -157,14 +157,13 @@ struct DuArgs {  // du[m][j] = s sum_n dY[m][n] B[n][j]; planes of u and of du x
   u32x4* u_planes;
   u32x4* du_planes;
   int32_t splits;         // du_splits(M, N)
-  int32_t tiles;          // (set by the launcher)
   float* partial;         // du_partial_floats(M, N, r)
   uint32_t* counters;     // du_tiles(M)
 };
 int64_t du_tiles(int64_t M);
 int du_splits(int64_t M, int64_t N);
 int64_t du_partial_floats(int64_t M, int64_t N, int r);
-hipError_t launch_du(DuArgs a, hipStream_t stream);
+hipError_t launch_du(const DuArgs& a, hipStream_t stream);
 
 // ------------------------------------------------------------ adapter ops
 struct NtArgs {  // C[m][j] = alpha * sum_k X[m][k] Y[j][k]
