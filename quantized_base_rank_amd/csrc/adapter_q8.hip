@@ -173,12 +173,19 @@ __device__ __forceinline__ void tokens_block(const TokensArgs& a, int block, f32
   for (int j = 0; j < JT; ++j)
 #pragma unroll
     for (int t = 0; t < kFW; ++t) acc[j][t] = f32x16{};
+  // (issued in the loop's own order: at the loop's head the compiler waits for
+  // what both ways in leave pending)
 #pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) load_x(st0 + i, x[i]);
-  load_z(st0, z[0]);
+  for (int i = 0; i < kRing - 1; ++i) {
+    if (i == kRing - 2) load_z(st0, z[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    load_x(st0 + i, x[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   for (int64_t st = st0; st < st1; st += kRing) {
 #pragma unroll
     for (int i = 0; i < kRing; ++i) {
+      if (i > 0 && st + i >= st1) break;
       // (the planes come from the cache: one step ahead is enough)
       load_z(st + i + 1, z[(i + 1) % 2]);
       load_x(st + i + kRing - 1, x[(i + kRing - 1) % kRing]);
