@@ -14,7 +14,7 @@ from typing import Optional
 
 import numpy as np
 
-from ._lib import (EXPORTS, LIB_PATH, QLIN_BF16, QLIN_F32, QLIN_FMT_INT4_GROUP, QLIN_FMT_NF,
+from ._lib import (EXPORTS, LIB_PATH, QLIN_BF16, QLIN_E_WORKSPACE, QLIN_F32, QLIN_FMT_INT4_GROUP, QLIN_FMT_NF,
                    QLIN_FMT_NF4, QlinError, QWeightStruct, check, lib)
 
 __all__ = [
@@ -27,9 +27,15 @@ __all__ = [
 ]
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t) -> Optional[int]:
@@ -45,7 +51,7 @@ def _stream(device) -> int:
 
 
 def _need(t, dtype, shape, name):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: expected contiguous {dtype} CUDA tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} "
                          f"cuda={t.is_cuda}")
@@ -356,6 +362,20 @@ def _stream_workspace(device, stream: int, nbytes: int):
     return ws
 
 
+def _call_with_workspace(call, nbytes, device, stream: int, ws) -> int:
+    """``call(ws)`` with the caller's workspace, or with this stream's.  The
+    call itself says when that is too small (before it enqueues anything), so
+    the size is asked for only then."""
+    if ws is not None:
+        return call(ws)
+    ws = _WS_STREAM.get((device.index, stream))
+    if ws is not None:
+        status = call(ws)
+        if status != QLIN_E_WORKSPACE:
+            return status
+    return call(_stream_workspace(device, stream, nbytes()))
+
+
 def qlin_quantize_q8(x, codes=None, scale=None, values=None) -> Q8Rows:
     """Rows of x (bf16 or fp32, [rows][d]) in 8 bits, one scale per row.
     ``values`` (bf16 [rows][d]) receives codes * scale when given."""
@@ -453,12 +473,13 @@ def qlin_rmsnorm_bwd(h, gamma, rstd, dy, dh=None, dx=None, dgamma=None, ws=None)
         dgamma = torch.empty((d,), dtype=torch.float32, device=dev)
     else:
         _need(dgamma, torch.float32, (d,), "dgamma")
-    st = _stream(dev)
-    if ws is None:
-        ws = _stream_workspace(dev, st, lib().qlin_rmsnorm_workspace_bytes(M, d))
-    check(lib().qlin_rmsnorm_bwd(h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), dy.data_ptr(), _ptr(dh),
-                                 M, d, dx.data_ptr(), dgamma.data_ptr(), ws.data_ptr(), ws.numel(), st),
-          "qlin_rmsnorm_bwd")
+    st, L = _stream(dev), lib()
+
+    def call(ws):
+        return L.qlin_rmsnorm_bwd(h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), dy.data_ptr(), _ptr(dh), M, d,
+                                  dx.data_ptr(), dgamma.data_ptr(), ws.data_ptr(), ws.numel(), st)
+
+    check(_call_with_workspace(call, lambda: L.qlin_rmsnorm_workspace_bytes(M, d), dev, st, ws), "qlin_rmsnorm_bwd")
     return dx, dgamma
 
 
@@ -474,12 +495,13 @@ def qlin_w8a8_fwd(x: Q8Rows, w: Q8Rows, y=None, ws=None):
         y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     else:
         _need(y, torch.bfloat16, (M, N), "y")
-    st = _stream(dev)
-    if ws is None:
-        ws = _stream_workspace(dev, st, lib().qlin_w8a8_workspace_bytes(M, N, K))
-    check(lib().qlin_w8a8_fwd(x.codes.data_ptr(), x.scale.data_ptr(), M, w.codes.data_ptr(),
-                              w.scale.data_ptr(), N, K, y.data_ptr(), ws.data_ptr(), ws.numel(), st),
-          "qlin_w8a8_fwd")
+    st, L = _stream(dev), lib()
+
+    def call(ws):
+        return L.qlin_w8a8_fwd(x.codes.data_ptr(), x.scale.data_ptr(), M, w.codes.data_ptr(), w.scale.data_ptr(), N, K,
+                               y.data_ptr(), ws.data_ptr(), ws.numel(), st)
+
+    check(_call_with_workspace(call, lambda: L.qlin_w8a8_workspace_bytes(M, N, K), dev, st, ws), "qlin_w8a8_fwd")
     return y
 
 
@@ -509,16 +531,16 @@ def qlin_bwd_q8(w: QWeight, x: Q8Rows, A, B, r: int, s: float, dy, u, pool: int 
         dB = torch.empty((w.d_out, r), dtype=torch.bfloat16, device=dev)
     else:
         _need(dB, torch.bfloat16, (w.d_out, r), "dB")
-    s_ = w.struct()
-    st = _stream(dev)
-    if ws is None:
-        nbytes = lib().qlin_bwd_q8_workspace_bytes(ctypes.byref(s_), M, r, pool)
-        if nbytes == 0:
-            raise QlinError(2, "qlin_bwd_q8_workspace_bytes")
-        ws = _stream_workspace(dev, st, nbytes)
-    check(lib().qlin_bwd_q8(ctypes.byref(s_), x.codes.data_ptr(), x.scale.data_ptr(), M, A.data_ptr(),
-                            B.data_ptr(), r, float(s), pool, dy.data_ptr(), u.data_ptr(), _ptr(dx),
-                            dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.numel(), st), "qlin_bwd_q8")
+    wref = ctypes.byref(w.struct())
+    st, L = _stream(dev), lib()
+
+    def call(ws):
+        return L.qlin_bwd_q8(wref, x.codes.data_ptr(), x.scale.data_ptr(), M, A.data_ptr(), B.data_ptr(), r, float(s),
+                             pool, dy.data_ptr(), u.data_ptr(), _ptr(dx), dA.data_ptr(), dB.data_ptr(), ws.data_ptr(),
+                             ws.numel(), st)
+
+    check(_call_with_workspace(call, lambda: L.qlin_bwd_q8_workspace_bytes(wref, M, r, pool), dev, st, ws),
+          "qlin_bwd_q8")
     return dx, dA, dB
 
 

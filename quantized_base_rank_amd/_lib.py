@@ -9,6 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libqlin.so")
 
 QLIN_OK = 0
+QLIN_E_WORKSPACE = 6
 QLIN_FMT_NF4 = 1
 QLIN_FMT_INT4_GROUP = 2
 QLIN_FMT_NF = 3
