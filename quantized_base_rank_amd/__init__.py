@@ -347,32 +347,35 @@ def _need_q8(q: Q8Rows, shape, name):
 
 
 _WS_STREAM = {}
+_WS_COUNTERS = 1 << 16  # bytes at a workspace's start that have to be zero before its first use
 
 
 def _stream_workspace(device, stream: int, nbytes: int):
-    """A zero-filled workspace of at least ``nbytes`` for calls on one stream of
-    one device (grown on demand), so that calls in flight on different streams
-    never share one."""
+    """A workspace of at least ``nbytes`` for calls on one stream of one device
+    (grown on demand), so that calls in flight on different streams never
+    share one."""
     torch = _torch()
-    key = (device.index, stream)
-    ws = _WS_STREAM.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _WS_STREAM[key] = ws
+    ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    ws[:_WS_COUNTERS].zero_()
+    if not torch.cuda.is_current_stream_capturing():
+        _WS_STREAM[(device.index, stream)] = ws
     return ws
 
 
 def _call_with_workspace(call, nbytes, device, stream: int, ws) -> int:
     """``call(ws)`` with the caller's workspace, or with this stream's.  The
     call itself says when that is too small (before it enqueues anything), so
-    the size is asked for only then."""
+    the size is asked for only then.  A call that is being captured into a
+    graph gets memory of that graph's own: the stream's workspace may be
+    replaced while the graph lives."""
     if ws is not None:
         return call(ws)
-    ws = _WS_STREAM.get((device.index, stream))
-    if ws is not None:
-        status = call(ws)
-        if status != QLIN_E_WORKSPACE:
-            return status
+    if not _torch().cuda.is_current_stream_capturing():
+        ws = _WS_STREAM.get((device.index, stream))
+        if ws is not None:
+            status = call(ws)
+            if status != QLIN_E_WORKSPACE:
+                return status
     return call(_stream_workspace(device, stream, nbytes()))
 
 
@@ -386,11 +389,11 @@ def qlin_quantize_q8(x, codes=None, scale=None, values=None) -> Q8Rows:
     dev = x.device
     _need(x, x.dtype, (rows, d), "x")
     if codes is None:
-        codes = torch.empty((rows, d), dtype=torch.int8, device=dev)
+        codes = torch.empty(rows, d, dtype=torch.int8, device=dev)
     else:
         _need(codes, torch.int8, (rows, d), "codes")
     if scale is None:
-        scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+        scale = torch.empty(rows, dtype=torch.float32, device=dev)
     else:
         _need(scale, torch.float32, (rows,), "scale")
     if values is not None:
@@ -407,7 +410,7 @@ def qlin_dequant_q8(q: Q8Rows, out=None):
     rows, d = q.codes.shape
     _need_q8(q, (rows, d), "q")
     if out is None:
-        out = torch.empty((rows, d), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(rows, d, dtype=torch.bfloat16, device=q.device)
     else:
         _need(out, torch.bfloat16, (rows, d), "out")
     check(lib().qlin_dequant_q8(q.codes.data_ptr(), q.scale.data_ptr(), rows, d, out.data_ptr(),
@@ -432,15 +435,15 @@ def qlin_rmsnorm_q8(x, gamma, eps: float, residual=None, want_values: bool = Fal
         else:
             _need(h, torch.bfloat16, (M, d), "h")
     if codes is None:
-        codes = torch.empty((M, d), dtype=torch.int8, device=dev)
+        codes = torch.empty(M, d, dtype=torch.int8, device=dev)
     else:
         _need(codes, torch.int8, (M, d), "codes")
     if scale is None:
-        scale = torch.empty((M,), dtype=torch.float32, device=dev)
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
     else:
         _need(scale, torch.float32, (M,), "scale")
     if rstd is None:
-        rstd = torch.empty((M,), dtype=torch.float32, device=dev)
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
     else:
         _need(rstd, torch.float32, (M,), "rstd")
     if values is not None:
@@ -470,7 +473,7 @@ def qlin_rmsnorm_bwd(h, gamma, rstd, dy, dh=None, dx=None, dgamma=None, ws=None)
     else:
         _need(dx, torch.bfloat16, (M, d), "dx")
     if dgamma is None:
-        dgamma = torch.empty((d,), dtype=torch.float32, device=dev)
+        dgamma = torch.empty(d, dtype=torch.float32, device=dev)
     else:
         _need(dgamma, torch.float32, (d,), "dgamma")
     st, L = _stream(dev), lib()
@@ -492,7 +495,7 @@ def qlin_w8a8_fwd(x: Q8Rows, w: Q8Rows, y=None, ws=None):
     _need_q8(x, (M, K), "x")
     _need_q8(w, (N, K), "w")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
     else:
         _need(y, torch.bfloat16, (M, N), "y")
     st, L = _stream(dev), lib()
@@ -520,15 +523,15 @@ def qlin_bwd_q8(w: QWeight, x: Q8Rows, A, B, r: int, s: float, dy, u, pool: int 
     if not need_dx:
         dx = None
     elif dx is None:
-        dx = torch.empty((M, w.d_in), dtype=torch.bfloat16, device=dev)
+        dx = torch.empty(M, w.d_in, dtype=torch.bfloat16, device=dev)
     else:
         _need(dx, torch.bfloat16, (M, w.d_in), "dx")
     if dA is None:
-        dA = torch.empty((r, w.d_in // pool), dtype=torch.bfloat16, device=dev)
+        dA = torch.empty(r, w.d_in // pool, dtype=torch.bfloat16, device=dev)
     else:
         _need(dA, torch.bfloat16, (r, w.d_in // pool), "dA")
     if dB is None:
-        dB = torch.empty((w.d_out, r), dtype=torch.bfloat16, device=dev)
+        dB = torch.empty(w.d_out, r, dtype=torch.bfloat16, device=dev)
     else:
         _need(dB, torch.bfloat16, (w.d_out, r), "dB")
     wref = ctypes.byref(w.struct())

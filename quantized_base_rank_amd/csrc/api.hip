@@ -882,7 +882,8 @@ struct BwdQ8Plan {
   size_t off_du = 0, off_zu = 0, off_zdu = 0, off_At = 0, off_partial = 0, off_partial_dA = 0, off_tc = 0, total = 0;
 };
 
-// Tokens the products' launches and offsets are made for.
+// Sizes that the kernels' launches and 32-bit offsets (64 rows of dY, 16 rows
+// of codes) are made for: tokens, and below 2^24 features either way.
 constexpr int64_t kMaxBwdTokens = int64_t{1} << 24;
 
 BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t pool) {
@@ -898,7 +899,7 @@ BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t 
   const int64_t counters = std::max<int64_t>({p.dB_counters + (p.dA_splits > 1 ? tokens_strips(K) : 0),
                                               p.du_splits > 1 ? du_tiles(M) : 0,
                                               p.dx_stream && p.ds_splits > 1 ? dx_stream_panels(K) : 0});
-  p.fits = counters <= kCounterWords && M <= kMaxBwdTokens && 64 * N * 2 < (int64_t{1} << 31);
+  p.fits = counters <= kCounterWords && M <= kMaxBwdTokens && N < (int64_t{1} << 24) && K < (int64_t{1} << 24);
   const int64_t partial = std::max<int64_t>({du_partial_floats(M, N, r), tokens_partial_floats(M, N, r),
                                              p.dx_stream ? dx_stream_partial_floats(N, K, fmt) : 0});
   size_t off = kCounterBytes;

@@ -124,21 +124,32 @@ __device__ __forceinline__ RowScale row_scale(float mx) {
 // Sizes of a row kernel's instantiations: threads per row, vectors a thread.
 // One wave per row up to 1024 columns (several rows share a workgroup and
 // nothing needs a barrier), then as few waves as hold the row in two vectors
-// a thread, four beyond 16384 columns.  Rows below eight columns or past
-// kRowMax take the kernels that walk a row element by element.
-constexpr int kRowMin = 8, kRowMax = 32768;
-template <typename F>
+// a thread, four beyond 16384 columns.  The gradient holds three rows and its
+// sums: 512 threads at most, which have 256 registers each, so its widest
+// rows end at half the width.  Rows below eight columns or past the widest
+// take the kernels that walk a row element by element.
+constexpr int kRowMin = 8, kRowMax = 32768, kGradRowMax = 16384;
+template <bool GRAD, typename F>
 hipError_t by_row_width(int64_t d, F f) {
   if (d <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
   if (d <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
   if (d <= 2048) return f(std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{});
   if (d <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
   if (d <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
-  if (d <= 16384) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+  if constexpr (GRAD) {
+    return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
+  } else {
+    if (d <= 16384) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+  }
 }
 // Rows that share a workgroup: only rows of one wave, which need no barrier.
 constexpr int rows_per_group(int threads) { return threads == 64 ? 4 : 1; }
+// This thread's row of the group, known to be the same for its whole wave.
+template <int T>
+__device__ __forceinline__ int row_of_group() {
+  return rows_per_group(T) == 1 ? 0 : __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / T);
+}
 // Workgroups for `rows` rows, `per` of them each; a longer queue is walked.
 inline uint32_t row_grid(int64_t rows, int per) {
   const int64_t n = (rows + per - 1) / per;

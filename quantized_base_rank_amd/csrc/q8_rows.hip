@@ -42,7 +42,7 @@ __global__ __launch_bounds__(T * rows_per_group(T)) void k_quant_q8(Q8RowsArgs a
   constexpr int kRows = rows_per_group(T);
   __shared__ float s_red[T / 64];
   const int t = threadIdx.x % T, d = static_cast<int>(a.d);
-  for (int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T; m < a.rows;
+  for (int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + row_of_group<T>(); m < a.rows;
        m += static_cast<int64_t>(gridDim.x) * kRows) {
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + m * a.d;
     u32x4 v[NV];
@@ -123,7 +123,7 @@ hipError_t launch_quant_q8(const Q8RowsArgs& a, bool f32, hipStream_t stream) {
     hipLaunchKernelGGL(k_quant_q8_two_pass<false>, dim3(row_grid(a.rows, 1)), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
-  return by_row_width(a.d, [&](auto t, auto nv) {
+  return by_row_width<false>(a.d, [&](auto t, auto nv) {
     constexpr int T = decltype(t)::value, NV = decltype(nv)::value, R = rows_per_group(T);
     hipLaunchKernelGGL((k_quant_q8<T, NV>), dim3(row_grid(a.rows, R)), dim3(T * R), 0, stream, a);
     return hipGetLastError();

@@ -27,7 +27,7 @@ __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_q8(RmsNormArg
   constexpr int kRows = rows_per_group(T);
   __shared__ float s_red[T / 64];
   const int t = threadIdx.x % T, d = static_cast<int>(a.d);
-  for (int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T; m < a.M;
+  for (int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + row_of_group<T>(); m < a.M;
        m += static_cast<int64_t>(gridDim.x) * kRows) {
     const int64_t row = m * a.d;
     u32x4 xv[NV], rv[NV], gv[NV];
@@ -132,7 +132,7 @@ template <int T, int NV, bool DH>
 __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_bwd(RmsNormBwdArgs a) {
   constexpr int kRows = rows_per_group(T);
   __shared__ float s_red[2][T / 64];
-  const int t = threadIdx.x % T, sub = threadIdx.x / T, d = static_cast<int>(a.d);
+  const int t = threadIdx.x % T, sub = row_of_group<T>(), d = static_cast<int>(a.d);
   const int64_t share = static_cast<int64_t>(blockIdx.x) * kRows + sub;
   const int64_t m0 = share * a.per, m1 = m0 + a.per < a.M ? m0 + a.per : a.M;
   u32x4 gv[NV];
@@ -143,8 +143,8 @@ __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_bwd(RmsNormBw
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[i][e] = 0.0f;
   }
-  // (1024 threads leave 128 registers each: no room for the next row)
-  constexpr int kAhead = T < 1024 ? 1 : 0;
+  // (four vectors a thread leave no room for the next row)
+  constexpr int kAhead = NV < 4 ? 1 : 0;
   u32x4 hv[1 + kAhead][NV], yv[1 + kAhead][NV], ev[1 + kAhead][NV];
   float rs[1 + kAhead];
   auto load = [&](int64_t m, int p) {
@@ -160,11 +160,11 @@ __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_bwd(RmsNormBw
   };
   const float inv_d = 1.0f / static_cast<float>(a.d);
   if (kAhead != 0) load(m0, 0);
-  for (int64_t mm = m0; mm < m1; mm += 2) {
+  for (int64_t mm = m0; mm < m1; mm += 1 + kAhead) {
 #pragma unroll
-    for (int turn = 0; turn < 2; ++turn) {
-      const int p = kAhead != 0 ? turn : 0;
-      const int64_t m = mm + turn;
+    for (int p = 0; p < 1 + kAhead; ++p) {
+      const int64_t m = mm + p;
+      const int turn = static_cast<int>(m & 1);
       if (m >= m1) break;
       load(m + kAhead, kAhead != 0 ? 1 - p : 0);
       const float rstd = rs[p];
@@ -178,6 +178,7 @@ __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_bwd(RmsNormBw
           dg[i][e] = __builtin_fmaf(dy, xh, dg[i][e]);
           c = __builtin_fmaf(e >= dup ? dy * elem8(gv[i], e) : 0.0f, xh, c);
         }
+        if (NV >= 4) __builtin_amdgcn_sched_barrier(0);  // one vector unpacked at a time
       }
       // (two buffers take turns, so one barrier a row)
       c = warp_sum(c);
@@ -191,6 +192,9 @@ __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_bwd(RmsNormBw
       c *= inv_d;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
+        // (unpacked again from here: held over the sum as fp32 the row would
+        // take twice the registers, of which the wide rows have none left)
+        __asm__ volatile("" : "+v"(hv[p][i]), "+v"(yv[p][i]), "+v"(gv[i]));
         const Vec q = row_vec(t + T * i, d);
         u32x4 o;
 #pragma unroll
@@ -206,6 +210,7 @@ __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_bwd(RmsNormBw
           o[j] = pack_bf16x2(v[0], v[1]);
         }
         if (q.in) store8(a.dx + m * a.d + q.k, o);
+        if (NV >= 4) __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -284,7 +289,7 @@ hipError_t launch_rmsnorm_q8(const RmsNormArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(k_rmsnorm_q8_wide, dim3(row_grid(a.M, 1)), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
-  return by_row_width(a.d, [&](auto t, auto nv) {
+  return by_row_width<false>(a.d, [&](auto t, auto nv) {
     constexpr int T = decltype(t)::value, NV = decltype(nv)::value, R = rows_per_group(T);
     const dim3 grid(row_grid(a.M, R)), block(T * R);
     if (a.res != nullptr)
@@ -302,13 +307,13 @@ hipError_t launch_rmsnorm_bwd(const RmsNormBwdArgs& args, hipStream_t stream) {
   a.per = bwd_rows(a.M);
   const int64_t shares = bwd_shares(a.M);
   hipError_t e;
-  if (a.d < kRowMin || a.d > kRowMax) {
+  if (a.d < kRowMin || a.d > kGradRowMax) {
     hipLaunchKernelGGL(k_rmsnorm_dx_wide, dim3(row_grid(a.M, 1)), dim3(256), 0, stream, a);
     hipLaunchKernelGGL(k_rmsnorm_dgamma_wide, dim3(static_cast<uint32_t>((a.d + 255) / 256), static_cast<uint32_t>(shares)),
                        dim3(256), 0, stream, a);
     e = hipGetLastError();
   } else {
-    e = by_row_width(a.d, [&](auto t, auto nv) {
+    e = by_row_width<true>(a.d, [&](auto t, auto nv) {
       constexpr int T = decltype(t)::value, NV = decltype(nv)::value, R = rows_per_group(T);
       const dim3 grid(static_cast<uint32_t>((shares + R - 1) / R)), block(T * R);
       if (a.dh != nullptr)

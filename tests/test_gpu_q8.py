@@ -454,6 +454,46 @@ def test_other_stream_and_graph(qb, oracle):
             assert torch.equal(a, b)
 
 
+def test_graph_with_the_binding_s_workspace(qb):
+    """Captured without a workspace of the caller's: the graph keeps its own,
+    and eager calls in between that make the stream's grow leave it alone."""
+    import torch
+    rng = np.random.default_rng(12)
+    x = dev_rows(qb, codes_of(rng, 4, 8192), np.ones(4, np.float32))
+    w = dev_rows(qb, codes_of(rng, 64, 8192), np.ones(64, np.float32))  # K in shares: counters and sums
+    big = dev_rows(qb, codes_of(rng, 200, 4096), np.ones(200, np.float32))
+    bigw = dev_rows(qb, codes_of(rng, 3000, 4096), np.ones(3000, np.float32))
+    eager = qb.qlin_w8a8_fwd(x, w).clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = qb.qlin_w8a8_fwd(x, w)
+    first = qb.qlin_w8a8_fwd(big, bigw).clone()
+    for _ in range(4):
+        y.zero_()
+        assert torch.equal(qb.qlin_w8a8_fwd(x, w), eager)
+        g.replay()
+        assert torch.equal(qb.qlin_w8a8_fwd(big, bigw), first)
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager)
+
+
+@pytest.mark.parametrize("d", [9000, 16384, 20000, 32768])
+def test_norm_gradient_wide_rows(qb, d):
+    rng = np.random.default_rng(d)
+    M = 37
+    h, dy = (val(bf16(rng.standard_normal((M, d)))) for _ in range(2))
+    gamma = val(bf16(1 + 0.2 * rng.standard_normal(d)))
+    rstd = (1 / np.sqrt((h.astype(np.float64) ** 2).mean(axis=1) + 1e-5)).astype(np.float32)
+    dx, dg = qb.qlin_rmsnorm_bwd(to_dev_bf16(bf16(h)), to_dev_bf16(bf16(gamma)), to_dev_f32(rstd), to_dev_bf16(bf16(dy)))
+    dx64, dg64 = Q.rmsnorm_backward(h, gamma, rstd, dy)
+    xh = np.abs(h.astype(np.float64)) * rstd[:, None]
+    gy = np.abs(dy * gamma.astype(np.float64))
+    size = rstd[:, None] * (gy + xh * (gy * xh).mean(axis=1, keepdims=True))
+    assert (np.abs(val(bf16_host_bits(dx)) - dx64) <= np.abs(dx64) * BF + size * (SUM(d) + 10 * U)).all()
+    assert (np.abs(host(dg) - dg64) <= np.abs(dy * xh).sum(axis=0) * (M + 32) * U).all()
+
+
 def test_binding_refuses(qb):
     import torch
     x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
