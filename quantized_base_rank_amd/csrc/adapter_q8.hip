@@ -127,7 +127,7 @@ constexpr int tokens_waves(int jt) { return jt <= 2 ? 8 : 4; }
 
 template <bool Q8, int JT>
 __device__ __forceinline__ void tokens_block(const TokensArgs& a, int block, f32x4* s_acc, uint32_t* s_ticket) {
-  constexpr int kWaves = tokens_waves(JT), kRing = Q8 ? 8 : 4;
+  constexpr int kWaves = tokens_waves(JT), kRing = 3;
   constexpr int kEl = Q8 ? 1 : 2, kW = kEl;  // words of a lane's piece of a row
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -137,31 +137,41 @@ __device__ __forceinline__ void tokens_block(const TokensArgs& a, int block, f32
   const int64_t M = a.M, P = a.P, p0 = static_cast<int64_t>(strip) * kStrip;
   const int64_t steps = (M + kStep - 1) / kStep, per = (steps + kWaves * S - 1) / (kWaves * S);
   const int64_t b0 = (share * kWaves + wave) * per;
-  const int64_t st0 = b0 < steps ? b0 : steps, st1 = b0 + per < steps ? b0 + per : steps;
+  const int64_t st0 = b0 < steps ? b0 : steps;
+  // this wave's steps
+  const int n = __builtin_amdgcn_readfirstlane(static_cast<int>(b0 + per < steps ? per : steps - st0));
 
-  // Rows past M lie outside a step's resource (zeros, as Z's planes there).
-  // Columns past P hold the next row's values (or zeros), and columns of Z
-  // past r zeros: their outputs are never stored.
+  // Rows past M lie outside a step's resource (zeros, as Z's planes there),
+  // and so does everything past the wave's steps.  Columns past P hold the
+  // next row's values (or zeros), and columns of Z past r zeros: their
+  // outputs are never stored.  The loads take the steps in order, so bases
+  // and rows left are carried along in scalar registers.
   const uint32_t xo = static_cast<uint32_t>((8 * h * P + p0 + kFW * l32) * kEl);
   const uint32_t zo = static_cast<uint32_t>(lane * 16);
+  const int row_bytes = static_cast<int>(P * kEl);
   typedef uint32_t words_t __attribute__((ext_vector_type(2)));
   words_t x[kRing][8];
-  u32x4 z[2][JT][2];
-  auto load_x = [&](int64_t st, words_t (&v)[8]) {
-    const bool in = st < st1;
-    const int64_t m = (in ? st : 0) * kStep;
-    const uint32_t rows = in ? static_cast<uint32_t>(M - m < kStep ? M - m : kStep) : 0u;
-    const rsrc_t xr = uniform_rsrc(static_cast<const uint8_t*>(a.X) + m * P * kEl, rows * static_cast<uint32_t>(P * kEl));
+  u32x4 z[kRing][JT][2];
+  const uint8_t* x_base = static_cast<const uint8_t*>(a.X) + st0 * kStep * row_bytes;
+  const u32x4* z_base = a.Z + st0 * JT * 128;
+  int x_rows = __builtin_amdgcn_readfirstlane(
+      static_cast<int>(M - st0 * kStep < static_cast<int64_t>(n) * kStep ? M - st0 * kStep : static_cast<int64_t>(n) * kStep));
+  int z_steps = n;
+  auto load_x = [&](words_t (&v)[8]) {
+    const int rows = x_rows < 0 ? 0 : x_rows < kStep ? x_rows : kStep;
+    const rsrc_t xr = uniform_rsrc(x_base, static_cast<uint32_t>(rows) * static_cast<uint32_t>(row_bytes));
+    x_base += kStep * static_cast<int64_t>(row_bytes);
+    x_rows -= kStep;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int so = static_cast<int>(e * P * kEl);
-      if constexpr (kW == 2) v[e] = __builtin_amdgcn_raw_buffer_load_b64(xr, xo, so, 0);
-      else v[e][0] = __builtin_amdgcn_raw_buffer_load_b32(xr, xo, so, 0);
+      if constexpr (kW == 2) v[e] = __builtin_amdgcn_raw_buffer_load_b64(xr, xo, e * row_bytes, 0);
+      else v[e][0] = __builtin_amdgcn_raw_buffer_load_b32(xr, xo, e * row_bytes, 0);
     }
   };
-  auto load_z = [&](int64_t st, u32x4 (&v)[JT][2]) {
-    const bool in = st < st1;
-    const rsrc_t zr = uniform_rsrc(a.Z + (in ? st : 0) * JT * 128, in ? JT * 2048u : 0u);
+  auto load_z = [&](u32x4 (&v)[JT][2]) {
+    const rsrc_t zr = uniform_rsrc(z_base, z_steps > 0 ? JT * 2048u : 0u);
+    z_base += JT * 128;
+    --z_steps;
 #pragma unroll
     for (int j = 0; j < JT; ++j)
 #pragma unroll
@@ -177,18 +187,15 @@ __device__ __forceinline__ void tokens_block(const TokensArgs& a, int block, f32
   // what both ways in leave pending)
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) {
-    if (i == kRing - 2) load_z(st0, z[0]);
-    __builtin_amdgcn_sched_barrier(0);
-    load_x(st0 + i, x[i]);
+    load_z(z[i]);
+    load_x(x[i]);
     __builtin_amdgcn_sched_barrier(0);
   }
-  for (int64_t st = st0; st < st1; st += kRing) {
+  for (int st = 0; st < n; st += kRing) {
 #pragma unroll
     for (int i = 0; i < kRing; ++i) {
-      if (i > 0 && st + i >= st1) break;
-      // (the planes come from the cache: one step ahead is enough)
-      load_z(st + i + 1, z[(i + 1) % 2]);
-      load_x(st + i + kRing - 1, x[(i + kRing - 1) % kRing]);
+      load_z(z[(i + kRing - 1) % kRing]);
+      load_x(x[(i + kRing - 1) % kRing]);
       __builtin_amdgcn_sched_barrier(0);
       auto tile = [&](auto T) {
         constexpr int t = decltype(T)::value;
@@ -201,12 +208,16 @@ __device__ __forceinline__ void tokens_block(const TokensArgs& a, int block, f32
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int j = 0; j < JT; ++j) acc[j][t] = mfma32(z[i % 2][j][p], b, acc[j][t]);
+          for (int j = 0; j < JT; ++j) acc[j][t] = mfma32(z[i][j][p], b, acc[j][t]);
       };
-      tile(std::integral_constant<int, 0>{});
-      tile(std::integral_constant<int, 1>{});
-      tile(std::integral_constant<int, 2>{});
-      tile(std::integral_constant<int, 3>{});
+      // (a branch may skip arithmetic; one past the loads would make the
+      // compiler copy or spill what it carries round the loop)
+      if (i == 0 || st + i < n) {
+        tile(std::integral_constant<int, 0>{});
+        tile(std::integral_constant<int, 1>{});
+        tile(std::integral_constant<int, 2>{});
+        tile(std::integral_constant<int, 3>{});
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
