@@ -5,20 +5,28 @@
 // Tile: 256 channels x 64 J tokens (J = 1 .. 4) per workgroup of 4 waves (one
 // per SIMD), each wave 128 x 32 J in 64 J accumulator registers, so that at
 // J = 4 a K slice of 32 bytes costs 8 LDS reads of 16 bytes per lane for 16
-// matrix instructions.  Both operands stream through a ring of four
-// 64-byte-deep half-stages (32 KB each at J = 4) by direct-to-LDS loads, the
-// last of which are issued three half-stages ahead.  One barrier per
-// half-stage, in its middle: by then every wave holds the half-stage's last
-// fragments in registers, so its slot is free for the loads of the half-stage
-// four on, and the next one has landed (counted wait), so the fragments of
-// its first slice load while this one's last matrix instructions run.
+// matrix instructions.  Both operands stream through a ring of 64-byte-deep
+// half-stages (32 KB each at J = 4, five of them) by direct-to-LDS loads.
+// One barrier per half-stage, in its middle: by then every wave holds the
+// half-stage's last fragments in registers, so its slot is free for loads,
+// and the next one has landed (counted wait), so the fragments of its first
+// slice load while this one's last matrix instructions run.
 //
-// At 4096 x 8192 x 28672: 806-822 us, 2.34-2.39 PFLOP/s, matrix cores busy
-// 56 % of the cycles at 2.0 GHz.  Timing copies: without the loads 615 us
-// (the clock falls to 1.77 GHz: power), with every load hitting L2 740-770 us
-// at 1.62 GHz, with zeros as data 434 us at 2.4 GHz.  So what remains above
-// the power limit is the L2 misses' share, under 10 %; a fifth slot of the
-// ring (160 KB) gained nothing.
+// A 128-byte line holds two half-stages of a row.  Asked for one at a time,
+// half a microsecond apart, it came from L2 twice (the rows of a pair of
+// half-stages are twice the L1); so the loads of a pair go out together, the
+// two halves of a line one behind the other, in four equal parts over the
+// pair's four slices.  At 4096 x 8192 x 28672 one half-stage at a time took
+// 846 us, pairs 784 us with the loads in two bursts, 721 in three, 704 in
+// four equal parts (2.73 PFLOP/s); 4096 x 4096 x 4096: 64 to 62 us, 333 x
+// 32003 x 4096 (J = 3): 59.7 to 53.3 us.  A ring of whole 128-byte stages,
+// two deep (all that fits), took 876 us: its loads are short of time.
+//
+// What bounds the largest: power.  Timing copies of the kernel with four
+// single half-stages: without the loads 615 us (the clock falls to 1.77 GHz),
+// with zeros as data 434 us at 2.4 GHz.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "q8_common.hpp"
@@ -35,16 +43,12 @@ constexpr int kTN = 256;    // channels per tile
 constexpr int kHalf = 64;   // bytes of K per half-stage
 constexpr int kWBytes = kTN * kHalf;
 
-// Waits until at most two half-stages of this wave's loads (4 + J each) are
-// in flight and its LDS reads are done, then meets the other waves.  One asm
-// block: a fence would wait for every direct-to-LDS load in flight.
-template <int J>
-__device__ __forceinline__ void half_barrier() {
-  static_assert(J >= 1 && J <= 4, "one wait for each");
-  if constexpr (J == 1) __asm__ volatile("s_waitcnt vmcnt(10) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  if constexpr (J == 2) __asm__ volatile("s_waitcnt vmcnt(12) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  if constexpr (J == 3) __asm__ volatile("s_waitcnt vmcnt(14) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  if constexpr (J == 4) __asm__ volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// Waits until at most N of this wave's loads are in flight and its LDS reads
+// are done, then meets the other waves.  One asm block: a fence would wait
+// for every direct-to-LDS load in flight.
+template <int N>
+__device__ __forceinline__ void ring_barrier() {
+  __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // Fragments of one 32-byte slice of K: lane (l, h) holds bytes 16 h .. of row
@@ -63,9 +67,11 @@ __device__ __forceinline__ void read_frags(const uint8_t* slot, uint32_t woff, u
 }
 
 // Order of a slice's instructions: its 4 + J LDS reads two by two behind the
-// first matrix instructions, then a global load every other one.
+// first matrix instructions, then a global load after every one or two of
+// the next.  Nothing moves from one slice into another.
 template <int J, int LOADS>
 __device__ __forceinline__ void slice_order() {
+  constexpr int kRest = 4 * J - (4 + J) / 2, kEach = kRest >= 2 * LOADS ? 2 : 1;
 #pragma unroll
   for (int i = 0; i < (4 + J) / 2; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
@@ -74,21 +80,44 @@ __device__ __forceinline__ void slice_order() {
   if constexpr (J % 2 == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, J >= 3 ? 2 : 1, 0);
+    if (kEach * i < kRest) __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
     __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
   }
-  constexpr int kLeft = 4 * J - (4 + J) / 2 - LOADS * (J >= 3 ? 2 : 1);
-  if constexpr (kLeft > 0) __builtin_amdgcn_sched_group_barrier(0x008, kLeft, 0);
+  if constexpr (kRest > kEach * LOADS) __builtin_amdgcn_sched_group_barrier(0x008, kRest - kEach * LOADS, 0);
+  __builtin_amdgcn_sched_barrier(0);
 }
+
+// The ring holds R half-stages; the loads of a pair of them (e, e + 1: e
+// even) go out in four equal parts, the first after the barrier of half-stage
+// e + 1 - R, which frees the pair's second slot, the others in the next three
+// slices.
+template <int J>
+struct Ring {
+  static constexpr int kSlots = J == 1 ? 4 : J == 2 ? 6 : 5;                      // what the LDS holds (J = 1: two workgroups)
+  static constexpr int kTurn = kSlots % 2 == 0 ? kSlots : 2 * kSlots;             // half-stages after which slot and parity repeat
+  static constexpr int kPair = 2 * (4 + J);                                       // loads of a pair
+  static constexpr int kA = (kPair + 3) / 4, kB = (kPair + 2) / 4, kC = (kPair + 1) / 4;
+  // loads of pair e that have gone out before the first half-stage
+  static constexpr int before(int e) {
+    const int start = e + 1 - kSlots;
+    return start < -2 ? kPair : start == -2 ? kA + kB + kC : start == -1 ? kA : 0;
+  }
+  static constexpr int kAhead = before(2) + before(4);                            // .. of those, the ones behind pair 0's
+  // loads in flight behind pair e's at the barrier of half-stage e - 1
+  static constexpr int kBehind = (kSlots - 4) / 2 * kPair + (kSlots % 2 != 0 ? kA + kB : 0);
+};
 
 template <int J>
 __global__ __launch_bounds__(256, 1) void k_w8a8_gemm(W8A8Args a) {
-  constexpr int kTM = 64 * J, kLoads = 4 + J, kSlot = kWBytes + kTM * kHalf;
-  // one array per slot: a read of one is not held for loads into another
+  constexpr int kTM = 64 * J, R = Ring<J>::kSlots, kSlot = kWBytes + kTM * kHalf;
+  // one array per slot (those that the ring does not have are never named, so
+  // take no room): a read of one is not held for loads into another
   __shared__ __attribute__((aligned(16))) uint8_t s0[kSlot];
   __shared__ __attribute__((aligned(16))) uint8_t s1[kSlot];
   __shared__ __attribute__((aligned(16))) uint8_t s2[kSlot];
   __shared__ __attribute__((aligned(16))) uint8_t s3[kSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t s4[kSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t s5[kSlot];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -102,29 +131,33 @@ __global__ __launch_bounds__(256, 1) void k_w8a8_gemm(W8A8Args a) {
   int tm, tn;
   grouped_tile(tile, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = static_cast<int64_t>(tm) * kTM, n0 = static_cast<int64_t>(tn) * kTN;
-  const int all = static_cast<int>((K + kHalf - 1) / kHalf), per = (all + S - 1) / S;
+  const int all = static_cast<int>((K + kHalf - 1) / kHalf), per = ((all + S - 1) / S + 1) & ~1;
   const int h_begin = share * per < all ? share * per : all, h_end = h_begin + per < all ? h_begin + per : all;
 
   // Loads: instruction i of wave w fills rows 16 (4 i + w) .. +15 of an
   // operand, four 16-byte pieces a row; piece c of row r sits at
   // c ^ ((r / 4) % 4), which puts one piece of 16 consecutive rows in 16
   // distinct bank groups.  Rows past the matrix lie outside the resource and
-  // read as zero, pieces past K get an offset outside it, half-stages past
-  // the share an empty resource.
+  // read as zero; pieces past K and half-stages past the share get an offset
+  // outside it.
   const int64_t xrows = M - m0 < kTM ? M - m0 : kTM, wrows = N - n0 < kTN ? N - n0 : kTN;
   const rsrc_t xr = uniform_rsrc(a.xq + m0 * K, static_cast<uint32_t>(xrows * K));
   const rsrc_t wr = uniform_rsrc(a.wq + n0 * K, static_cast<uint32_t>(wrows * K));
-  const rsrc_t none = uniform_rsrc(a.xq, 0u);
   const int piece = (lane & 3) ^ ((lane >> 4) & 3);
   const uint32_t voff = static_cast<uint32_t>((wave * 16 + (lane >> 2)) * K + piece * 16);
   const int tail = static_cast<int>(K % kHalf);
   const uint32_t voff_tail = voff | ((tail != 0 && piece * 16 >= tail) ? 0x80000000u : 0u);
   const int wslot = wave * 1024;
-  auto load = [&](int hs, uint8_t* slot, int i) {  // i < 4: channels, else tokens
-    const rsrc_t r = hs < h_end ? (i < 4 ? wr : xr) : none;
-    const uint32_t vo = hs == all - 1 ? voff_tail : voff;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(slot + i * 4096 + wslot), 16, vo,
-                                             static_cast<int>((i & 3) * 64 * K + hs * kHalf), 0, 0);
+  auto slot = [&](int s) {
+    return s % R == 0 ? s0 : s % R == 1 ? s1 : s % R == 2 ? s2 : s % R == 3 ? s3 : s % R == 4 ? s4 : s5;
+  };
+  // load i of the pair of half-stages hs, hs + 1: both halves of a row
+  // group's 128-byte lines one behind the other; row groups < 4 are channels
+  auto load = [&](int hs, int s, int i) {
+    const int half = i & 1, row = i >> 1;
+    const uint32_t vo = hs + half >= h_end ? 0x80000000u : hs + half == all - 1 ? voff_tail : voff;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(row < 4 ? wr : xr, (lds_ptr_t)(slot(s + half) + row * 4096 + wslot), 16, vo,
+                                             static_cast<int>((row & 3) * 64 * K + (hs + half) * kHalf), 0, 0);
   };
 
   // fragment offsets of the half-stage's two slices
@@ -145,41 +178,57 @@ __global__ __launch_bounds__(256, 1) void k_w8a8_gemm(W8A8Args a) {
       for (int j = 0; j < J; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[i], f.x[j], acc[i][j], 0, 0, 0);
   };
 
-  // The loads of the half-stage four on go out in two parts: four after the
-  // barrier that frees the slot, the rest in the first slice of the next
-  // half-stage (an even stream: 2 % over all of them after the barrier).
+  using G = Ring<J>;
   Frags<J> f0, f1;
 #pragma unroll
-  for (int st = 0; st < 4; ++st)
+  for (int e = 0; e < R; e += 2)
 #pragma unroll
-    for (int i = 0; i < (st == 3 ? 4 : kLoads); ++i)
-      load(h_begin + st, st == 0 ? s0 : st == 1 ? s1 : st == 2 ? s2 : s3, i);
-  if constexpr (J == 1) __asm__ volatile("s_waitcnt vmcnt(14)\n\ts_barrier" ::: "memory");
-  if constexpr (J == 2) __asm__ volatile("s_waitcnt vmcnt(16)\n\ts_barrier" ::: "memory");
-  if constexpr (J == 3) __asm__ volatile("s_waitcnt vmcnt(18)\n\ts_barrier" ::: "memory");
-  if constexpr (J == 4) __asm__ volatile("s_waitcnt vmcnt(20)\n\ts_barrier" ::: "memory");
+    for (int i = 0; i < G::before(e); ++i) load(h_begin + e, e, i);
+  __asm__ volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(G::kAhead) : "memory");
   read_frags<J>(s0, wrow + c0, xrow + c0, f0);
 
-  // whole turns of the ring: half-stages past the share hold zeros
-  for (int hs0 = h_begin; hs0 < h_end; hs0 += 4) {
+  int hs0 = h_begin;
+  auto turn = [&](auto last) __attribute__((always_inline)) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      uint8_t* const cur = p == 0 ? s0 : p == 1 ? s1 : p == 2 ? s2 : s3;
-      uint8_t* const prv = p == 0 ? s3 : p == 1 ? s0 : p == 2 ? s1 : s2;
-      const uint8_t* const nxt = p == 0 ? s1 : p == 1 ? s2 : p == 2 ? s3 : s0;
-      read_frags<J>(cur, wrow + c1, xrow + c1, f1);
+    for (int p = 0; p < G::kTurn; ++p) {
+      if (decltype(last)::value && p % 2 == 0 && hs0 + p >= h_end) return;
+      const bool starts = ((p + R) & 1) != 0;  // this half-stage's barrier frees a pair of slots
+      read_frags<J>(slot(p), wrow + c1, xrow + c1, f1);
+      if (starts) {
 #pragma unroll
-      for (int i = 4; i < kLoads; ++i) load(hs0 + p + 3, prv, i);
+        for (int i = G::kA + G::kB + G::kC; i < G::kPair; ++i) load(hs0 + p + R - 3, p + R - 3, i);
+      } else {
+#pragma unroll
+        for (int i = G::kA; i < G::kA + G::kB; ++i) load(hs0 + p + R - 2, p + R - 2, i);
+      }
       mfmas(f0);
-      slice_order<J, J>();
-      half_barrier<J>();
+      if (starts)
+        slice_order<J, G::kPair - G::kA - G::kB - G::kC>();
+      else
+        slice_order<J, G::kB>();
+      if (p % 2 != 0)
+        ring_barrier<G::kBehind>();
+      else
+        ring_barrier<63>();  // the next half-stage has landed with this one
+      read_frags<J>(slot(p + 1), wrow + c0, xrow + c0, f0);
+      if (starts) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load(hs0 + p + 4, cur, i);
-      read_frags<J>(nxt, wrow + c0, xrow + c0, f0);
+        for (int i = 0; i < G::kA; ++i) load(hs0 + p + R - 1, p + R - 1, i);
+      } else {
+#pragma unroll
+        for (int i = G::kA + G::kB; i < G::kA + G::kB + G::kC; ++i) load(hs0 + p + R - 2, p + R - 2, i);
+      }
       mfmas(f1);
-      slice_order<J, 4>();
+      if (starts)
+        slice_order<J, G::kA>();
+      else
+        slice_order<J, G::kC>();
     }
-  }
+  };
+  // whole turns of the ring, then the pairs that are left (an exit inside the
+  // loop would move the sums about in it)
+  for (; hs0 + G::kTurn <= h_end; hs0 += G::kTurn) turn(std::false_type{});
+  turn(std::true_type{});
   __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   const int64_t mw = m0 + wm * 32 * J, nw = n0 + wn * 128;
@@ -284,19 +333,22 @@ __global__ __launch_bounds__(256) void k_w8a8_join(W8A8Args a) {
 
 int64_t w8a8_gemm_tiles(int64_t M, int64_t N, int j) { return (M + 64 * j - 1) / (64 * j) * ((N + kTN - 1) / kTN); }
 
-// Tile height and shares of K by estimated time, from what the kernel
-// measured: a half-stage of a lone workgroup takes 0.53, 0.59, 0.63, 0.67 us
-// (J = 1 .. 4: the ring's depth over the memory's latency), of a full card
-// 0.85 (two workgroups a unit, J = 1 only), 0.62, 0.725, 0.917 us; the
-// weights stream at 4.6 TB/s at best; joining shares costs a launch and 8
-// bytes per output and share at 3.5 TB/s.  (128 x 8192 x 28672: J = 2 in 8
-// shares 62 us, against 79 for J = 1 in 4 and 301 for J = 4 in one; 333 x
-// 32003 x 4096: J = 3 57 us, against 60 for J = 4.)
+// Tile height and shares of K by estimated time.  The constants were fitted
+// to every allowed shape at 53 sizes (65 .. 4096 tokens, 512 .. 32003
+// channels, K 1024 .. 28672): a half-stage of a lone workgroup takes 0.45,
+// 0.52, 0.52, 0.70 us (J = 1 .. 4: the ring's depth over the memory's
+// latency), of a full card 0.66 (two workgroups a unit, J = 1 only), 0.50,
+// 0.60, 0.79 us, start and end of a tile eight half-stages; the operands
+// stream at 4.4 TB/s at best; joining shares costs a launch and 8 bytes per
+// output and share at 3.5 TB/s.  Its picks were 1.6 % off the fastest on
+// average, 12 % at worst.  (128 x 8192 x 28672: J = 2 in 8 shares 61 us, in 6
+// 68, J = 1 in 4 89, J = 4 in one 272; 333 x 32003 x 4096: J = 3 53 us, J = 4
+// 60, J = 2 74.)
 W8A8Shape w8a8_gemm_shape(int64_t M, int64_t N, int64_t K) {
-  static const double kLone[4] = {0.53, 0.59, 0.63, 0.67}, kFull[4] = {0.85, 0.62, 0.725, 0.917};
+  static const double kLone[4] = {0.45, 0.52, 0.52, 0.70}, kFull[4] = {0.66, 0.50, 0.60, 0.79};
   static const int kShares[] = {1, 2, 3, 4, 6, 8, 12, 16};
   const int64_t halves = (K + kHalf - 1) / kHalf;
-  const double stream = static_cast<double>(K) * static_cast<double>(M + N) / 4.6e6;
+  const double stream = static_cast<double>(K) * static_cast<double>(M + N) / 4.4e6;
   W8A8Shape best;
   double best_t = 0.0;
   for (int j = 4; j >= 1; --j) {
@@ -306,7 +358,7 @@ W8A8Shape w8a8_gemm_shape(int64_t M, int64_t N, int64_t K) {
       const double fill = tiles * s < slots ? static_cast<double>(tiles * s) / static_cast<double>(slots) : 1.0;
       const double half = kLone[j - 1] + (kFull[j - 1] - kLone[j - 1]) * fill;
       const double rounds = static_cast<double>((tiles * s + slots - 1) / slots);
-      double t = rounds * static_cast<double>((halves + s - 1) / s + 6) * half;
+      double t = rounds * static_cast<double>((halves + s - 1) / s + 8) * half;
       if (t < stream) t = stream;
       if (s > 1) t += 4.0 + 8.0 * static_cast<double>(M) * static_cast<double>(N) * s / 3.5e6;
       if (best_t == 0.0 || t < best_t) {
