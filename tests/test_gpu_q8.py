@@ -274,6 +274,23 @@ def test_product(qb, M, N, K):
     assert torch.equal(qb.qlin_w8a8_fwd(x, w), y)
 
 
+@pytest.mark.parametrize("M,N", [(100, 300), (1000, 4096), (700, 11008), (2048, 8192)])
+def test_product_depths(qb, M, N):
+    """Every remainder of the depth over the turn of the ring that the operands stream through, at each tile height
+    (64, 128, 192, 256 rows), and lengths that end inside a step; at (100, 300) also depths in several shares."""
+    import torch
+    print(f"[w8a8 depths] {M}x{N}", flush=True)
+    rng = np.random.default_rng(M)
+    K0 = 3504
+    xq, wq = (torch.from_numpy(codes_of(rng, n, K0)).cuda() for n in (M, N))
+    xs, ws = (to_dev_f32(rng.uniform(0.5, 2, n).astype(np.float32) * np.float32(0.01)) for n in (M, N))
+    for K in [64 * h + 16 * (h % 4) for h in range(1, 22)] + ([K0] if M > 100 else list(range(1392, K0 + 1, 176))):
+        x, w = qb.Q8Rows(xq[:, :K].contiguous(), xs), qb.Q8Rows(wq[:, :K].contiguous(), ws)
+        got = qb.qlin_w8a8_fwd(x, w).double()
+        ref = (x.codes.double() @ w.codes.double().t().contiguous()) * xs.double()[:, None] * ws.double()[None]
+        assert bool(((got - ref).abs() <= ref.abs() * (BF + 4 * U)).all()), K
+
+
 def test_product_extreme_codes(qb):
     """Every code at the format's ends: the integer sum is exact in int32."""
     for M, N in ((3, 70), (260, 270)):
