@@ -6,12 +6,15 @@
 // chunks of kChunk bytes.  The chunk of all token rows is copied to LDS (two
 // buffers, direct-to-LDS loads one chunk ahead): read from cache by every
 // wave, the token operands cost as many load instructions as the weights (16
-// tokens by 8192 x 28672: 59 us, against 46 through LDS).  Each wave takes a
+// tokens by 8192 x 28672: 54 us, against 50 through LDS).  Each wave takes a
 // contiguous eighth of the chunk for all rows, in 64-byte slices: a weight
-// operand is 16 bytes from 16 g of row r for lane (r, g), loaded two chunks
-// ahead into a register ring.  The waves' int32 sums meet in LDS (integer
-// addition: any order gives the same sum); shares of K publish theirs and the
-// last workgroup of a tile (atomic ticket) adds them.
+// operand is 16 bytes from 16 g of row r for lane (r, g).  The weights of two
+// slices are loaded together, two chunks ahead into a register ring, so that
+// both halves of a 128-byte line are asked for one behind the other (slice by
+// slice the line came from L2 twice: 52.6 against 49.0 us, 4.8 TB/s).  The
+// waves' int32 sums meet in LDS (integer addition: any order gives the same
+// sum); shares of K publish theirs and the last workgroup of a tile (atomic
+// ticket) adds them.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "q8_common.hpp"
@@ -33,6 +36,7 @@ template <int RT, int MT>
 __global__ __launch_bounds__(64 * kFewWaves, 2) void k_w8a8_few(W8A8Args a) {
   constexpr int kRows = 16 * RT, kTok = 16 * MT, kChunk = few_chunk(MT);
   constexpr int kSl = kChunk / kSlice / kFewWaves;         // slices per wave and chunk
+  static_assert(kSl % 2 == 0, "whole lines");
   constexpr int kDma = kTok * kChunk / 1024 / kFewWaves;   // token loads per wave and chunk
   // one array per buffer: a read of one is not held for loads into the other
   __shared__ __attribute__((aligned(16))) uint8_t s_x0[kTok * kChunk];
@@ -79,18 +83,22 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void k_w8a8_few(W8A8Args a) {
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[r][m] = i32x4{};
-  auto load_weights = [&](int c, int i, i32x4 (&w)[RT]) {
-    const int k = c * kChunk + i * kSlice;
-    const int so = c < c_end && k + wave * kSl * kSlice < K ? k : 0x7FFFFFFF;
+  // slices i and i + 1 (i even): the halves of a row's 128-byte lines one
+  // behind the other
+  auto load_weights = [&](int c, int i, i32x4 (&w0)[RT], i32x4 (&w1)[RT]) {
+    const int k = c * kChunk + i * kSlice, kw = k + wave * kSl * kSlice;
+    const int so0 = c < c_end && kw < K ? k : 0x7FFFFFFF, so1 = c < c_end && kw + kSlice < K ? k + kSlice : 0x7FFFFFFF;
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-      w[t] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[t], so, 0));
+    for (int t = 0; t < RT; ++t) {
+      w0[t] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[t], so0, 0));
+      w1[t] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[t], so1, 0));
+    }
   };
   load_tokens(c_begin, s_x0);
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int i = 0; i < kSl; ++i) load_weights(c_begin + c, i, wv[c][i]);
+    for (int i = 0; i < kSl; i += 2) load_weights(c_begin + c, i, wv[c][i], wv[c][i + 1]);
   for (int i = tid; i < kTok * (kRows + 4); i += 64 * kFewWaves) (&s_sum[0][0])[i] = 0;
 
   // Chunk c: its token rows and this wave's weights have landed once at most
@@ -121,7 +129,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void k_w8a8_few(W8A8Args a) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
             acc[r][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[p][i][r], xv[m], acc[r][m], 0, 0, 0);
-        load_weights(c + 2, i, wv[p][i]);
+        if (i % 2 != 0) load_weights(c + 2, i - 1, wv[p][i - 1], wv[p][i]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
