@@ -877,7 +877,7 @@ int check_rows(int64_t rows, int64_t d) {
 struct BwdQ8Plan {
   bool dx_stream = false;  // <= 16 tokens: dX streamed
   bool fits = true;
-  int du_splits = 1, dB_splits = 1, dA_splits = 1, ds_splits = 1;
+  int du_splits = 1, dB_splits = 1, dA_splits = 1, ds_splits = 1, dx_shares = 1;
   int64_t dB_counters = 0;  // dB's and dA's tickets are taken in one launch: dA's follow dB's
   size_t off_du = 0, off_zu = 0, off_zdu = 0, off_At = 0, off_partial = 0, off_partial_dA = 0, off_tc = 0, total = 0;
 };
@@ -892,6 +892,7 @@ BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t 
   const int fmt = fmt_of(w);
   p.dx_stream = M <= kSmallM && dx_stream_fits(N, K, fmt);
   p.ds_splits = dx_stream_splits(N, K, fmt);
+  p.dx_shares = p.dx_stream ? 1 : dx_gemm_shares(M, N, K);
   p.du_splits = du_splits(M, N);
   p.dB_splits = tokens_splits(M, N, r);
   p.dA_splits = tokens_splits(M, K, r);
@@ -901,7 +902,8 @@ BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t 
                                               p.dx_stream && p.ds_splits > 1 ? dx_stream_panels(K) : 0});
   p.fits = counters <= kCounterWords && M <= kMaxBwdTokens && N < (int64_t{1} << 24) && K < (int64_t{1} << 24);
   const int64_t partial = std::max<int64_t>({du_partial_floats(M, N, r), tokens_partial_floats(M, N, r),
-                                             p.dx_stream ? dx_stream_partial_floats(N, K, fmt) : 0});
+                                             p.dx_stream ? dx_stream_partial_floats(N, K, fmt) : 0,
+                                             p.dx_shares > 1 ? p.dx_shares * M * K : 0});
   size_t off = kCounterBytes;
   p.off_du = off;         off = align256(off + static_cast<size_t>(M) * r * sizeof(float));
   p.off_zu = off;         off = align256(off + static_cast<size_t>(plane_bytes(M, r)));
@@ -1094,6 +1096,9 @@ int qlin_bwd_q8(const qlin_qweight* w, const int8_t* xq, const float* x_scale, i
   QLIN_TRY(hooked("k_transpose16", stream, [&] { return launch_transpose16(A, r, G, At, stream); }));
   DxArgs a{};
   a.w = v; a.dy = dy; a.M = M; a.At = At; a.du = du; a.r = r; a.pool = pool; a.pool_shift = pool_shift; a.dx = dx;
+  a.splits = p.dx_shares; a.partial = partial;
+  if (a.splits > 1)
+    return hip_status(hooked("k_dx_gemm", stream, [&] { return launch_dx_gemm_shares(a, fmt, stream); }));
   return hip_status(hooked("k_dx_gemm", stream, [&] { return launch_dx_gemm(a, fmt, stream); }));
 }
 

@@ -79,7 +79,10 @@ struct RowParams<kFmtINT4> {
 template <>
 struct RowParams<kFmtNFG> : RowParams<kFmtINT4> {};  // the same group words
 
-template <int FMT>
+// SHARES: a workgroup takes one of a.splits shares of the reduction (whole
+// pairs of steps) and leaves fp32 sums [share][M][K] for k_dx_join; the first
+// share holds the adapter's term.
+template <int FMT, bool SHARES = false>
 __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   // decoded-weight stages (2 x 32 KB), dY half-stages (4 x 16 KB) and code
   // stages (2 x 8 KB), each an array of its own so that a read of one is
@@ -104,14 +107,27 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   const int tiles_k = static_cast<int>((K + kTK - 1) / kTK);
   // tiles in 4 x 8 blocks per XCD (4 token tiles sharing their dY rows, 8
   // column tiles sharing their packed weight columns)
-  int tm, tk;
-  grouped_tile(xcd_round_order(static_cast<int>(blockIdx.x), tiles_m * tiles_k), tiles_m, tiles_k, tm, tk);
+  int tm, tk, share = 0;
+  if constexpr (SHARES) {
+    const int work = xcd_round_order(static_cast<int>(blockIdx.x), tiles_m * tiles_k * a.splits);
+    share = __builtin_amdgcn_readfirstlane(work / (tiles_m * tiles_k));
+    grouped_tile(work % (tiles_m * tiles_k), tiles_m, tiles_k, tm, tk);
+  } else {
+    grouped_tile(xcd_round_order(static_cast<int>(blockIdx.x), tiles_m * tiles_k), tiles_m, tiles_k, tm, tk);
+  }
   tm = __builtin_amdgcn_readfirstlane(tm);
   tk = __builtin_amdgcn_readfirstlane(tk);
   const int64_t m0 = static_cast<int64_t>(tm) * kTMx, k0 = static_cast<int64_t>(tk) * kTK;
-  // whole pairs of steps (a step past the last one meets weight rows past N,
-  // which decode to zero)
-  const int64_t nsteps = (N + kNS - 1) / kNS;
+  // this workgroup's rows of the weight: n_begin .. n_begin + Ns - 1
+  int64_t n_begin = 0, Ns = N;
+  if constexpr (SHARES) {
+    const int64_t pairs = (N + 2 * kNS - 1) / (2 * kNS), n_end = (share + 1) * pairs / a.splits * (2 * kNS);
+    n_begin = share * pairs / a.splits * (2 * kNS);
+    Ns = (n_end < N ? n_end : N) - n_begin;
+  }
+  // whole pairs of steps (a step past the last one meets dY values that load
+  // as zero)
+  const int64_t nsteps = (Ns + kNS - 1) / kNS;
   const int64_t npairs = (nsteps + 1) >> 1;
 
   // this wave's 64 columns (clamped into the matrix; masked when past K)
@@ -140,10 +156,10 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   // token's dX through the zero weights there.
   const int64_t dy_rows = M - m0 < kTMx ? M - m0 : kTMx;
   const rsrc_t dyr = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint16_t*>(a.dy + m0 * N), 0, static_cast<int>(dy_rows * N * 2), 0x00020000);
+      const_cast<uint16_t*>(a.dy + m0 * N + n_begin), 0, static_cast<int>((dy_rows * N - n_begin) * 2), 0x00020000);
   const int dpiece = (lane & 3) ^ ((lane >> 4) & 3);  // source piece of this lane
   const uint32_t dyvoff = static_cast<uint32_t>((wave * 16 + (lane >> 2)) * N * 2 + (dpiece << 4));
-  const int n_tail = static_cast<int>(N % kNS);  // valid rows of the last step (0: all)
+  const int n_tail = static_cast<int>(Ns % kNS);  // valid rows of the last step (0: all)
   // lane offsets of the last step's two parts (pieces past N out of range)
   uint32_t dyvoff_tail[2];
 #pragma unroll
@@ -171,8 +187,8 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   // loads, each instruction 8 whole rows (wave w: rows 16 w .. 16 w + 15),
   // 16-byte chunk c of row r at c ^ ((r / 2) % 8).  Rows past N fall outside
   // the resource; columns past K meet masked tables.
-  const rsrc_t cr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w.codes), 0,
-                                                      static_cast<int>(N * (K >> 1)), 0x00020000);
+  const rsrc_t cr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w.codes) + n_begin * (K >> 1), 0,
+                                                      static_cast<int>(Ns * (K >> 1)), 0x00020000);
   uint32_t cvoff[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -205,11 +221,11 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
     pr0 = uniform_rsrc(a.w.absmax, static_cast<uint32_t>(a.w.dq ? nblk : 4 * nblk));
     pr1 = uniform_rsrc(a.w.dq ? static_cast<const void*>(a.w.absmax2) : a.w.absmax,
                        static_cast<uint32_t>(a.w.dq ? 4 * ((nblk + 255) >> 8) : 4 * nblk));
-    plane = static_cast<uint32_t>(lane * (K >> 6) + (kwc >> 6));
+    plane = static_cast<uint32_t>((lane + n_begin) * (K >> 6) + (kwc >> 6));
   } else {
     pr0 = uniform_rsrc(a.w.scale, static_cast<uint32_t>(4 * nblk));
     pr1 = uniform_rsrc(a.w.zero, static_cast<uint32_t>(4 * nblk));
-    plane = static_cast<uint32_t>((lane * (K >> 5) + (kwc >> 5)) * 2);
+    plane = static_cast<uint32_t>(((lane + n_begin) * (K >> 5) + (kwc >> 5)) * 2);
   }
   const uint32_t pshift = a.w.dq ? 8u : 0u;
   // (the 8-bit code comes from the aligned word that holds it: a byte load
@@ -239,7 +255,7 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   // constants (their offsets lie past the constant arrays) and so get
   // all-zero tables; INT4 tables of such rows are masked.
   auto build_lut_part = [&](int set, const RowParams<FMT>& rc, int64_t st, int part) {
-    const bool valid = FMT == kFmtNF4 || st * kNS + lane < N;
+    const bool valid = FMT == kFmtNF4 || st * kNS + lane < Ns;
     if constexpr (FMT == kFmtNF4) {
       if (part == 0) lscale[set] = nf4_params_scale_sel(a.w, BlockParams{(rc.bp.a >> rc.sh) & 0xFFu, rc.bp.b}, valid);
       const float sc = lscale[set];
@@ -447,7 +463,7 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   // columns at a time (rows padded by 16 B against bank conflicts), every
   // load of a chunk in flight at once.  Indices are clamped and values
   // masked (no divergent branches around loads).
-  if (a.du != nullptr && a.At != nullptr && a.r > 0) {
+  if (a.du != nullptr && a.At != nullptr && a.r > 0 && share == 0) {
     const int rr = a.r;
     constexpr int kJC = 48;          // adapter columns per staged chunk
     constexpr int rp = kJC + 8;      // staged row length (elements): 28 KB per operand
@@ -522,6 +538,24 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
     }
   }
 
+  if constexpr (SHARES) {
+    float* const part = a.partial + share * M * K;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t m = m0 + 128 * wm + 32 * j + l32;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t k = k0 + 128 * wk + 32 * i + 8 * q + 4 * h;
+          if (m < M && k < K)
+            *reinterpret_cast<f32x4*>(part + m * K + k) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        }
+    }
+    return;
+  }
+
   // store: lane holds D[k = 8q + 4h + t][m = l32] of each 32x32 tile, i.e.
   // 8 bytes of 32 different output rows per instruction.  The bf16 tile goes
   // through LDS instead (512 B per token: tokens 0-63 in s_w0, 64-127 in
@@ -563,10 +597,66 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   }
 }
 
+// dX from the shares' sums, added in share order: eight columns a thread.
+__global__ __launch_bounds__(256) void k_dx_join(DxArgs a) {
+  const int64_t n = a.M * a.w.K, at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (at >= n) return;
+  f32x4 t[2] = {};
+#pragma unroll 4
+  for (int sp = 0; sp < a.splits; ++sp) {
+    const f32x4* const p = reinterpret_cast<const f32x4*>(a.partial + sp * n + at);
+    t[0] += p[0];
+    t[1] += p[1];
+  }
+  *reinterpret_cast<u32x4*>(a.dx + at) = u32x4{pack_bf16x2(t[0][0], t[0][1]), pack_bf16x2(t[0][2], t[0][3]),
+                                               pack_bf16x2(t[1][0], t[1][1]), pack_bf16x2(t[1][2], t[1][3])};
+}
+
+int dx_gemm_tiles(int64_t M, int64_t K) { return static_cast<int>(((M + kTMx - 1) / kTMx) * ((K + kTK - 1) / kTK)); }
+
 }  // namespace
 
+// Shares of the reduction for few tiles, in one round of workgroups, by
+// estimated time: a pair of steps takes 3.0 us, start and end of a workgroup
+// three pairs, the join a launch and 8 bytes per output and share at 6 TB/s
+// (they mostly stay in the caches).  INT4, one share and the chosen: 100 x
+// 4096 x 4096 103 and 31 us, 512 x 4096 x 4096 106 and 47, 100 x 11008 x 4096
+// 265 and 41, 512 x 28672 x 1024 654 and 59; 300 x 8192 x 28672 stays at one
+// (210, against 244 in two).
+int dx_gemm_shares(int64_t M, int64_t N, int64_t K) {
+  static const int kShares[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+  const int64_t pairs = (N + 2 * kNS - 1) / (2 * kNS);
+  const int64_t tiles = (M + kTMx - 1) / kTMx * ((K + kTK - 1) / kTK);
+  int best = 1;
+  double best_t = 0.0;
+  for (int s : kShares) {
+    if (s > 1 && (tiles * s > 256 || pairs < 2 * s)) break;
+    double t = static_cast<double>((pairs + s - 1) / s + 3) * 3.0;
+    if (s > 1) t += 4.0 + 8.0 * static_cast<double>(M) * static_cast<double>(K) * s / 6.0e6;
+    if (s == 1 || t < best_t) {
+      best_t = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+hipError_t launch_dx_gemm_shares(const DxArgs& a, int fmt, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(dx_gemm_tiles(a.M, a.w.K) * a.splits)), block(256);
+  if (fmt == kFmtNF4)
+    hipLaunchKernelGGL((k_dx_gemm<kFmtNF4, true>), grid, block, 0, stream, a);
+  else if (fmt == kFmtINT4)
+    hipLaunchKernelGGL((k_dx_gemm<kFmtINT4, true>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_dx_gemm<kFmtNFG, true>), grid, block, 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_dx_join, dim3(static_cast<uint32_t>((a.M * a.w.K / 8 + 255) / 256)), block, 0, stream, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_dx_gemm(const DxArgs& a, int fmt, hipStream_t stream) {
-  const int grid = static_cast<int>(((a.M + kTMx - 1) / kTMx) * ((a.w.K + kTK - 1) / kTK));
+  const int grid = dx_gemm_tiles(a.M, a.w.K);
   if (fmt == kFmtNF4)
     hipLaunchKernelGGL(k_dx_gemm<kFmtNF4>, dim3(grid), dim3(256), 0, stream, a);
   else if (fmt == kFmtINT4)

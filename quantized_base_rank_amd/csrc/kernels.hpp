@@ -251,8 +251,13 @@ struct DxArgs {
   int32_t pool;        // power of two
   int32_t pool_shift;  // log2(pool)
   uint16_t* dx;        // [M][K]
+  int32_t splits;      // launch_dx_gemm_shares: shares of the reduction,
+  float* partial;      // their sums [splits][M][K]
 };
 hipError_t launch_dx_gemm(const DxArgs& a, int fmt, hipStream_t stream);
+// The same in shares (of at least one), joined by a second launch.
+int dx_gemm_shares(int64_t M, int64_t N, int64_t K);
+hipError_t launch_dx_gemm_shares(const DxArgs& a, int fmt, hipStream_t stream);
 
 // Few-token (M <= 16) weight-streaming kernels, one launch per pass; the
 // adapter terms are folded into the split reductions.

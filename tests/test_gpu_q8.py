@@ -395,6 +395,35 @@ def test_backward_from_checkpoint(qb, oracle, fmt, M, N, K, r, pool):
     assert none is None and torch.equal(dA, dA2) and torch.equal(dB, dB2)
 
 
+@pytest.mark.parametrize("fmt,M,N,K,pool", [("int4", 17, 4096, 320, 32), ("nf4", 100, 2064, 576, 1), ("nf4", 257, 1168, 256, 1),
+                                            ("int4", 300, 720, 128, 1), ("nf4", 40, 11008, 64, 1), ("nf4", 33, 272, 4160, 1)])
+def test_backward_input_gradient_in_shares(qb, oracle, fmt, M, N, K, pool):
+    """dX of few tiles: the sum over the output features split between workgroups, last shares that end inside a
+    step, and a non-finite dY row that stays in its token; the same bits from run to run."""
+    import torch
+    print(f"[bwd q8 shares] {fmt} M={M} {N}x{K}", flush=True)
+    rng = np.random.default_rng(M + N + K)
+    r = 12
+    w, Wd = (int4_weight if fmt == "int4" else nf4_weight)(qb, oracle, rng, N, K)
+    xv = Q.rows_values(*Q.quantize_rows(val(bf16(rng.standard_normal((M, K))))))
+    q = qb.qlin_quantize_q8(to_dev_bf16(bf16(val(bf16(xv)))))
+    A = val(bf16(rng.uniform(-1, 1, (r, K // pool)) / np.sqrt(K // pool)))
+    B = val(bf16(rng.standard_normal((N, r)) * 0.1))
+    dy = val(bf16(rng.standard_normal((M, N))))
+    u = rng.standard_normal((M, r)).astype(np.float32)
+    args = (to_dev_bf16(bf16(A)), to_dev_bf16(bf16(B)), r, 2.0, to_dev_bf16(bf16(dy)), to_dev_f32(u))
+    dx, _, _ = qb.qlin_bwd_q8(w, q, *args, pool=pool)
+    du = 2.0 * (dy.astype(np.float64) @ B)
+    ref = dy.astype(np.float64) @ Wd + np.repeat(du @ A.astype(np.float64), pool, axis=1)
+    parity.check({"dX": (val(bf16_host_bits(dx)), ref)})
+    assert torch.equal(qb.qlin_bwd_q8(w, q, *args, pool=pool)[0], dx)
+    bad = dy.copy()
+    bad[M // 2, N - 1] = np.inf
+    dxb, _, _ = qb.qlin_bwd_q8(w, q, args[0], args[1], r, 2.0, to_dev_bf16(bf16(bad)), args[5], pool=pool)
+    keep = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(dxb[keep], dx[keep]) and not bool(torch.isfinite(dxb[M // 2].float()).all())
+
+
 def test_backward_checkpoint_gradient_by_differences(qb, oracle):
     """dA against central differences of <dY, y> in the oracle's forward on
     the checkpoint's values: linear in A, so differences are exact up to
