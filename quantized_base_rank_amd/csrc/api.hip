@@ -903,7 +903,7 @@ BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t 
   p.fits = counters <= kCounterWords && M <= kMaxBwdTokens && N < (int64_t{1} << 24) && K < (int64_t{1} << 24);
   const int64_t partial = std::max<int64_t>({du_partial_floats(M, N, r), tokens_partial_floats(M, N, r),
                                              p.dx_stream ? dx_stream_partial_floats(N, K, fmt) : 0,
-                                             p.dx_shares > 1 ? p.dx_shares * M * K : 0});
+                                             dx_gemm_partial_floats(M, K, p.dx_shares)});
   size_t off = kCounterBytes;
   p.off_du = off;         off = align256(off + static_cast<size_t>(M) * r * sizeof(float));
   p.off_zu = off;         off = align256(off + static_cast<size_t>(plane_bytes(M, r)));
@@ -1097,8 +1097,6 @@ int qlin_bwd_q8(const qlin_qweight* w, const int8_t* xq, const float* x_scale, i
   DxArgs a{};
   a.w = v; a.dy = dy; a.M = M; a.At = At; a.du = du; a.r = r; a.pool = pool; a.pool_shift = pool_shift; a.dx = dx;
   a.splits = p.dx_shares; a.partial = partial;
-  if (a.splits > 1)
-    return hip_status(hooked("k_dx_gemm", stream, [&] { return launch_dx_gemm_shares(a, fmt, stream); }));
   return hip_status(hooked("k_dx_gemm", stream, [&] { return launch_dx_gemm(a, fmt, stream); }));
 }
 

@@ -79,9 +79,10 @@ struct RowParams<kFmtINT4> {
 template <>
 struct RowParams<kFmtNFG> : RowParams<kFmtINT4> {};  // the same group words
 
-// SHARES: a workgroup takes one of a.splits shares of the reduction (whole
-// pairs of steps) and leaves fp32 sums [share][M][K] for k_dx_join; the first
-// share holds the adapter's term.
+// SHARES: the tiles from a.tile0 on, a workgroup taking one of a.splits shares
+// of the reduction (whole pairs of steps); it leaves its tile's fp32 sums
+// [share][tile][256 tokens][256 columns] for k_dx_join, the first share with
+// the adapter's term.
 template <int FMT, bool SHARES = false>
 __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   // decoded-weight stages (2 x 32 KB), dY half-stages (4 x 16 KB) and code
@@ -107,11 +108,13 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   const int tiles_k = static_cast<int>((K + kTK - 1) / kTK);
   // tiles in 4 x 8 blocks per XCD (4 token tiles sharing their dY rows, 8
   // column tiles sharing their packed weight columns)
-  int tm, tk, share = 0;
+  int tm, tk, share = 0, part_tile = 0;
   if constexpr (SHARES) {
-    const int work = xcd_round_order(static_cast<int>(blockIdx.x), tiles_m * tiles_k * a.splits);
-    share = __builtin_amdgcn_readfirstlane(work / (tiles_m * tiles_k));
-    grouped_tile(work % (tiles_m * tiles_k), tiles_m, tiles_k, tm, tk);
+    const int tiles = tiles_m * tiles_k - a.tile0;
+    const int work = xcd_round_order(static_cast<int>(blockIdx.x), tiles * a.splits);
+    share = __builtin_amdgcn_readfirstlane(work / tiles);
+    grouped_tile(a.tile0 + work % tiles, tiles_m, tiles_k, tm, tk);
+    part_tile = work;
   } else {
     grouped_tile(xcd_round_order(static_cast<int>(blockIdx.x), tiles_m * tiles_k), tiles_m, tiles_k, tm, tk);
   }
@@ -539,17 +542,17 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   }
 
   if constexpr (SHARES) {
-    float* const part = a.partial + share * M * K;
+    float* const part = a.partial + static_cast<int64_t>(part_tile) * (kTMx * kTK);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + 128 * wm + 32 * j + l32;
+      const int row = 128 * wm + 32 * j + l32;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int64_t k = k0 + 128 * wk + 32 * i + 8 * q + 4 * h;
-          if (m < M && k < K)
-            *reinterpret_cast<f32x4*>(part + m * K + k) =
+          const int col = 128 * wk + 32 * i + 8 * q + 4 * h;
+          if (m0 + row < M && k0 + col < K)
+            *reinterpret_cast<f32x4*>(part + row * kTK + col) =
                 f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         }
     }
@@ -597,42 +600,51 @@ __global__ __launch_bounds__(256, 1) void k_dx_gemm(DxArgs a) {
   }
 }
 
-// dX from the shares' sums, added in share order: eight columns a thread.
+// dX of the tiles from a.tile0 on from the shares' sums, added in share
+// order: 32 workgroups a tile, eight columns a thread.
 __global__ __launch_bounds__(256) void k_dx_join(DxArgs a) {
-  const int64_t n = a.M * a.w.K, at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (at >= n) return;
+  const int tiles_m = static_cast<int>((a.M + kTMx - 1) / kTMx), tiles_k = static_cast<int>((a.w.K + kTK - 1) / kTK);
+  const int tile = static_cast<int>(blockIdx.x >> 5);
+  int tm, tk;
+  grouped_tile(a.tile0 + tile, tiles_m, tiles_k, tm, tk);
+  const int row = static_cast<int>(blockIdx.x & 31) * 8 + static_cast<int>(threadIdx.x >> 5), col = (threadIdx.x & 31) * 8;
+  const int64_t m = static_cast<int64_t>(tm) * kTMx + row, k = static_cast<int64_t>(tk) * kTK + col;
+  if (m >= a.M || k >= a.w.K) return;
+  const float* const part = a.partial + static_cast<int64_t>(tile) * (kTMx * kTK) + row * kTK + col;
+  const int64_t stride = static_cast<int64_t>(tiles_m * tiles_k - a.tile0) * (kTMx * kTK);
   f32x4 t[2] = {};
 #pragma unroll 4
   for (int sp = 0; sp < a.splits; ++sp) {
-    const f32x4* const p = reinterpret_cast<const f32x4*>(a.partial + sp * n + at);
+    const f32x4* const p = reinterpret_cast<const f32x4*>(part + sp * stride);
     t[0] += p[0];
     t[1] += p[1];
   }
-  *reinterpret_cast<u32x4*>(a.dx + at) = u32x4{pack_bf16x2(t[0][0], t[0][1]), pack_bf16x2(t[0][2], t[0][3]),
-                                               pack_bf16x2(t[1][0], t[1][1]), pack_bf16x2(t[1][2], t[1][3])};
+  *reinterpret_cast<u32x4*>(a.dx + m * a.w.K + k) = u32x4{pack_bf16x2(t[0][0], t[0][1]), pack_bf16x2(t[0][2], t[0][3]),
+                                                          pack_bf16x2(t[1][0], t[1][1]), pack_bf16x2(t[1][2], t[1][3])};
 }
 
-int dx_gemm_tiles(int64_t M, int64_t K) { return static_cast<int>(((M + kTMx - 1) / kTMx) * ((K + kTK - 1) / kTK)); }
+int64_t dx_gemm_tiles(int64_t M, int64_t K) { return ((M + kTMx - 1) / kTMx) * ((K + kTK - 1) / kTK); }
+constexpr int64_t kRound = 256;  // workgroups at once: one a unit
 
 }  // namespace
 
-// Shares of the reduction for few tiles, in one round of workgroups, by
-// estimated time: a pair of steps takes 3.0 us, start and end of a workgroup
-// three pairs, the join a launch and 8 bytes per output and share at 6 TB/s
-// (they mostly stay in the caches).  INT4, one share and the chosen: 100 x
-// 4096 x 4096 103 and 31 us, 512 x 4096 x 4096 106 and 47, 100 x 11008 x 4096
-// 265 and 41, 512 x 28672 x 1024 654 and 59; 300 x 8192 x 28672 stays at one
-// (210, against 244 in two).
+// Shares of the reduction for the tiles that do not fill a round of
+// workgroups (all of them, where there are few), by estimated time: a pair of
+// steps takes 3.0 us, start and end of a workgroup three pairs, the join a
+// launch and 8 bytes per output and share at 6 TB/s (they mostly stay in the
+// caches).  INT4, one share and the chosen: 100 x 4096 x 4096 103 and 31 us,
+// 512 x 4096 x 4096 106 and 47, 100 x 11008 x 4096 265 and 41, 512 x 28672 x
+// 1024 654 and 59; 300 x 8192 x 28672 stays at one (210, against 244 in two).
 int dx_gemm_shares(int64_t M, int64_t N, int64_t K) {
   static const int kShares[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
-  const int64_t pairs = (N + 2 * kNS - 1) / (2 * kNS);
-  const int64_t tiles = (M + kTMx - 1) / kTMx * ((K + kTK - 1) / kTK);
+  const int64_t pairs = (N + 2 * kNS - 1) / (2 * kNS), tiles = dx_gemm_tiles(M, K) % kRound;
+  const double outputs = static_cast<double>(tiles) * kTK * static_cast<double>(M < kTMx ? M : kTMx);
   int best = 1;
   double best_t = 0.0;
   for (int s : kShares) {
-    if (s > 1 && (tiles * s > 256 || pairs < 2 * s)) break;
+    if (s > 1 && (tiles == 0 || tiles * s > kRound || pairs < 2 * s)) break;
     double t = static_cast<double>((pairs + s - 1) / s + 3) * 3.0;
-    if (s > 1) t += 4.0 + 8.0 * static_cast<double>(M) * static_cast<double>(K) * s / 6.0e6;
+    if (s > 1) t += 4.0 + 8.0 * outputs * s / 6.0e6;
     if (s == 1 || t < best_t) {
       best_t = t;
       best = s;
@@ -640,30 +652,33 @@ int dx_gemm_shares(int64_t M, int64_t N, int64_t K) {
   }
   return best;
 }
-
-hipError_t launch_dx_gemm_shares(const DxArgs& a, int fmt, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(dx_gemm_tiles(a.M, a.w.K) * a.splits)), block(256);
-  if (fmt == kFmtNF4)
-    hipLaunchKernelGGL((k_dx_gemm<kFmtNF4, true>), grid, block, 0, stream, a);
-  else if (fmt == kFmtINT4)
-    hipLaunchKernelGGL((k_dx_gemm<kFmtINT4, true>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((k_dx_gemm<kFmtNFG, true>), grid, block, 0, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_dx_join, dim3(static_cast<uint32_t>((a.M * a.w.K / 8 + 255) / 256)), block, 0, stream, a);
-  return hipGetLastError();
+int64_t dx_gemm_partial_floats(int64_t M, int64_t K, int shares) {
+  return shares > 1 ? shares * (dx_gemm_tiles(M, K) % kRound) * kTMx * kTK : 0;
 }
 
-hipError_t launch_dx_gemm(const DxArgs& a, int fmt, hipStream_t stream) {
-  const int grid = dx_gemm_tiles(a.M, a.w.K);
-  if (fmt == kFmtNF4)
-    hipLaunchKernelGGL(k_dx_gemm<kFmtNF4>, dim3(grid), dim3(256), 0, stream, a);
-  else if (fmt == kFmtINT4)
-    hipLaunchKernelGGL(k_dx_gemm<kFmtINT4>, dim3(grid), dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL(k_dx_gemm<kFmtNFG>, dim3(grid), dim3(256), 0, stream, a);
+namespace {
+template <int FMT>
+hipError_t launch_dx_fmt(DxArgs a, hipStream_t stream) {
+  const int tiles = static_cast<int>(dx_gemm_tiles(a.M, a.w.K));
+  a.tile0 = a.splits > 1 ? tiles - tiles % kRound : tiles;
+  const dim3 block(256);
+  if (a.tile0 > 0) {
+    hipLaunchKernelGGL(k_dx_gemm<FMT>, dim3(static_cast<uint32_t>(a.tile0)), block, 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits <= 1) return e;
+  }
+  const int rest = tiles - a.tile0;
+  hipLaunchKernelGGL((k_dx_gemm<FMT, true>), dim3(static_cast<uint32_t>(rest * a.splits)), block, 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_dx_join, dim3(static_cast<uint32_t>(rest) * 32u), block, 0, stream, a);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_dx_gemm(const DxArgs& a, int fmt, hipStream_t stream) {
+  if (fmt == kFmtNF4) return launch_dx_fmt<kFmtNF4>(a, stream);
+  return fmt == kFmtINT4 ? launch_dx_fmt<kFmtINT4>(a, stream) : launch_dx_fmt<kFmtNFG>(a, stream);
 }
 
 }  // namespace qlin

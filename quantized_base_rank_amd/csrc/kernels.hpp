@@ -251,13 +251,14 @@ struct DxArgs {
   int32_t pool;        // power of two
   int32_t pool_shift;  // log2(pool)
   uint16_t* dx;        // [M][K]
-  int32_t splits;      // launch_dx_gemm_shares: shares of the reduction,
-  float* partial;      // their sums [splits][M][K]
+  int32_t splits;      // shares of the reduction for the last tiles (0 or 1: none, one launch)
+  float* partial;      // their sums, dx_gemm_partial_floats
+  int32_t tile0;       // (the launch's own) the first of those tiles
 };
-hipError_t launch_dx_gemm(const DxArgs& a, int fmt, hipStream_t stream);
-// The same in shares (of at least one), joined by a second launch.
+// Shares that pay for the tiles past the last whole round of workgroups.
 int dx_gemm_shares(int64_t M, int64_t N, int64_t K);
-hipError_t launch_dx_gemm_shares(const DxArgs& a, int fmt, hipStream_t stream);
+int64_t dx_gemm_partial_floats(int64_t M, int64_t K, int shares);
+hipError_t launch_dx_gemm(const DxArgs& a, int fmt, hipStream_t stream);
 
 // Few-token (M <= 16) weight-streaming kernels, one launch per pass; the
 // adapter terms are folded into the split reductions.

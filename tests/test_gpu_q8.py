@@ -396,10 +396,12 @@ def test_backward_from_checkpoint(qb, oracle, fmt, M, N, K, r, pool):
 
 
 @pytest.mark.parametrize("fmt,M,N,K,pool", [("int4", 17, 4096, 320, 32), ("nf4", 100, 2064, 576, 1), ("nf4", 257, 1168, 256, 1),
-                                            ("int4", 300, 720, 128, 1), ("nf4", 40, 11008, 64, 1), ("nf4", 33, 272, 4160, 1)])
+                                            ("int4", 300, 720, 128, 1), ("nf4", 40, 11008, 64, 1), ("nf4", 33, 272, 4160, 1),
+                                            ("int4", 513, 1040, 22144, 32)])
 def test_backward_input_gradient_in_shares(qb, oracle, fmt, M, N, K, pool):
-    """dX of few tiles: the sum over the output features split between workgroups, last shares that end inside a
-    step, and a non-finite dY row that stays in its token; the same bits from run to run."""
+    """dX of few tiles, or of the few left after whole rounds: the sum over the output features split between
+    workgroups, last shares that end inside a step, and a non-finite dY row that stays in its token; the same bits
+    from run to run."""
     import torch
     print(f"[bwd q8 shares] {fmt} M={M} {N}x{K}", flush=True)
     rng = np.random.default_rng(M + N + K)
