@@ -473,6 +473,9 @@ int qlin_w8a8_fwd(const int8_t *xq, const float *x_scale, int64_t M, const int8_
  *   xq, x_scale  8-bit rows [M][d_in]
  *   u            fp32[M][r] from qlin_fwd's u_out (required)
  *   the rest, and the outputs dx (NULL skips it), dA, dB, as for qlin_bwd
+ *   (the sum of dX over d_out may be split between workgroups, in an order
+ *   that depends on the sizes only: the same bits from run to run, but not
+ *   always qlin_bwd's)
  *   M <= 2^24; d_in, d_out < 2^24 (QLIN_E_SHAPE otherwise)
  *   workspace, ws_bytes  >= qlin_bwd_q8_workspace_bytes(w, M, r, pool) (0 for
  *                invalid arguments); zero-filled once before its first use, as
