@@ -121,13 +121,16 @@ __device__ __forceinline__ RowScale row_scale(float mx) {
   return r;
 }
 
-// Sizes of a row kernel's instantiations: threads per row, vectors a thread.
-// One wave per row up to 1024 columns (several rows share a workgroup and
-// nothing needs a barrier), then as few waves as hold the row in two vectors
-// a thread, four beyond 16384 columns.  The gradient holds three rows and its
-// sums: 512 threads at most, which have 256 registers each, so its widest
-// rows end at half the width.  Rows below eight columns or past the widest
-// take the kernels that walk a row element by element.
+// Sizes of a row kernel's instantiations: threads per row, vectors of eight a
+// thread.  One wave per row up to 1024 columns (several rows share a workgroup
+// and nothing needs a barrier), then two or three vectors a thread up to 512
+// threads, and beyond 8192 columns as many vectors as 512 threads need.  (4096
+// rows to 8 bits, 512 threads against 1024 with two or four vectors: 11008
+// columns 27 and 32 us, 28672 64 and 76; the norm at 11008 77 and 101 us, at
+// 16384 112 and 129.  5120 columns: 256 x 3 14.6 us, 512 x 2 15.9.)  The
+// gradient holds three rows and its sums, so its widest rows end at half the
+// width.  Rows below eight columns or past the widest take the kernels that
+// walk a row element by element.
 constexpr int kRowMin = 8, kRowMax = 32768, kGradRowMax = 16384;
 template <bool GRAD, typename F>
 hipError_t by_row_width(int64_t d, F f) {
@@ -135,12 +138,18 @@ hipError_t by_row_width(int64_t d, F f) {
   if (d <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
   if (d <= 2048) return f(std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{});
   if (d <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  if (d <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  if (d <= 6144) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 3>{});
+  constexpr std::integral_constant<int, 512> wide{};
+  if (d <= 8192) return f(wide, std::integral_constant<int, 2>{});
+  if (d <= 12288) return f(wide, std::integral_constant<int, 3>{});
   if constexpr (GRAD) {
-    return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
+    return f(wide, std::integral_constant<int, 4>{});
   } else {
-    if (d <= 16384) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
-    return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+    if (d <= 16384) return f(wide, std::integral_constant<int, 4>{});
+    if (d <= 20480) return f(wide, std::integral_constant<int, 5>{});
+    if (d <= 24576) return f(wide, std::integral_constant<int, 6>{});
+    if (d <= 28672) return f(wide, std::integral_constant<int, 7>{});
+    return f(wide, std::integral_constant<int, 8>{});
   }
 }
 // Rows that share a workgroup: only rows of one wave, which need no barrier.

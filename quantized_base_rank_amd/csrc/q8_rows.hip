@@ -37,8 +37,8 @@ __device__ __forceinline__ u32x2 codes8(u32x4 v, const RowScale& s) {
 
 // bf16 rows, held in registers between the maximum and the codes: one read
 // of x.  HBM-bound: 3 bytes per element (5 with the values).  4096 x 28672:
-// 68-72 us, 5.0 TB/s (reading the rows twice took 247 us); 16 rows of 28672,
-// one workgroup each: 5.5 us, the latency of load, maximum and store.
+// 59 us, 6.0 TB/s (reading the rows twice took 247 us); 16 rows of 28672, one
+// workgroup each: 5.0 us, the latency of load, maximum and store.
 template <int T, int NV>
 __global__ __launch_bounds__(T * rows_per_group(T)) void k_quant_q8(Q8RowsArgs a) {
   constexpr int kRows = rows_per_group(T);

@@ -67,7 +67,8 @@ def values_of(codes, scale):
 # ------------------------------------------------------------ rows to 8 bits
 
 SIZES = [(1, 1), (3, 7), (1, 4096), (5, 64), (257, 5003), (130, 8192), (2, 28672), (2, 131072), (9, 1001),
-         (1000, 48), (33, 520), (4, 16392), (3, 40001)]
+         (1000, 48), (33, 520), (4, 16392), (3, 40001), (3, 1500), (3, 6144), (5, 11008), (3, 12290), (2, 20000),
+         (3, 24575), (2, 32768)]
 
 
 @pytest.mark.parametrize("M,d", SIZES)
