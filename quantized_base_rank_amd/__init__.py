@@ -50,6 +50,14 @@ def _stream(device) -> int:
         return torch.cuda.current_stream(device).cuda_stream
 
 
+def _capturing() -> bool:
+    torch = _torch()
+    try:
+        return torch._C._cuda_isCurrentStreamCapturing()  # without the module's own check, 0.2 us less
+    except AttributeError:
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _need(t, dtype, shape, name):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: expected contiguous {dtype} CUDA tensor of shape {tuple(shape)}, "
@@ -340,10 +348,14 @@ class Q8Rows:
         return self.codes.numel() + 4 * self.scale.numel()
 
 
-def _need_q8(q: Q8Rows, shape, name):
+def _need_q8(q: Q8Rows, rows: int, d: int, name):
     torch = _torch()
-    _need(q.codes, torch.int8, shape, name + ".codes")
-    _need(q.scale, torch.float32, shape[:1], name + ".scale")
+    c, s = q.codes, q.scale
+    # (one test where all is well: half the time of two _need calls)
+    if not (c.dtype is torch.int8 and s.dtype is torch.float32 and c.shape == (rows, d) and s.shape == (rows,)
+            and c.is_contiguous() and s.is_contiguous() and c.is_cuda and s.is_cuda):
+        _need(c, torch.int8, (rows, d), name + ".codes")
+        _need(s, torch.float32, (rows,), name + ".scale")
 
 
 _WS_STREAM = {}
@@ -357,7 +369,7 @@ def _stream_workspace(device, stream: int, nbytes: int):
     torch = _torch()
     ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
     ws[:_WS_COUNTERS].zero_()
-    if not torch.cuda.is_current_stream_capturing():
+    if not _capturing():
         _WS_STREAM[(device.index, stream)] = ws
     return ws
 
@@ -370,7 +382,7 @@ def _call_with_workspace(call, nbytes, device, stream: int, ws) -> int:
     replaced while the graph lives."""
     if ws is not None:
         return call(ws)
-    if not _torch().cuda.is_current_stream_capturing():
+    if not _capturing():
         ws = _WS_STREAM.get((device.index, stream))
         if ws is not None:
             status = call(ws)
@@ -408,7 +420,7 @@ def qlin_dequant_q8(q: Q8Rows, out=None):
     """bf16(codes * scale), [rows][d]."""
     torch = _torch()
     rows, d = q.codes.shape
-    _need_q8(q, (rows, d), "q")
+    _need_q8(q, rows, d, "q")
     if out is None:
         out = torch.empty(rows, d, dtype=torch.bfloat16, device=q.device)
     else:
@@ -492,8 +504,8 @@ def qlin_w8a8_fwd(x: Q8Rows, w: Q8Rows, y=None, ws=None):
     M, K = x.codes.shape
     N = w.codes.shape[0]
     dev = x.device
-    _need_q8(x, (M, K), "x")
-    _need_q8(w, (N, K), "w")
+    _need_q8(x, M, K, "x")
+    _need_q8(w, N, K, "w")
     if y is None:
         y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
     else:
@@ -515,7 +527,7 @@ def qlin_bwd_q8(w: QWeight, x: Q8Rows, A, B, r: int, s: float, dy, u, pool: int 
     torch = _torch()
     M = x.codes.shape[0]
     dev = x.device
-    _need_q8(x, (M, w.d_in), "x")
+    _need_q8(x, M, w.d_in, "x")
     _need(dy, torch.bfloat16, (M, w.d_out), "dy")
     _need(A, torch.bfloat16, (r, w.d_in // pool), "A")
     _need(B, torch.bfloat16, (w.d_out, r), "B")
