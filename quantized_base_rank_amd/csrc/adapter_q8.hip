@@ -465,18 +465,56 @@ int du_rt(int64_t M) { return M < 16384 ? 2 : 4; }
 }  // namespace
 
 int64_t tokens_strips(int64_t P) { return (P + kStrip - 1) / kStrip; }
-// Token shares: about one workgroup per compute unit, each wave at least two
-// steps.
-int tokens_splits(int64_t M, int64_t P, int r) {
-  const int64_t steps = (M + kStep - 1) / kStep;
-  int64_t s = 256 / tokens_strips(P);
-  const int64_t most = steps / (2 * tokens_waves((r + 31) / 32));
-  if (s > most) s = most;
-  return static_cast<int>(s < 1 ? 1 : s);
+// Token shares of dB and dA, whose blocks share one launch (dA's first, one
+// workgroup a unit): those with the shortest estimated end.  The constants
+// were fitted to every pair of shares at 31 sizes (150 .. 4096 tokens, 512 ..
+// 28672 columns, ranks 16 .. 128; the picks were 0.8 % off the fastest on
+// average, 6 % at worst): a block takes 6 us and 0.5 per 32 ranks, its waves'
+// steps, and with shares 7 us and 1 for every batch of their loads.  (As many
+// shares as fit a round each, which leaves partial rounds and long joins: 2048
+// x 4096 x 11008 rank 64 41 us with du, now 30; 3279 x 704 x 4928 rank 97 65
+// and 39; 4096 x 2048 x 2176 rank 64 48 and 31.)
+TokensShares tokens_shares(int64_t M, int64_t N, int64_t K, int r) {
+  static const int kShares[] = {1, 2, 3, 4, 6, 8, 12};
+  static const double kA[4] = {0.5, 0.85, 0.75, 1.3}, kB[4] = {0.7, 0.7, 0.7, 1.1};  // us a step, by 32 ranks
+  const int jt = (r + 31) / 32, waves = tokens_waves(jt), batch = jt == 1 ? 4 : 2;
+  const int64_t steps = (M + kStep - 1) / kStep, strips_a = tokens_strips(K), strips_b = tokens_strips(N);
+  auto block_us = [&](int s, double step) {
+    const double t = 6.0 + 0.5 * jt + static_cast<double>((steps + waves * s - 1) / (waves * s)) * step;
+    return s > 1 ? t + 7.0 + static_cast<double>((s + batch - 1) / batch) : t;
+  };
+  // the end of na blocks of ta and then nb of tb on 256 units
+  auto end_us = [](int64_t na, double ta, int64_t nb, double tb) {
+    const int64_t rounds = na / 256, more = na % 256;
+    double late = static_cast<double>(rounds + (more != 0 ? 1 : 0)) * ta, early = static_cast<double>(rounds) * ta;
+    double end = late;
+    while (nb > 0) {
+      double& t = more != 0 && late <= early ? late : early;
+      nb -= &t == &late ? more : 256 - more;
+      t += tb;
+      if (t > end) end = t;
+    }
+    return end;
+  };
+  TokensShares best;
+  double best_t = 0.0;
+  for (int sa : kShares) {
+    if (sa > 1 && (steps < sa * waves || strips_a * sa > 512)) break;
+    const double ta = block_us(sa, kA[jt - 1]);
+    for (int sb : kShares) {
+      if (sb > 1 && (steps < sb * waves || strips_b * sb > 512)) break;
+      const double t = end_us(strips_a * sa, ta, strips_b * sb, block_us(sb, kB[jt - 1]));
+      if (best_t == 0.0 || t < best_t) {
+        best_t = t;
+        best.dA = sa;
+        best.dB = sb;
+      }
+    }
+  }
+  return best;
 }
-int64_t tokens_partial_floats(int64_t M, int64_t P, int r) {
-  const int64_t s = tokens_splits(M, P, r);
-  return s > 1 ? s * tokens_strips(P) * 4 * ((r + 31) / 32) * kFW * 256 : 0;
+int64_t tokens_partial_floats(int64_t P, int r, int shares) {
+  return shares > 1 ? shares * tokens_strips(P) * 4 * ((r + 31) / 32) * kFW * 256 : 0;
 }
 int64_t plane_bytes(int64_t M, int r) { return (M + kStep - 1) / kStep * ((r + 31) / 32) * 2048; }
 

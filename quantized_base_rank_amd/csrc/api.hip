@@ -894,14 +894,15 @@ BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t 
   p.ds_splits = dx_stream_splits(N, K, fmt);
   p.dx_shares = p.dx_stream ? 1 : dx_gemm_shares(M, N, K);
   p.du_splits = du_splits(M, N);
-  p.dB_splits = tokens_splits(M, N, r);
-  p.dA_splits = tokens_splits(M, K, r);
+  const TokensShares shares = tokens_shares(M, N, K, r);
+  p.dB_splits = shares.dB;
+  p.dA_splits = shares.dA;
   p.dB_counters = p.dB_splits > 1 ? tokens_strips(N) : 0;
   const int64_t counters = std::max<int64_t>({p.dB_counters + (p.dA_splits > 1 ? tokens_strips(K) : 0),
                                               p.du_splits > 1 ? du_tiles(M) : 0,
                                               p.dx_stream && p.ds_splits > 1 ? dx_stream_panels(K) : 0});
   p.fits = counters <= kCounterWords && M <= kMaxBwdTokens && N < (int64_t{1} << 24) && K < (int64_t{1} << 24);
-  const int64_t partial = std::max<int64_t>({du_partial_floats(M, N, r), tokens_partial_floats(M, N, r),
+  const int64_t partial = std::max<int64_t>({du_partial_floats(M, N, r), tokens_partial_floats(N, r, p.dB_splits),
                                              p.dx_stream ? dx_stream_partial_floats(N, K, fmt) : 0,
                                              dx_gemm_partial_floats(M, K, p.dx_shares)});
   size_t off = kCounterBytes;
@@ -910,7 +911,7 @@ BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t 
   p.off_zdu = off;        off = align256(off + static_cast<size_t>(plane_bytes(M, r)));
   p.off_At = off;         off = align256(off + (p.dx_stream ? 0 : static_cast<size_t>(G) * r * sizeof(uint16_t)));
   p.off_partial = off;    off = align256(off + static_cast<size_t>(partial) * sizeof(float));
-  p.off_partial_dA = off; off = align256(off + static_cast<size_t>(tokens_partial_floats(M, K, r)) * sizeof(float));
+  p.off_partial_dA = off; off = align256(off + static_cast<size_t>(tokens_partial_floats(K, r, p.dA_splits)) * sizeof(float));
   p.off_tc = off;         off += transcode_bytes(w);
   p.total = off;
   return p;

@@ -134,14 +134,17 @@ struct TokensArgs {
   int32_t r, pool;        // pool 1 or 32 (codes)
   float alpha;
   uint16_t* C;
-  int32_t splits;         // tokens_splits(M, P, r)
+  int32_t splits;         // token shares (tokens_shares)
   int32_t blocks;         // (set by the launcher)
-  float* partial;         // tokens_partial_floats(M, P, r)
+  float* partial;         // tokens_partial_floats(P, r, splits)
   uint32_t* counters;     // tokens_strips(P)
 };
 int64_t tokens_strips(int64_t P);
-int tokens_splits(int64_t M, int64_t P, int r);
-int64_t tokens_partial_floats(int64_t M, int64_t P, int r);
+struct TokensShares {
+  int dB = 1, dA = 1;
+};
+TokensShares tokens_shares(int64_t M, int64_t N, int64_t K, int r);
+int64_t tokens_partial_floats(int64_t P, int r, int shares);
 int64_t plane_bytes(int64_t M, int r);
 hipError_t launch_tokens(const TokensArgs& dB, TokensArgs dA, hipStream_t stream);
 
