@@ -336,21 +336,22 @@ __global__ __launch_bounds__(256) void k_w8a8_join(W8A8Args a) {
 int64_t w8a8_gemm_tiles(int64_t M, int64_t N, int j) { return (M + 64 * j - 1) / (64 * j) * ((N + kTN - 1) / kTN); }
 
 // Tile height and shares of K by estimated time.  The constants were fitted
-// to every allowed shape at 53 sizes (65 .. 4096 tokens, 512 .. 32003
-// channels, K 1024 .. 28672): a half-stage of a lone workgroup takes 0.45,
-// 0.52, 0.52, 0.70 us (J = 1 .. 4: the ring's depth over the memory's
-// latency), of a full card 0.66 (two workgroups a unit, J = 1 only), 0.50,
-// 0.60, 0.79 us, start and end of a tile eight half-stages; the operands
-// stream at 4.4 TB/s at best; joining shares costs a launch and 8 bytes per
-// output and share at 3.5 TB/s.  Its picks were 1.6 % off the fastest on
-// average, 12 % at worst.  (128 x 8192 x 28672: J = 2 in 8 shares 61 us, in 6
-// 68, J = 1 in 4 89, J = 4 in one 272; 333 x 32003 x 4096: J = 3 53 us, J = 4
-// 60, J = 2 74.)
+// to every allowed shape at 59 sizes (65 .. 4096 tokens, 512 .. 32942
+// channels, K 256 .. 28672): a half-stage of a lone workgroup takes 0.47,
+// 0.44, 0.46, 0.89 us (J = 1 .. 4), of a full card 0.67 (two workgroups a
+// unit, J = 1 only), 0.51, 0.63, 0.73 us, start and end of a tile as long as
+// 5, 9, 7, 26 half-stages; the operands stream at 4.5 TB/s at best; joining
+// shares costs a launch and 8 bytes per output and share at 4.4 TB/s.  Its
+// picks were 1.1 % off the fastest on average, 12 % at worst.  (128 x 8192 x
+// 28672: J = 2 in 8 shares 61 us, in 6 68, J = 1 in 4 89, J = 4 in one 272;
+// 333 x 32003 x 4096: J = 3 53 us, J = 4 60, J = 2 74; 2772 x 32768 x 512: J =
+// 3 92, J = 4 101; 4096 x 8192 x 28672: J = 4 704, J = 3 815, J = 2 869.)
 W8A8Shape w8a8_gemm_shape(int64_t M, int64_t N, int64_t K) {
-  static const double kLone[4] = {0.45, 0.52, 0.52, 0.70}, kFull[4] = {0.66, 0.50, 0.60, 0.79};
+  static const double kLone[4] = {0.47, 0.44, 0.46, 0.89}, kFull[4] = {0.67, 0.51, 0.63, 0.73};
+  static const double kEnds[4] = {5, 9, 7, 26};
   static const int kShares[] = {1, 2, 3, 4, 6, 8, 12, 16};
   const int64_t halves = (K + kHalf - 1) / kHalf;
-  const double stream = static_cast<double>(K) * static_cast<double>(M + N) / 4.4e6;
+  const double stream = static_cast<double>(K) * static_cast<double>(M + N) / 4.5e6;
   W8A8Shape best;
   double best_t = 0.0;
   for (int j = 4; j >= 1; --j) {
@@ -360,9 +361,9 @@ W8A8Shape w8a8_gemm_shape(int64_t M, int64_t N, int64_t K) {
       const double fill = tiles * s < slots ? static_cast<double>(tiles * s) / static_cast<double>(slots) : 1.0;
       const double half = kLone[j - 1] + (kFull[j - 1] - kLone[j - 1]) * fill;
       const double rounds = static_cast<double>((tiles * s + slots - 1) / slots);
-      double t = rounds * static_cast<double>((halves + s - 1) / s + 8) * half;
+      double t = rounds * (static_cast<double>((halves + s - 1) / s) + kEnds[j - 1]) * half;
       if (t < stream) t = stream;
-      if (s > 1) t += 4.0 + 8.0 * static_cast<double>(M) * static_cast<double>(N) * s / 3.5e6;
+      if (s > 1) t += 3.8 + 8.0 * static_cast<double>(M) * static_cast<double>(N) * s / 4.4e6;
       if (best_t == 0.0 || t < best_t) {
         best_t = t;
         best.j = j;
