@@ -998,9 +998,9 @@ ProductPlan make_product_plan(int64_t M, int64_t N, int64_t K) {
   ProductPlan p;
   p.few = M <= kFewProductM;
   if (p.few) {
-    p.splits = w8a8_few_splits(N, K);
+    p.splits = w8a8_few_splits(M, N, K);
     p.words = w8a8_few_partial_words(M, N, K);
-    p.fits = w8a8_few_tiles(N, K) <= (p.splits == 1 ? kMaxTiles : kCounterWords);
+    p.fits = w8a8_few_tiles(M, N, K) <= (p.splits == 1 ? kMaxTiles : kCounterWords);
   } else {
     const W8A8Shape s = w8a8_gemm_shape(M, N, K);
     p.j = s.j;

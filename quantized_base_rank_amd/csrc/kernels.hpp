@@ -120,8 +120,8 @@ int64_t w8a8_gemm_tiles(int64_t M, int64_t N, int j);
 int64_t w8a8_gemm_partial_words(int64_t M, int64_t N, W8A8Shape s);
 hipError_t launch_w8a8_gemm(const W8A8Args& a, int j, hipStream_t stream);  // any M
 hipError_t launch_w8a8_few(const W8A8Args& a, hipStream_t stream);   // M <= 64
-int64_t w8a8_few_tiles(int64_t N, int64_t K);
-int w8a8_few_splits(int64_t N, int64_t K);
+int64_t w8a8_few_tiles(int64_t M, int64_t N, int64_t K);
+int w8a8_few_splits(int64_t M, int64_t N, int64_t K);
 int64_t w8a8_few_partial_words(int64_t M, int64_t N, int64_t K);
 
 // Sums over the tokens: C = alpha Z^T X, Z [M][r] as bf16 hi/lo planes in

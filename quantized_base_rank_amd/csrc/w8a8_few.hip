@@ -172,41 +172,44 @@ double few_fill(int64_t groups) { return static_cast<double>(groups) / (256.0 * 
 
 // 16-row tiles per workgroup.  More rows use each token operand more often
 // but leave fewer workgroups.  Four where K has four chunks for each of the
-// shares that fill the card (16 tokens by 8192 x 28672: 50 us, against 54 and
-// 56 with two and one), else two where that fills the rounds about as well as
-// one does (32003 x 4096: 31 against 35; 11008 x 4096, 344 groups: 16 against
-// 14).
-int few_rt(int64_t N, int64_t K) {
-  const int64_t t4 = (N + 63) / 64, shares = t4 < 256 ? 256 / t4 : 1;
-  if (K >= shares * 4 * 2048 && t4 * shares >= 128) return 4;
-  const int64_t t2 = (N + 31) / 32, t1 = (N + 15) / 16;
-  return t2 >= 256 && few_fill(t2) > few_fill(t1) - 0.1 ? 2 : 1;
+// shares that fill the card (16 tokens by 8192 x 28672: 49 us, against 53 and
+// 57 with two and one), and for more than 32 tokens where four fill the rounds
+// about as well as two do (64 by 14336 x 4096: 22 against 25; 22016 x 2048,
+// 344 groups: 23 against 22); else two where those fill them about as well as
+// one (16 by 7168 x 4096: 9.8 against 10.7; 64 by 7168 x 4096: 13.6 against
+// 17.1; 11008 x 4096, 344 groups: 16 against 15).
+int few_rt(int64_t M, int64_t N, int64_t K) {
+  const int64_t t4 = (N + 63) / 64, t2 = (N + 31) / 32, t1 = (N + 15) / 16, shares = t4 < 256 ? 256 / t4 : 1;
+  if (t4 >= 128 && K >= shares * 4 * 2048) return 4;
+  if (M > 32 && t4 >= 128 && few_fill(t4) > few_fill(t2) - 0.1) return 4;
+  return t2 >= 128 && few_fill(t2) > few_fill(t1) - 0.1 ? 2 : 1;
 }
 int few_mt(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 
 }  // namespace
 
-int64_t w8a8_few_tiles(int64_t N, int64_t K) {
-  return (N + 16 * few_rt(N, K) - 1) / (16 * few_rt(N, K));
+int64_t w8a8_few_tiles(int64_t M, int64_t N, int64_t K) {
+  const int rows = 16 * few_rt(M, N, K);
+  return (N + rows - 1) / rows;
 }
 // Shares of K: about one workgroup per compute unit, each a chunk or
 // more.
-int w8a8_few_splits(int64_t N, int64_t K) {
-  const int64_t tiles = w8a8_few_tiles(N, K), chunks = (K + 2047) / 2048;
+int w8a8_few_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = w8a8_few_tiles(M, N, K), chunks = (K + 2047) / 2048;
   int64_t s = 256 / tiles;
   if (s > chunks) s = chunks;
   return static_cast<int>(s < 1 ? 1 : s);
 }
 int64_t w8a8_few_partial_words(int64_t M, int64_t N, int64_t K) {
-  const int64_t s = w8a8_few_splits(N, K);
-  return s > 1 ? s * w8a8_few_tiles(N, K) * 16 * few_rt(N, K) * 16 * few_mt(M) : 0;
+  const int64_t s = w8a8_few_splits(M, N, K);
+  return s > 1 ? s * w8a8_few_tiles(M, N, K) * 16 * few_rt(M, N, K) * 16 * few_mt(M) : 0;
 }
 
 namespace {
 
 template <int RT>
 hipError_t launch_few_rt(const W8A8Args& a, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(w8a8_few_tiles(a.N, a.K) * a.splits)), block(64 * kFewWaves);
+  const dim3 grid(static_cast<uint32_t>(w8a8_few_tiles(a.M, a.N, a.K) * a.splits)), block(64 * kFewWaves);
   switch (few_mt(a.M)) {
     case 1: hipLaunchKernelGGL((k_w8a8_few<RT, 1>), grid, block, 0, stream, a); break;
     case 2: hipLaunchKernelGGL((k_w8a8_few<RT, 2>), grid, block, 0, stream, a); break;
@@ -218,7 +221,7 @@ hipError_t launch_few_rt(const W8A8Args& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_w8a8_few(const W8A8Args& a, hipStream_t stream) {
-  switch (few_rt(a.N, a.K)) {
+  switch (few_rt(a.M, a.N, a.K)) {
     case 1: return launch_few_rt<1>(a, stream);
     case 2: return launch_few_rt<2>(a, stream);
     default: return launch_few_rt<4>(a, stream);
