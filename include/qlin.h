@@ -476,7 +476,9 @@ int qlin_w8a8_fwd(const int8_t *xq, const float *x_scale, int64_t M, const int8_
  *   (the sum of dX over d_out may be split between workgroups, in an order
  *   that depends on the sizes only: the same bits from run to run, but not
  *   always qlin_bwd's)
- *   M <= 2^24; d_in, d_out < 2^24 (QLIN_E_SHAPE otherwise)
+ *   M <= 2^24; d_in, d_out < 2^24; with dx for more than 16 tokens also
+ *   min(M, 256) d_out < 2^30 and (d_out + 128) d_in < 2^33 (QLIN_E_SHAPE
+ *   otherwise)
  *   workspace, ws_bytes  >= qlin_bwd_q8_workspace_bytes(w, M, r, pool) (0 for
  *                invalid arguments); zero-filled once before its first use, as
  *                for qlin_workspace_bytes

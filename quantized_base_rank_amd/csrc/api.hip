@@ -886,6 +886,12 @@ struct BwdQ8Plan {
 // of codes) are made for: tokens, and below 2^24 features either way.
 constexpr int64_t kMaxBwdTokens = int64_t{1} << 24;
 
+// What the many-token dX reaches with 32-bit offsets: a tile's rows of dY (bit
+// 31 marks what is out of range) and the packed codes, a step past their end.
+bool dx_gemm_reaches(int64_t M, int64_t N, int64_t K) {
+  return std::min<int64_t>(M, 256) * N * 2 < (int64_t{1} << 31) && (N + 128) * (K >> 1) < (int64_t{1} << 32);
+}
+
 BwdQ8Plan make_bwd_q8_plan(const qlin_qweight* w, int64_t M, int32_t r, int32_t pool) {
   BwdQ8Plan p;
   const int64_t N = w->d_out, K = w->d_in, G = K / pool;
@@ -1060,6 +1066,7 @@ int qlin_bwd_q8(const qlin_qweight* w, const int8_t* xq, const float* x_scale, i
     return QLIN_E_ALIGN;
   const BwdQ8Plan p = make_bwd_q8_plan(w, M, r, pool);
   if (!p.fits) return QLIN_E_SHAPE;
+  if (dx != nullptr && !p.dx_stream && !dx_gemm_reaches(M, w->d_out, w->d_in)) return QLIN_E_SHAPE;
   if (workspace == nullptr || ws_bytes < p.total) return QLIN_E_WORKSPACE;
   if (!aligned16(workspace)) return QLIN_E_ALIGN;
 

@@ -92,6 +92,11 @@ def test_backward_refusals():
     assert f(*_swap(good, 8, 16)) == UNSUPPORTED
     assert f(*_swap(good, 0, ctypes.byref(_qw(fmt=1, block=64, dq=256)))) == UNSUPPORTED  # pooled needs INT4
     assert f(*_swap(good, 14, None)) == WORKSPACE and f(*_swap(good, 15, 64)) == WORKSPACE
+    # dX beyond its 32-bit offsets: 256 rows of dY, the packed codes
+    for m, d_out, d_in in ((256, 1 << 22, 64), (300, 1 << 23, 64), (20, 1 << 17, 1 << 16)):
+        big = [ctypes.byref(_qw(d_out=d_out, d_in=d_in)), *good[1:]]
+        big[3], big[15] = m, 1 << 50
+        assert f(*big) == SHAPE
     n = _lib.lib().qlin_bwd_q8_workspace_bytes
     assert n(ctypes.byref(w), 20, 8, 32) > 0
     assert n(ctypes.byref(w), 20, 0, 32) == 0 and n(ctypes.byref(w), 0, 8, 32) == 0
