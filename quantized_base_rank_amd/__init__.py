@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import threading
 from typing import Optional
 
 import numpy as np
@@ -359,6 +360,7 @@ def _need_q8(q: Q8Rows, rows: int, d: int, name):
 
 
 _WS_STREAM = {}
+_WS_LOCKS = {}
 _WS_COUNTERS = 1 << 16  # bytes at a workspace's start that have to be zero before its first use
 
 
@@ -374,21 +376,34 @@ def _stream_workspace(device, stream: int, nbytes: int):
     return ws
 
 
+def _lock_of(key):
+    """The lock of a workspace that host threads share (reentrant: memory
+    taken inside may run a finalizer)."""
+    lock = _WS_LOCKS.get(key)
+    return lock if lock is not None else _WS_LOCKS.setdefault(key, threading.RLock())
+
+
 def _call_with_workspace(call, nbytes, device, stream: int, ws) -> int:
     """``call(ws)`` with the caller's workspace, or with this stream's.  The
     call itself says when that is too small (before it enqueues anything), so
-    the size is asked for only then.  A call that is being captured into a
-    graph gets memory of that graph's own: the stream's workspace may be
-    replaced while the graph lives."""
+    the size is asked for only then.  Threads that use the same stream take
+    turns at its workspace: a call's launches hand sums to one another in it,
+    and the interpreter's lock is dropped during the call.  (Threads that pass
+    one workspace of their own have to take turns themselves.)  A call that is
+    being captured into a graph gets memory of that graph's own: the stream's
+    workspace may be replaced while the graph lives."""
     if ws is not None:
         return call(ws)
-    if not _capturing():
-        ws = _WS_STREAM.get((device.index, stream))
+    if _capturing():
+        return call(_stream_workspace(device, stream, nbytes()))
+    key = (device.index, stream)
+    with _lock_of(key):
+        ws = _WS_STREAM.get(key)
         if ws is not None:
             status = call(ws)
             if status != QLIN_E_WORKSPACE:
                 return status
-    return call(_stream_workspace(device, stream, nbytes()))
+        return call(_stream_workspace(device, stream, nbytes()))
 
 
 def qlin_quantize_q8(x, codes=None, scale=None, values=None) -> Q8Rows:
