@@ -200,6 +200,14 @@ def qlin_workspace_bytes(w: QWeight, M: int, r: int, pool: int = 1) -> int:
 
 
 _WS = {}
+_WS_LOCKS = {}
+
+
+def _lock_of(key):
+    """The lock of a workspace that host threads share (reentrant: memory
+    taken inside may run a finalizer)."""
+    lock = _WS_LOCKS.get(key)
+    return lock if lock is not None else _WS_LOCKS.setdefault(key, threading.RLock())
 
 
 def workspace(device, nbytes: int):
@@ -212,6 +220,16 @@ def workspace(device, nbytes: int):
         ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
         _WS[key] = ws
     return ws
+
+
+def _call_with_device_workspace(call, nbytes: int, device, ws) -> int:
+    """``call(ws)`` with the caller's workspace, or with the device's, at
+    which host threads take turns: a call's launches hand sums to one another
+    in it."""
+    if ws is not None:
+        return call(ws)
+    with _lock_of(str(device)):
+        return call(workspace(device, nbytes))
 
 
 def qlin_fwd(w: QWeight, x, A, B, r: int, s: float, pool: int = 1, y=None, u_out=None,
@@ -232,12 +250,14 @@ def qlin_fwd(w: QWeight, x, A, B, r: int, s: float, pool: int = 1, y=None, u_out
     if u_out is None and want_u:
         u_out = torch.empty((M, r), dtype=torch.float32, device=dev)
     nbytes = qlin_workspace_bytes(w, M, r, pool)
-    if ws is None:
-        ws = workspace(dev, nbytes)
     s_ = w.struct()
-    check(lib().qlin_fwd(ctypes.byref(s_), x.data_ptr(), M, _ptr(A), _ptr(B), r,
-                         float(s), pool, y.data_ptr(), _ptr(u_out), ws.data_ptr(), ws.numel(),
-                         _stream(dev)), "qlin_fwd")
+
+    def call(ws):
+        return lib().qlin_fwd(ctypes.byref(s_), x.data_ptr(), M, _ptr(A), _ptr(B), r,
+                              float(s), pool, y.data_ptr(), _ptr(u_out), ws.data_ptr(), ws.numel(),
+                              _stream(dev))
+
+    check(_call_with_device_workspace(call, nbytes, dev, ws), "qlin_fwd")
     return y, u_out
 
 
@@ -279,13 +299,15 @@ def qlin_bwd(w: QWeight, x, A, B, r: int, s: float, dy, pool: int = 1, u_saved=N
     if dB is None:
         dB = torch.empty((w.d_out, r), dtype=torch.bfloat16, device=dev)
     nbytes = qlin_workspace_bytes(w, M, r, pool)
-    if ws is None:
-        ws = workspace(dev, nbytes)
     s_ = w.struct()
-    check(lib().qlin_bwd(ctypes.byref(s_), x.data_ptr(), M, A.data_ptr(), B.data_ptr(), r,
-                         float(s), pool, dy.data_ptr(), _ptr(u_saved),
-                         _ptr(dx) if need_dx else None, dA.data_ptr(), dB.data_ptr(),
-                         ws.data_ptr(), ws.numel(), _stream(dev)), "qlin_bwd")
+
+    def call(ws):
+        return lib().qlin_bwd(ctypes.byref(s_), x.data_ptr(), M, A.data_ptr(), B.data_ptr(), r,
+                              float(s), pool, dy.data_ptr(), _ptr(u_saved),
+                              _ptr(dx) if need_dx else None, dA.data_ptr(), dB.data_ptr(),
+                              ws.data_ptr(), ws.numel(), _stream(dev))
+
+    check(_call_with_device_workspace(call, nbytes, dev, ws), "qlin_bwd")
     return dx, dA, dB
 
 
@@ -360,7 +382,6 @@ def _need_q8(q: Q8Rows, rows: int, d: int, name):
 
 
 _WS_STREAM = {}
-_WS_LOCKS = {}
 _WS_COUNTERS = 1 << 16  # bytes at a workspace's start that have to be zero before its first use
 
 
@@ -374,13 +395,6 @@ def _stream_workspace(device, stream: int, nbytes: int):
     if not _capturing():
         _WS_STREAM[(device.index, stream)] = ws
     return ws
-
-
-def _lock_of(key):
-    """The lock of a workspace that host threads share (reentrant: memory
-    taken inside may run a finalizer)."""
-    lock = _WS_LOCKS.get(key)
-    return lock if lock is not None else _WS_LOCKS.setdefault(key, threading.RLock())
 
 
 def _call_with_workspace(call, nbytes, device, stream: int, ws) -> int:

@@ -88,3 +88,52 @@ def test_calls_on_different_streams_do_not_wait(monkeypatch):
         return 0
     keys = [(0, 5), (0, 6), (1, 5)]
     _in_threads(3, lambda i: qb._call_with_workspace(call, lambda: 1, SimpleNamespace(index=keys[i][0]), keys[i][1], None))
+
+
+class _Tensor:
+    """What the binding asks of a device tensor, without a device."""
+    is_cuda = True
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape = dtype, shape
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x1000
+
+    def numel(self):
+        return 1 << 20
+
+
+def test_layer_calls_on_the_device_s_workspace_take_turns(monkeypatch):
+    import torch
+    inside, most = [], []
+
+    def native(*args):
+        inside.append(1)
+        most.append(len(inside))
+        time.sleep(0.005)
+        inside.pop()
+        return 0
+    fake = SimpleNamespace(qlin_fwd=native, qlin_bwd=native, qlin_workspace_bytes=lambda *a: 1)
+    monkeypatch.setattr(qb, "lib", lambda: fake)
+    monkeypatch.setattr(qb, "_stream", lambda device: 0)
+    monkeypatch.setattr(qb, "workspace", lambda device, nbytes: _Tensor(torch.uint8, 1 << 20))
+    bf = torch.bfloat16
+    dev = torch.device("cuda", 0)
+    x, A, B, dy = _Tensor(bf, 4, 64), _Tensor(bf, 2, 64), _Tensor(bf, 16, 2), _Tensor(bf, 4, 16)
+    u = _Tensor(torch.float32, 4, 2)
+    for t in (x, A, B, dy, u):
+        t.device = dev
+    w = qb.QWeight(qb.QLIN_FMT_NF4, 64, 0, 16, 64, _Tensor(torch.uint8, 16, 32), absmax=_Tensor(torch.float32, 16))
+
+    def body(i):
+        for _ in range(3):
+            if i % 2 == 0:
+                qb.qlin_fwd(w, x, A, B, 2, 1.0, y=dy, u_out=u)
+            else:
+                qb.qlin_bwd(w, x, A, B, 2, 1.0, dy, u_saved=u, dx=x, dA=A, dB=B)
+    _in_threads(6, body)
+    assert max(most) == 1 and len(most) == 18
