@@ -70,7 +70,9 @@ typedef enum {
                              value outside the fp16 range)                     */
   QLIN_E_UNSUPPORTED = 5, /* a valid but unimplemented parameter combination   */
   QLIN_E_WORKSPACE = 6,   /* workspace NULL or smaller than qlin_workspace_bytes */
-  QLIN_E_HIP = 7          /* the HIP runtime reported an error                 */
+  QLIN_E_HIP = 7,         /* the HIP runtime reported an error                 */
+  QLIN_E_OVERLAP = 8      /* an output overlaps an input, another output or the
+                             workspace (8-bit row operators)                   */
 } qlin_status;
 
 /* Packed weight formats. */
@@ -381,7 +383,9 @@ int qlin_int4_scale_zero_grad(const qlin_qweight *w, const uint16_t *x, int64_t 
  * and a row of zeros has scale 0 and codes 0.  A row that holds NaN or an
  * infinity has scale NaN and codes 0: whatever is computed from it is NaN for
  * that row and for no other.  The functions of this part are asynchronous and
- * report nothing from the device.  [QLoRA "Background: what is
+ * report nothing from the device.  Their outputs must overlap neither inputs
+ * nor one another nor the workspace (QLIN_E_OVERLAP; the packed weight's arrays
+ * are not looked at), so h = residual or dx = dy cannot be formed in place.  [QLoRA "Background: what is
  * quantization?": absmax scaling of a block, here one row]
  * ---------------------------------------------------------------------- */
 
@@ -420,7 +424,7 @@ int qlin_dequant_q8(const int8_t *codes, const float *scale, int64_t rows, int64
  *   rstd      fp32[M] (output, may be NULL), for qlin_rmsnorm_bwd
  *   values    bf16[M][d] (output, may be NULL): bf16(fl32(codes * scale))
  * A row whose sum of squares leaves fp32's range counts as non-finite.
- * Outputs must not overlap inputs.  Asynchronous on `stream`.
+ * Asynchronous on `stream`.
  */
 int qlin_rmsnorm_q8(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t M,
                     int64_t d, float eps, uint16_t *h, int8_t *codes, float *scale, float *rstd,
@@ -438,7 +442,7 @@ int qlin_rmsnorm_q8(const uint16_t *x, const uint16_t *residual, const uint16_t 
  *   dgamma  fp32[d] (output), summed in a fixed order
  *   workspace, ws_bytes  >= qlin_rmsnorm_workspace_bytes(M, d) (0 for invalid
  *           sizes); no initial contents needed
- * Outputs must not overlap inputs.  Asynchronous on `stream`.
+ * Asynchronous on `stream`.
  */
 size_t qlin_rmsnorm_workspace_bytes(int64_t M, int64_t d);
 int qlin_rmsnorm_bwd(const uint16_t *h, const uint16_t *gamma, const float *rstd,

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -492,6 +493,7 @@ const char* qlin_status_string(int status) {
     case QLIN_E_UNSUPPORTED: return "unsupported parameter combination";
     case QLIN_E_WORKSPACE: return "workspace missing or too small";
     case QLIN_E_HIP: return "HIP runtime error";
+    case QLIN_E_OVERLAP: return "an output overlaps an input, another output or the workspace";
     default: return "unknown status";
   }
 }
@@ -868,6 +870,31 @@ namespace {
 constexpr int64_t kMaxRowLen = 131072;   // columns of an 8-bit row
 constexpr int64_t kMaxProductK = 131056; // 128 * 128 * K stays below 2^31
 
+// Memory of a call: where it starts and how many bytes (p NULL: none).
+struct Span {
+  const void* p;
+  size_t n;
+};
+Span span(const void* p, int64_t count, size_t size) { return Span{p, static_cast<size_t>(count) * size}; }
+
+// Whether one of `outs` overlaps another or one of `ins`.  The row kernels
+// take a row's last vector from memory that a neighbouring vector covers too,
+// and some read a row again after part of the output is stored, so no output
+// may stand in for an input.
+bool overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && x < y + b.n && y < x + a.n;
+  };
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* p = o + 1; p != outs.end(); ++p)
+      if (meet(*o, *p)) return true;
+    for (const Span& i : ins)
+      if (meet(*o, i)) return true;
+  }
+  return false;
+}
+
 int check_rows(int64_t rows, int64_t d) {
   if (rows < 1 || rows > (int64_t{1} << 31) || d < 1 || d > kMaxRowLen) return QLIN_E_SHAPE;
   return QLIN_OK;
@@ -932,6 +959,9 @@ int qlin_quantize_q8(const void* x, int32_t dtype, int64_t rows, int64_t d, int8
   const int st = check_rows(rows, d);
   if (st != QLIN_OK) return st;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scale) || !aligned16(values)) return QLIN_E_ALIGN;
+  const int64_t n = rows * d;
+  if (overlap({span(codes, n, 1), span(scale, rows, 4), span(values, n, 2)}, {span(x, n, dtype == QLIN_F32 ? 4 : 2)}))
+    return QLIN_E_OVERLAP;
   Q8RowsArgs a{};
   a.x = x; a.rows = rows; a.d = d; a.codes = codes; a.scale = scale; a.values = values;
   return hip_status(hooked("k_quant_q8", stream, [&] { return launch_quant_q8(a, dtype == QLIN_F32, stream); }));
@@ -943,6 +973,7 @@ int qlin_dequant_q8(const int8_t* codes, const float* scale, int64_t rows, int64
   const int st = check_rows(rows, d);
   if (st != QLIN_OK) return st;
   if (!aligned16(codes) || !aligned16(scale) || !aligned16(out)) return QLIN_E_ALIGN;
+  if (overlap({span(out, rows * d, 2)}, {span(codes, rows * d, 1), span(scale, rows, 4)})) return QLIN_E_OVERLAP;
   return hip_status(launch_dequant_q8(codes, scale, rows, d, out, stream));
 }
 
@@ -958,6 +989,10 @@ int qlin_rmsnorm_q8(const uint16_t* x, const uint16_t* residual, const uint16_t*
   if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(h) || !aligned16(codes) ||
       !aligned16(scale) || !aligned16(rstd) || !aligned16(values))
     return QLIN_E_ALIGN;
+  const int64_t n = M * d;
+  if (overlap({span(h, n, 2), span(codes, n, 1), span(scale, M, 4), span(rstd, M, 4), span(values, n, 2)},
+              {span(x, n, 2), span(residual, n, 2), span(gamma, d, 2)}))
+    return QLIN_E_OVERLAP;
   RmsNormArgs a{};
   a.x = x; a.res = residual; a.gamma = gamma; a.M = M; a.d = d; a.eps = eps; a.h = h; a.codes = codes;
   a.scale = scale; a.rstd = rstd; a.values = values;
@@ -981,8 +1016,13 @@ int qlin_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd
   if (!aligned16(h) || !aligned16(gamma) || !aligned16(rstd) || !aligned16(dy) || !aligned16(dh) ||
       !aligned16(dx) || !aligned16(dgamma))
     return QLIN_E_ALIGN;
-  if (workspace == nullptr || ws_bytes < qlin_rmsnorm_workspace_bytes(M, d)) return QLIN_E_WORKSPACE;
+  const size_t need = qlin_rmsnorm_workspace_bytes(M, d);
+  if (workspace == nullptr || ws_bytes < need) return QLIN_E_WORKSPACE;
   if (!aligned16(workspace)) return QLIN_E_ALIGN;
+  const int64_t n = M * d;
+  if (overlap({span(dx, n, 2), span(dgamma, d, 4), Span{workspace, need}},
+              {span(h, n, 2), span(gamma, d, 2), span(rstd, M, 4), span(dy, n, 2), span(dh, n, 2)}))
+    return QLIN_E_OVERLAP;
   RmsNormBwdArgs a{};
   a.h = h; a.gamma = gamma; a.rstd = rstd; a.dy = dy; a.dh = dh; a.M = M; a.d = d; a.dx = dx; a.dgamma = dgamma;
   a.partial = ws_at<float>(workspace, kCounterBytes);
@@ -1036,6 +1076,9 @@ int qlin_w8a8_fwd(const int8_t* xq, const float* x_scale, int64_t M, const int8_
     return QLIN_E_ALIGN;
   if (workspace == nullptr || ws_bytes < need) return QLIN_E_WORKSPACE;
   if (!aligned16(workspace)) return QLIN_E_ALIGN;
+  if (overlap({span(y, M * N, 2), Span{workspace, need}},
+              {span(xq, M * K, 1), span(x_scale, M, 4), span(wq, N * K, 1), span(w_scale, N, 4)}))
+    return QLIN_E_OVERLAP;
   const ProductPlan p = make_product_plan(M, N, K);
   W8A8Args a{};
   a.xq = xq; a.xs = x_scale; a.M = M; a.wq = wq; a.ws = w_scale; a.N = N; a.K = K; a.y = y;
@@ -1071,6 +1114,10 @@ int qlin_bwd_q8(const qlin_qweight* w, const int8_t* xq, const float* x_scale, i
   if (!aligned16(workspace)) return QLIN_E_ALIGN;
 
   const int64_t N = w->d_out, K = w->d_in, G = K / pool;
+  if (overlap({span(dx, M * K, 2), span(dA, r * G, 2), span(dB, N * r, 2), Span{workspace, p.total}},
+              {span(xq, M * K, 1), span(x_scale, M, 4), span(A, r * G, 2), span(B, N * r, 2), span(dy, M * N, 2),
+               span(u, M * r, 4)}))
+    return QLIN_E_OVERLAP;
   const int fmt = fmt_of(w);
   float* partial = ws_at<float>(workspace, p.off_partial);
   uint32_t* counters = ws_at<uint32_t>(workspace, 0);
