@@ -340,20 +340,23 @@ int64_t w8a8_gemm_tiles(int64_t M, int64_t N, int j) { return (M + 64 * j - 1) /
 // channels, K 256 .. 28672): a half-stage of a lone workgroup takes 0.47,
 // 0.44, 0.46, 0.89 us (J = 1 .. 4), of a full card 0.67 (two workgroups a
 // unit, J = 1 only), 0.51, 0.63, 0.73 us, start and end of a tile as long as
-// 5, 9, 7, 26 half-stages; the operands stream at 4.5 TB/s at best; joining
-// shares costs a launch and 8 bytes per output and share at 4.4 TB/s.  Its
-// picks were 1.1 % off the fastest on average, 12 % at worst.  (128 x 8192 x
-// 28672: J = 2 in 8 shares 61 us, in 6 68, J = 1 in 4 89, J = 4 in one 272;
-// 333 x 32003 x 4096: J = 3 53 us, J = 4 60, J = 2 74; 2772 x 32768 x 512: J =
-// 3 92, J = 4 101; 4096 x 8192 x 28672: J = 4 704, J = 3 815, J = 2 869.)
+// 5, 9, 7, 26 half-stages; joining shares costs a launch and 8 bytes per
+// output and share at 4.4 TB/s.  The operands stream no faster than 4.9 TB/s
+// on a full card, 1.2 TB/s and its share of the rest on part of one; of
+// shapes that this floor makes equal, the one with less work of its own.
+// (With one floor of 4.5 TB/s for all, ties to the tallest, 128 x 8192 x 28672
+// took J = 3 in 6 shares, 74 us, for J = 2 in 8, 62; over 75 sizes, 65 .. 4096
+// tokens, the picks were 3.7 % off the fastest, 28 % at worst, now 1.5 and 15.)
+// 333 x 32003 x 4096: J = 3 53 us, J = 4 62, J = 2 73; 2772 x 32768 x 512: J =
+// 3 92, J = 4 101; 4096 x 8192 x 28672: J = 4 704, J = 3 815, J = 2 869.
 W8A8Shape w8a8_gemm_shape(int64_t M, int64_t N, int64_t K) {
   static const double kLone[4] = {0.47, 0.44, 0.46, 0.89}, kFull[4] = {0.67, 0.51, 0.63, 0.73};
   static const double kEnds[4] = {5, 9, 7, 26};
   static const int kShares[] = {1, 2, 3, 4, 6, 8, 12, 16};
   const int64_t halves = (K + kHalf - 1) / kHalf;
-  const double stream = static_cast<double>(K) * static_cast<double>(M + N) / 4.5e6;
+  const double operands = static_cast<double>(K) * static_cast<double>(M + N);  // bytes
   W8A8Shape best;
-  double best_t = 0.0;
+  double best_t = 0.0, best_own = 0.0;
   for (int j = 4; j >= 1; --j) {
     const int64_t tiles = w8a8_gemm_tiles(M, N, j), slots = j == 1 ? 512 : 256;
     for (int s : kShares) {
@@ -361,11 +364,13 @@ W8A8Shape w8a8_gemm_shape(int64_t M, int64_t N, int64_t K) {
       const double fill = tiles * s < slots ? static_cast<double>(tiles * s) / static_cast<double>(slots) : 1.0;
       const double half = kLone[j - 1] + (kFull[j - 1] - kLone[j - 1]) * fill;
       const double rounds = static_cast<double>((tiles * s + slots - 1) / slots);
-      double t = rounds * (static_cast<double>((halves + s - 1) / s) + kEnds[j - 1]) * half;
-      if (t < stream) t = stream;
+      const double own = rounds * (static_cast<double>((halves + s - 1) / s) + kEnds[j - 1]) * half;
+      const double stream = operands / (1.2e6 + 3.7e6 * fill);
+      double t = own < stream ? stream : own;
       if (s > 1) t += 3.8 + 8.0 * static_cast<double>(M) * static_cast<double>(N) * s / 4.4e6;
-      if (best_t == 0.0 || t < best_t) {
+      if (best_t == 0.0 || t < best_t || (t == best_t && own < best_own)) {
         best_t = t;
+        best_own = own;
         best.j = j;
         best.splits = s;
       }
