@@ -381,8 +381,9 @@ int qlin_int4_scale_zero_grad(const qlin_qweight *w, const uint16_t *x, int64_t 
  *     a = max_k |x[m][k]|,  scale[m] = RN32(a / 127),
  *     codes[m][k] = round_half_even(127 x[m][k] / a)      (-127 .. 127),
  * and a row of zeros has scale 0 and codes 0.  A row that holds NaN or an
- * infinity has scale NaN and codes 0: whatever is computed from it is NaN for
- * that row and for no other.  The functions of this part are asynchronous and
+ * infinity has scale NaN and codes 0: the values and products of that row are
+ * NaN and no other row's, and sums over the rows that take it up (dA, and
+ * dgamma through its rstd) are NaN altogether.  The functions of this part are asynchronous and
  * report nothing from the device.  Their outputs must overlap neither inputs
  * nor one another nor the workspace (QLIN_E_OVERLAP; the packed weight's arrays
  * are not looked at), so h = residual or dx = dy cannot be formed in place.  [QLoRA "Background: what is
