@@ -122,12 +122,15 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t a, uint32_t b) {
 // columns (four a lane) and a share of the tokens.  Waves: two per SIMD up to
 // rank 64 (128 accumulators each), so that one pairs its operands while the
 // other multiplies; one above.  dB and dA of 4096 tokens, 8192 x 28672, rank
-// 64 (184 MB): 57 us, 3.2 TB/s; the codes alone 35 us.  Timing copies: 42 us
-// without either operand's traffic, 35 with half of the matrix instructions
-// besides, so pairing, matrix work and the two rounds of workgroups (start and
-// join, some 7 us each) weigh more than HBM.  Slower: eight columns a lane and
-// one wave per SIMD 62-65 us, z's planes formed here from fp32 78 us, other
-// numbers of shares 62-74 us.
+// 64 (184 MB): 58 us, 3.2 TB/s; the codes alone 35 us.  No one resource is
+// full there: matrix cores busy 26 % of the cycles, half of the wave cycles
+// waiting to issue.  L2 serves 495 MB for the 184 MB of operands, since every
+// strip reads all of Z's planes again (288 strips, 1 MB each).  Timing copies:
+// 50 us without Z's traffic, 44 without X's, 42 without either's, 35 with half
+// of the matrix instructions besides; two rounds of workgroups pay start and
+// join, some 7 us each.  Slower: eight columns a lane and one wave per SIMD
+// 62-65 us, z's planes formed here from fp32 78 us, other numbers of shares
+// 62-74 us.
 constexpr int kFW = 4, kStrip = 32 * kFW;
 constexpr int tokens_waves(int jt) { return jt <= 2 ? 8 : 4; }
 
@@ -404,7 +407,7 @@ __global__ __launch_bounds__(64 * kDuWaves, FW == 8 ? 1 : 2) void k_du(DuArgs a)
     }
   }
   // Lane (l, g) holds token 16 q + 4 g + v of column c0 + t: item t RT + q.
-  // The waves' sums, in wave order; wave w ends with items w, w + 8, ...
+  // The waves' sums, in wave order; wave w ends with items w, w + 4, ...
 #pragma unroll
   for (int t = 0; t < FW; ++t)
 #pragma unroll

@@ -1032,7 +1032,14 @@ int qlin_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd
 namespace {
 
 constexpr int64_t kMaxTiles = int64_t{1} << 22;  // a launch of 512 threads each stays below 2^32
-constexpr int64_t kFewProductM = 64;  // weight-streaming product up to this many tokens
+// Weight-streaming product up to this many tokens, which is also the most that
+// its LDS holds; the tiled one's lowest tile has 64 rows.  Streaming and tiled,
+// us at 16, 32, 48, 64 tokens: 4096 x 4096 6.9, 8.2, 11.0, 11.8 and 12.1,
+// 13.1, 14.5, 15.6; 7168 x 4096 10.0, 11.4, 13.7, 14.3 and 14.3, 14.6, 16.2,
+// 16.7; 11008 x 4096 15, 21, 20, 20 and 21, 19, 20, 21; 8192 x 8192 22, 24,
+// 27, 28 and 23, 24, 25, 26; 8192 x 28672 50, 55, 59, 62 and 61, 63, 65, 66;
+// 32003 x 4096 32, 42, 43, 44 and 41, 42, 43, 43: at 64 the two meet.
+constexpr int64_t kFewProductM = 64;
 
 struct ProductPlan {
   bool few = false, fits = true;

@@ -23,8 +23,8 @@ __device__ __forceinline__ float norm_rstd(float ss, const RmsNormArgs& a) {
 // sum), so x and the residual are read once: HBM-bound, 9 bytes per element
 // with every output.  T threads hold a row, NV vectors of eight each.  4096 x
 // 8192 with the residual and the values: 53 us, 5.7 TB/s (202 us with a row
-// re-read for each of its three passes); one token of 4096: 3.0 us; 777 x
-// 5003 (rows at any alignment) 9.5 us, one round of workgroups' latency; 4096
+// re-read for each of its three passes); one token of 4096: 3.1 us; 777 x
+// 5003 (rows at any alignment) 8.0 us, one round of workgroups' latency; 4096
 // x 16384 112 us, 5.4 TB/s.
 template <int T, int NV, bool RES>
 __global__ __launch_bounds__(T * rows_per_group(T)) void k_rmsnorm_q8(RmsNormArgs a) {

@@ -298,7 +298,7 @@ __global__ __launch_bounds__(256, 1) void k_w8a8_gemm(W8A8Args a) {
 
 // The shares' sums (integers: exact), scaled and rounded: a thread takes four
 // channels of one token, as the matrix instruction left them.  128 x 8192 in
-// six shares: 7.5 us, 25 MB (3.4 TB/s).
+// eight shares: 8.0 us, 36 MB (4.5 TB/s).
 template <int J>
 __global__ __launch_bounds__(256) void k_w8a8_join(W8A8Args a) {
   const int tiles_m = static_cast<int>((a.M + 64 * J - 1) / (64 * J)), tiles_n = static_cast<int>((a.N + kTN - 1) / kTN);
