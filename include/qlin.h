@@ -424,7 +424,8 @@ int qlin_dequant_q8(const int8_t *codes, const float *scale, int64_t rows, int64
  *   codes, scale  the 8-bit rows of y (outputs)
  *   rstd      fp32[M] (output, may be NULL), for qlin_rmsnorm_bwd
  *   values    bf16[M][d] (output, may be NULL): bf16(fl32(codes * scale))
- * A row whose sum of squares leaves fp32's range counts as non-finite.
+ * A row whose sum of squares passes fp32's range counts as non-finite, and so
+ * does one whose mean square + eps is below its normal numbers (2^-126).
  * Asynchronous on `stream`.
  */
 int qlin_rmsnorm_q8(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t M,

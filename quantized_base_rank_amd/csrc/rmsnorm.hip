@@ -13,10 +13,12 @@ namespace qlin {
 
 namespace {
 
-// Reciprocal root of the mean square; NaN marks a non-finite row.
+// Reciprocal root of the mean square; NaN marks a non-finite row.  A mean
+// below the normal numbers has lost its bits (that of 2^-70 keeps nine); from
+// 2^-126 on the squares that underflow in the sum cost it 2^-24 at most.
 __device__ __forceinline__ float norm_rstd(float ss, const RmsNormArgs& a) {
-  const float r = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
-  return finite_f32(ss) && finite_f32(r) ? r : __uint_as_float(0x7FC00000u);
+  const float mean = ss / static_cast<float>(a.d) + a.eps;
+  return finite_f32(ss) && mean >= 0x1p-126f ? 1.0f / sqrtf(mean) : __uint_as_float(0x7FC00000u);
 }
 
 // The row's sum h = x + res stays in registers as fp32 (one rounding, of the

@@ -42,3 +42,27 @@ def test_backward_from_a_row_of_scale_nan(qb, M, r, pool):
         dxb, dAb, dBb = qb.qlin_bwd_q8(w, q, *args, pool=pool)
         assert torch.equal(dxb, dx) and torch.equal(dBb, dB)   # neither reads x
         assert bool(torch.isnan(dAb.float()).all())            # every element sums over the rows
+
+
+@pytest.mark.parametrize("d", [5, 64, 1000, 4096, 40000])
+def test_norm_of_rows_below_the_normal_range(qb, d):
+    """With eps = 0, a mean square below fp32's normal numbers (2^-126) has lost its bits: a non-finite row, like one
+    of zeros.  At 2^-126 and above, and with an eps that covers it, the row is as exact as any: the squares' sum is
+    off by at most d roundings of 2^-150, which is 2^-24 of d 2^-126, besides its own."""
+    tiny = np.full((4, d), 1.0, np.float32)
+    tiny *= np.float32([2.0 ** -70, 2.0 ** -64, 2.0 ** -63, 2.0 ** -40])[:, None]
+    tiny[:, 1:] *= np.float32([1.0, 1.0, -1.0, 1.0])[:, None]
+    gamma = _bf16(np.ones(d))
+    h, q, rstd, v = qb.qlin_rmsnorm_q8(_bf16(tiny), gamma, 0.0, want_values=True)
+    assert list(np.isnan(rstd.cpu().numpy())) == [True, True, False, False]
+    assert list(np.isnan(q.scale.cpu().numpy())) == [True, True, False, False]
+    assert int(q.codes[:2].count_nonzero()) == 0 and bool((q.codes[2:].abs() == 127).all())
+    u = 2.0 ** -24
+    bound = (d / 64 + 32) * u / 2 + 5 * u   # half of the sum's error, then mean, root, reciprocal
+    want = np.float64([2.0 ** 63, 2.0 ** 40])
+    assert (np.abs(rstd.cpu().numpy()[2:] - want) <= want * bound).all()
+    # eps = 2^-60 covers the first two
+    _, q, rstd, _ = qb.qlin_rmsnorm_q8(_bf16(tiny), gamma, 2.0 ** -60)
+    want = 1 / np.sqrt(np.float64([2.0 ** -140, 2.0 ** -128, 2.0 ** -126, 2.0 ** -80]) + 2.0 ** -60)
+    assert (np.abs(rstd.cpu().numpy() - want) <= want * bound).all()
+    assert bool((q.codes.abs() == 127).all())
