@@ -24,21 +24,24 @@
  *   [QA-LoRA] "QA-LoRA: Quantization-Aware Low-Rank Adaptation of Large
  *             Language Models", abstract (group-wise INT4 operators, merge).
  *
- * Around the layer stand operators on rows held in 8 bits (last part of this
- * file): the norm that feeds it, the product of layers kept in 8 bits, and
- * its backward pass from an 8-bit copy of its input.
+ * Around the layer stand operators on rows held in 8 bits: the norm that
+ * feeds it, the product of layers kept in 8 bits, and its backward pass from
+ * an 8-bit copy of its input; and, between a block's projections, causal
+ * attention with its gradient, and a paged cache of keys and values in 8-bit
+ * rows with the attention that reads it (last part of this file).
  *
  * Conventions for every entry point
  *   - Matrices are dense, row-major, contiguous.  "bf16" and "fp16" buffers
  *     are passed as uint16_t bit patterns.
  *   - Every pointer argument of qlin_quantize_*, qlin_fwd, qlin_bwd,
- *     qlin_dequant_* and the 8-bit row operators is DEVICE memory owned by the caller, except where a
+ *     qlin_dequant_*, the 8-bit row operators and attention is DEVICE memory
+ *     owned by the caller, except where a
  *     comment says "host".  The library never keeps a pointer after a call
  *     returns and never frees caller memory.
  *   - Device pointers must be 16-byte aligned (QLIN_E_ALIGN otherwise).
  *   - Argument errors are reported synchronously, before anything is
- *     enqueued.  qlin_fwd / qlin_bwd / qlin_dequant_bf16 and the 8-bit row
- *     operators are asynchronous on `stream`; a device-side fault surfaces at
+ *     enqueued.  qlin_fwd / qlin_bwd / qlin_dequant_bf16, the 8-bit row
+ *     operators and attention are asynchronous on `stream`; a device-side fault surfaces at
  *     the caller's next synchronisation.  The 4-bit and NormalFloat
  *     quantizers synchronise `stream` and report non-finite input.
  *   - Outputs are overwritten, never accumulated into.
@@ -72,7 +75,7 @@ typedef enum {
   QLIN_E_WORKSPACE = 6,   /* workspace NULL or smaller than qlin_workspace_bytes */
   QLIN_E_HIP = 7,         /* the HIP runtime reported an error                 */
   QLIN_E_OVERLAP = 8      /* an output overlaps an input, another output or the
-                             workspace (8-bit row operators)                   */
+                             workspace (8-bit row operators, attention)        */
 } qlin_status;
 
 /* Packed weight formats. */
@@ -496,6 +499,133 @@ int qlin_bwd_q8(const qlin_qweight *w, const int8_t *xq, const float *x_scale, i
                 const uint16_t *dy, const float *u, uint16_t *dx, uint16_t *dA, uint16_t *dB,
                 void *workspace, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Attention.  Rows of heads are bf16[tokens][heads][dim] with the elements of
+ * a row (one token, all heads) contiguous and the rows `ld` elements apart
+ * (ld a multiple of 8, >= heads * dim), so that q, k and v may be parts of one
+ * product's output.  The tokens of `batch` sequences are packed: those of
+ * sequence b are rows cu[b] .. cu[b + 1] - 1 (cu int32[batch + 1], ascending,
+ * 0 <= cu <= tokens; a sequence may be empty).  Rows that belong to no
+ * sequence are neither used nor written.  Query head h reads key head
+ * h / (heads_q / heads_kv).  For each query i and the keys j at or before its
+ * place,
+ *     s_ij = scale q_i . k_j,   p_ij = exp(s_ij) / sum_j exp(s_ij),
+ *     o_i = sum_j p_ij v_j,     lse_i = log sum_j exp(s_ij);
+ * without any key o_i = 0.  What lies behind the mask has no effect, whatever
+ * it holds; a NaN or an infinity in front of it reaches the queries that see
+ * it.  p is rounded to bf16 for the sum over values, and p and its gradient
+ * for the sums of the backward pass; sums and statistics are fp32, taken in an
+ * order that depends on the sizes only.
+ * Limits (QLIN_E_SHAPE): dim a multiple of 16, 16 .. 128; heads_q a multiple
+ * of heads_kv, at most 128 times it, heads_q <= 4096; tokens * heads_q < 2^31 -
+ * 2^16; 1 <= batch <= 2^20; ld < 2^23; scale finite and > 0.  No tokens: nothing is done.
+ * int32 arrays (cu, lens, table) need 4-byte alignment only.  Outputs must
+ * overlap neither inputs nor one another nor the workspace
+ * (QLIN_E_OVERLAP; parts of one buffer with the same ld may alternate).
+ * The values of int32 arrays are not looked at on the host; out-of-range ones
+ * cannot lead outside the arrays given here, but what they select is not
+ * specified except where said.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Causal attention of packed prompts, each token over its sequence up to
+ * itself.
+ *   q bf16[tokens][heads_q][dim], k, v bf16[tokens][heads_kv][dim]
+ *   o    bf16[tokens][heads_q][dim] (output, dense)
+ *   lse  fp32[tokens][heads_q] (output, may be NULL), for qlin_attn_bwd
+ * Asynchronous on `stream`.
+ */
+int qlin_attn_fwd(const uint16_t *q, int64_t q_ld, const uint16_t *k, int64_t k_ld,
+                  const uint16_t *v, int64_t v_ld, const int32_t *cu, int32_t batch,
+                  int64_t tokens, int32_t heads_q, int32_t heads_kv, int32_t dim, float scale,
+                  uint16_t *o, float *lse, hipStream_t stream);
+
+/*
+ * Its gradient:
+ *     delta_i = do_i . o_i,   ds_ij = p_ij (do_i . v_j - delta_i),
+ *     dv_j = sum_i p_ij do_i, dk_j = scale sum_i ds_ij q_i,
+ *     dq_i = scale sum_j ds_ij k_j,
+ * dk and dv summed over the query heads that share a key head.
+ *   o, lse  from qlin_attn_fwd;  dout bf16[tokens][heads_q][dim] (dense)
+ *   dq, dk, dv  outputs, laid out as q, k, v with row distances of their own
+ *   workspace, ws_bytes  >= qlin_attn_bwd_workspace_bytes(...) (0 for invalid
+ *           sizes); no initial contents needed
+ * A NaN or an infinity anywhere in a sequence may reach all gradients of that
+ * sequence, and no other's.  Asynchronous on `stream`.
+ */
+size_t qlin_attn_bwd_workspace_bytes(int32_t batch, int64_t tokens, int32_t heads_q,
+                                     int32_t heads_kv, int32_t dim);
+int qlin_attn_bwd(const uint16_t *q, int64_t q_ld, const uint16_t *k, int64_t k_ld,
+                  const uint16_t *v, int64_t v_ld, const uint16_t *o, const float *lse,
+                  const uint16_t *dout, const int32_t *cu, int32_t batch, int64_t tokens,
+                  int32_t heads_q, int32_t heads_kv, int32_t dim, float scale, uint16_t *dq,
+                  int64_t dq_ld, uint16_t *dk, int64_t dk_ld, uint16_t *dv, int64_t dv_ld,
+                  void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * A paged cache of keys and values in 8-bit rows (one token, one head): codes
+ * int8[pages][heads][page][dim], scales fp32[pages][heads][page].  page: a
+ * power of two, 16 .. 256; 1 <= pages <= 2^30; heads <= 1024.  Device pointers
+ * in a struct of the caller's.
+ */
+typedef struct {
+  int8_t *k_codes, *v_codes;
+  float *k_scale, *v_scale;
+  int64_t pages;
+  int32_t heads, page, dim;
+} qlin_kv_cache;
+
+/*
+ * The new tokens of a batch of sequences and where the cache holds them.
+ * lens[b] counts sequence b's tokens in the cache with the new ones, which are
+ * its last: of n = cu[b + 1] - cu[b], new token i has place lens[b] - n + i.
+ * Place t sits in row t % page of page table[b][t / page]; a table entry
+ * outside 0 .. pages - 1, and a place outside the table, is a page that is not
+ * there: nothing is written, keys there do not count, and reading gives zeros.
+ * (A place that two tokens share gets one of them.)  1 <= table_len <= 2^24.
+ */
+typedef struct {
+  const int32_t *cu;     /* [batch + 1] */
+  const int32_t *lens;   /* [batch] */
+  const int32_t *table;  /* [batch][table_len] */
+  int32_t batch, table_len;
+  int64_t tokens;        /* packed rows */
+} qlin_kv_batch;
+
+/*
+ * New tokens' keys and values into the cache, rounded as by
+ * qlin_quantize_q8 (a row that holds NaN or an infinity: scale NaN, codes 0).
+ *   k, v  bf16[tokens][heads][dim], rows k_ld, v_ld apart
+ * Asynchronous on `stream`.
+ */
+int qlin_kv_write_q8(const qlin_kv_cache *cache, const qlin_kv_batch *batch, const uint16_t *k,
+                     int64_t k_ld, const uint16_t *v, int64_t v_ld, hipStream_t stream);
+
+/*
+ * The batch's tokens (the last n of each sequence; with n = lens[b] all of
+ * them) read back: k, v bf16[tokens][heads][dim] (outputs, dense),
+ * bf16(fl32(codes * scale)).  Asynchronous on `stream`.
+ */
+int qlin_kv_read_q8(const qlin_kv_cache *cache, const qlin_kv_batch *batch, uint16_t *k,
+                    uint16_t *v, hipStream_t stream);
+
+/*
+ * Attention of the new tokens over the cache, which holds them already: each
+ * over the keys of its sequence up to its own place.  One new token per
+ * sequence is a decoding step, many a piece of a prompt.
+ *   q bf16[tokens][heads_q][dim], rows q_ld apart;  cache->heads key heads
+ *   max_len  no sequence is longer (>= 1; a longer one is taken as this long)
+ *   o        bf16[tokens][heads_q][dim] (output, dense)
+ *   workspace, ws_bytes  >= qlin_attn_q8_workspace_bytes(...) (0 for invalid
+ *            sizes); no initial contents needed
+ * Asynchronous on `stream`.
+ */
+size_t qlin_attn_q8_workspace_bytes(const qlin_kv_cache *cache, const qlin_kv_batch *batch,
+                                    int32_t heads_q, int64_t max_len);
+int qlin_attn_q8(const qlin_kv_cache *cache, const qlin_kv_batch *batch, const uint16_t *q,
+                 int64_t q_ld, int32_t heads_q, float scale, int64_t max_len, uint16_t *o,
+                 void *workspace, size_t ws_bytes, hipStream_t stream);
+
 /*
  * Test helper: writes the dequantized weight W_bf16 (bf16[d_out][d_in]) using
  * the same in-register lookup-table decode as the fused kernels.  Never
@@ -513,7 +643,8 @@ int qlin_dequant_bf16(const qlin_qweight *w, uint16_t *W_out, hipStream_t stream
  * "k_qa_pool_u", "k_qa_dA" (adapter products), "k_int4_scale_zero_grad",
  * "k_quant_q8", "k_rmsnorm_q8", "k_rmsnorm_bwd" (both of its launches),
  * "k_w8a8_few", "k_w8a8_gemm" (with the join of its shares), "k_du",
- * "k_tokens" (8-bit rows).  `start` and `stop` are HIP events created by the caller; the elapsed time between them is the
+ * "k_tokens" (8-bit rows), "k_kv_write", "k_kv_read", "k_attn_fwd",
+ * "k_attn_q8", "k_attn_bwd" (all launches of a call).  `start` and `stop` are HIP events created by the caller; the elapsed time between them is the
  * kernel's duration on the device.  kernel = NULL disarms.  One hook per
  * process (a later call replaces an armed one).  Host only; QLIN_E_NULL for
  * a missing event, QLIN_E_SHAPE for a name of 64 or more characters.

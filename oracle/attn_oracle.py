@@ -1,0 +1,81 @@
+"""fp64 oracle of the attention operators and of the paged 8-bit cache, one
+head of one sequence at a time, with bounds on what the stated roundings may
+move a result by.
+
+Bounds: every rounding to bf16 is off by at most U = 2^-8 of the value, one to
+fp32 by F = 2^-24.  The operators round to bf16: p (for the sum over values),
+p and ds (for the sums of the gradient), o as it enters delta, and the outputs.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+U, F = 2.0 ** -8, 2.0 ** -24
+
+
+def quantize_rows(x):
+    """8-bit rows of x [..., d]: (codes int8, scale fp32)."""
+    x = np.asarray(x, dtype=np.float64)
+    a = np.abs(x).max(axis=-1, keepdims=True)
+    bad = ~np.isfinite(a)
+    safe = np.where(bad | (a == 0), 1.0, a)
+    codes = np.where(bad, 0.0, np.rint(127 * np.where(bad, 0.0, x) / safe)).astype(np.int8)
+    scale = np.where(bad, np.nan, a / 127)[..., 0].astype(np.float32)
+    return codes, scale
+
+
+def _score_slack(q, k, scale, cached):
+    """Absolute bound on the error of scale q_i . k_j in fp32: the sum's D
+    roundings, the scale (and a cached row's own scale) and log2(e), relative
+    to the sum of magnitudes."""
+    return (q.shape[1] + (6 if cached else 4)) * F * scale * (np.abs(q) @ np.abs(k).T)
+
+
+def attend(q, k, v, first, scale, valid=None, cached=False):
+    """q [n][D] at places first .. first + n - 1 over k, v [L][D].  valid [L]:
+    keys that are there.  Returns o, lse, p and the bound of o."""
+    n, L = q.shape[0], k.shape[0]
+    seen = np.arange(L)[None, :] <= first + np.arange(n)[:, None]
+    if valid is not None:
+        seen &= valid[None, :]
+    kz, vz = np.where(seen.any(0)[:, None], k, 0.0), np.where(seen.any(0)[:, None], v, 0.0)
+    with np.errstate(invalid="ignore"):
+        s = np.where(seen, scale * (q @ kz.T), -np.inf)
+    any_ = seen.any(1)
+    top = np.where(any_, s.max(1, initial=-np.inf), 0.0)
+    w = np.where(seen, np.exp(s - top[:, None]), 0.0)
+    total = w.sum(1)
+    p = w / np.where(any_, total, 1.0)[:, None]
+    o = p @ vz
+    with np.errstate(divide="ignore"):
+        lse = np.where(any_, top + np.log(np.where(any_, total, 1.0)), -np.inf)
+    # p's relative error: the score's error twice (numerator, denominator) and
+    # the shifts, powers and sums of fp32 (a score of magnitude |s| log2(e) is
+    # held to F of it on both sides of the subtraction)
+    ds = np.where(seen, _score_slack(q, kz, scale, cached), 0.0)
+    mag = np.where(seen, np.abs(np.where(seen, s, 0.0)), 0.0).max(1, initial=0.0)
+    rel = 2 * (ds.max(1, initial=0.0) + 4 * F * mag) + (L + 40) * F
+    bound = U * np.abs(o) + ((U + rel[:, None]) * (1 + U)) * (p @ np.abs(vz)) * (1 + U)
+    return {"o": o, "lse": lse, "p": p, "rel": rel, "o_bound": bound, "lse_bound": rel + 4 * F * np.abs(np.where(any_, lse, 0.0))}
+
+
+def gradient(q, k, v, do, scale):
+    """Gradient of causal attention of one sequence and head, with bounds."""
+    f = attend(q, k, v, 0, scale)
+    p, o = f["p"], f["o"]
+    delta = (do * o).sum(1)
+    dp = do @ v.T
+    ds = p * (dp - delta[:, None])
+    # delta: o as stored (its bound), fp32 sum; dp: fp32 sum
+    e_delta = (np.abs(do) * f["o_bound"]).sum(1) + 8 * F * (np.abs(do) * np.abs(o)).sum(1)
+    e_dp = (q.shape[1] + 2) * F * (np.abs(do) @ np.abs(v).T)
+    rel = f["rel"][:, None] + f["lse_bound"][:, None]
+    e_ds = p * (1 + rel) * (e_dp + e_delta[:, None]) + (rel + U) * np.abs(ds) * (1 + U)
+    n = q.shape[0]
+    out = {"dq": scale * ds @ k, "dk": scale * ds.T @ q, "dv": p.T @ do}
+    grow = (1 + U) * (1 + 4 * n * F)
+    bounds = {"dq": scale * e_ds @ np.abs(k) * grow + U * np.abs(out["dq"]) + 2 * n * F * scale * np.abs(ds) @ np.abs(k),
+              "dk": scale * e_ds.T @ np.abs(q) * grow + U * np.abs(out["dk"]) + 2 * n * F * scale * np.abs(ds).T @ np.abs(q),
+              "dv": ((U + rel) * p).T @ np.abs(do) * grow + U * np.abs(out["dv"]) + 2 * n * F * p.T @ np.abs(do)}
+    return out, bounds

@@ -16,7 +16,7 @@ from typing import Optional
 import numpy as np
 
 from ._lib import (EXPORTS, LIB_PATH, QLIN_BF16, QLIN_E_WORKSPACE, QLIN_F32, QLIN_FMT_INT4_GROUP, QLIN_FMT_NF,
-                   QLIN_FMT_NF4, QlinError, QWeightStruct, check, lib)
+                   QLIN_FMT_NF4, KVBatchStruct, KVCacheStruct, QlinError, QWeightStruct, check, lib)
 
 __all__ = [
     "QWeight", "QlinError", "qlin_nf4_codebook", "qlin_quantize_nf4", "qlin_nf_codebook",
@@ -24,7 +24,8 @@ __all__ = [
     "qlin_quantize_int4_group", "qlin_workspace_bytes", "qlin_fwd", "qlin_fwd_noalloc", "qlin_bwd",
     "qlin_dequant_bf16", "qlin_qa_merge", "qlin_int4_scale_zero_grad", "qlin_profile_next_launch",
     "Q8Rows", "qlin_quantize_q8", "qlin_dequant_q8", "qlin_rmsnorm_q8", "qlin_rmsnorm_bwd", "qlin_w8a8_fwd",
-    "qlin_bwd_q8", "EXPORTS", "LIB_PATH",
+    "qlin_bwd_q8", "qlin_attn_fwd", "qlin_attn_bwd", "KVCache", "KVBatch", "qlin_kv_write_q8", "qlin_kv_read_q8",
+    "qlin_attn_q8", "EXPORTS", "LIB_PATH",
 ]
 
 
@@ -586,6 +587,240 @@ def qlin_bwd_q8(w: QWeight, x: Q8Rows, A, B, r: int, s: float, dy, u, pool: int 
     check(_call_with_workspace(call, lambda: L.qlin_bwd_q8_workspace_bytes(wref, M, r, pool), dev, st, ws),
           "qlin_bwd_q8")
     return dx, dA, dB
+
+
+# --------------------------------------------------------------- attention
+
+def _rows_ld(t, heads, dim, name) -> int:
+    """Distance of the rows of a bf16 tensor [tokens][heads][dim] whose rows are
+    contiguous (a part of a wider matrix is fine)."""
+    torch = _torch()
+    if t.dim() != 3 or t.dtype is not torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a bfloat16 CUDA tensor [tokens][heads][dim], got {t.dtype} "
+                         f"{tuple(t.shape)} cuda={t.is_cuda}")
+    n, h, d = t.shape
+    if (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise ValueError(f"{name}: expected {heads} heads of {dim}, got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+        raise ValueError(f"{name}: heads and elements of a row have to be contiguous, got strides {t.stride()}")
+    return s0 if n > 1 else -(-h * d // 8) * 8
+
+
+def _i32(t, shape, device, name):
+    torch = _torch()
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: expected contiguous int32 tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
+
+
+def _same_device(device, *named):
+    for t, name in named:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _on(device, f):
+    """f() with `device` as the current one (its stream takes the launches)."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        return f()
+    with torch.cuda.device(device):
+        return f()
+
+
+def qlin_attn_fwd(q, k, v, cu, scale: Optional[float] = None, out=None, lse=None):
+    """Causal attention of packed sequences.  q bf16 [tokens][heads_q][dim], k and
+    v [tokens][heads_kv][dim] (parts of one matrix are fine), cu int32
+    [sequences + 1]: sequence b is rows cu[b] .. cu[b + 1] - 1.  Query head h
+    reads key head h // (heads_q / heads_kv); scale defaults to 1 / sqrt(dim).
+    Returns (out, lse): out bf16 [tokens][heads_q][dim], lse fp32
+    [tokens][heads_q], for qlin_attn_bwd.  Rows that belong to no sequence are
+    not written."""
+    torch = _torch()
+    q_ld = _rows_ld(q, None, None, "q")
+    T, Hq, D = q.shape
+    k_ld = _rows_ld(k, None, D, "k")
+    Hkv = k.shape[1]
+    v_ld = _rows_ld(v, Hkv, D, "v")
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"q, k, v: {T}, {k.shape[0]} and {v.shape[0]} tokens")
+    dev = q.device
+    _i32(cu, (cu.numel(),), dev, "cu")
+    _same_device(dev, (k, "k"), (v, "v"), (out, "out"), (lse, "lse"))
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, torch.bfloat16, (T, Hq, D), "out")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, torch.float32, (T, Hq), "lse")
+    scale = D ** -0.5 if scale is None else float(scale)
+    check(_on(dev, lambda: lib().qlin_attn_fwd(q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+                                               cu.data_ptr(), cu.numel() - 1, T, Hq, Hkv, D, scale, out.data_ptr(),
+                                               lse.data_ptr(), _stream(dev))), "qlin_attn_fwd")
+    return out, lse
+
+
+def qlin_attn_bwd(q, k, v, out, lse, dout, cu, scale: Optional[float] = None, dq=None, dk=None, dv=None, ws=None):
+    """Gradient of qlin_attn_fwd: returns (dq, dk, dv).  out and lse are the
+    forward's.  dq, dk, dv may be given, as parts of one matrix too; rows that
+    belong to no sequence are not written."""
+    torch = _torch()
+    q_ld = _rows_ld(q, None, None, "q")
+    T, Hq, D = q.shape
+    k_ld = _rows_ld(k, None, D, "k")
+    Hkv = k.shape[1]
+    v_ld = _rows_ld(v, Hkv, D, "v")
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"q, k, v: {T}, {k.shape[0]} and {v.shape[0]} tokens")
+    dev = q.device
+    _i32(cu, (cu.numel(),), dev, "cu")
+    _need(out, torch.bfloat16, (T, Hq, D), "out")
+    _need(lse, torch.float32, (T, Hq), "lse")
+    _need(dout, torch.bfloat16, (T, Hq, D), "dout")
+    bf = {"dtype": torch.bfloat16, "device": dev}
+    dq = torch.empty((T, Hq, D), **bf) if dq is None else dq
+    dk = torch.empty((T, Hkv, D), **bf) if dk is None else dk
+    dv = torch.empty((T, Hkv, D), **bf) if dv is None else dv
+    ld = [_rows_ld(t, h, D, n) for t, h, n in ((dq, Hq, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv"))]
+    if dq.shape[0] != T or dk.shape[0] != T or dv.shape[0] != T:
+        raise ValueError(f"dq, dk, dv: expected {T} tokens")
+    _same_device(dev, (k, "k"), (v, "v"), (out, "out"), (lse, "lse"), (dout, "dout"), (dq, "dq"), (dk, "dk"),
+                 (dv, "dv"), (ws, "ws"))
+    scale = D ** -0.5 if scale is None else float(scale)
+    st, L, B = _stream(dev), lib(), cu.numel() - 1
+
+    def call(ws):
+        return L.qlin_attn_bwd(q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, out.data_ptr(), lse.data_ptr(),
+                               dout.data_ptr(), cu.data_ptr(), B, T, Hq, Hkv, D, scale, dq.data_ptr(), ld[0],
+                               dk.data_ptr(), ld[1], dv.data_ptr(), ld[2], ws.data_ptr(), ws.numel(), st)
+
+    check(_on(dev, lambda: _call_with_workspace(call, lambda: L.qlin_attn_bwd_workspace_bytes(B, T, Hq, Hkv, D), dev, st,
+                                                ws)), "qlin_attn_bwd")
+    return dq, dk, dv
+
+
+@dataclasses.dataclass
+class KVCache:
+    """A paged cache of keys and values in 8-bit rows."""
+    k_codes: object               # int8 [pages][heads][page][dim]
+    v_codes: object
+    k_scale: object               # fp32 [pages][heads][page]
+    v_scale: object
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, page: int = 64, device="cuda") -> "KVCache":
+        """A cache of zeros."""
+        torch = _torch()
+        codes = [torch.zeros((pages, heads, page, dim), dtype=torch.int8, device=device) for _ in range(2)]
+        scale = [torch.zeros((pages, heads, page), dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scale)
+
+    @property
+    def device(self):
+        return self.k_codes.device
+
+    def nbytes(self) -> int:
+        return 2 * (self.k_codes.numel() + 4 * self.k_scale.numel())
+
+
+@dataclasses.dataclass
+class KVBatch:
+    """The new tokens of a batch of sequences: sequence b's are packed rows cu[b]
+    .. cu[b + 1] - 1 and the last of its lens[b] tokens in the cache, whose
+    place t is row t % page of page table[b][t // page] (entries outside the
+    cache: no page)."""
+    cu: object                    # int32 [sequences + 1]
+    lens: object                  # int32 [sequences]
+    table: object                 # int32 [sequences][pages per sequence]
+
+
+def _kv_structs(cache: KVCache, batch: KVBatch, tokens: int):
+    torch = _torch()
+    k, v, ks, vs = cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale
+    if k.dim() != 4:
+        raise ValueError(f"cache: expected codes [pages][heads][page][dim], got {tuple(k.shape)}")
+    shape, dev = k.shape, k.device
+    for t, dt, sh, name in ((k, torch.int8, shape, "k_codes"), (v, torch.int8, shape, "v_codes"),
+                            (ks, torch.float32, shape[:3], "k_scale"), (vs, torch.float32, shape[:3], "v_scale")):
+        _need(t, dt, sh, "cache." + name)
+        if t.device != dev:
+            raise ValueError(f"cache.{name}: on {t.device}, expected {dev}")
+    cu, lens, table = batch.cu, batch.lens, batch.table
+    B = cu.numel() - 1
+    if table.dim() != 2:
+        raise ValueError(f"batch.table: expected [sequences][pages], got {tuple(table.shape)}")
+    _i32(cu, (B + 1,), dev, "batch.cu")
+    _i32(lens, (B,), dev, "batch.lens")
+    _i32(table, (B, table.shape[1]), dev, "batch.table")
+    return (KVCacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2], shape[3]),
+            KVBatchStruct(cu.data_ptr(), lens.data_ptr(), table.data_ptr(), B, table.shape[1], tokens), dev)
+
+
+def qlin_kv_write_q8(cache: KVCache, batch: KVBatch, k, v) -> None:
+    """New tokens' keys and values (bf16 [tokens][heads][dim]) into the cache, in
+    8-bit rows."""
+    _, heads, _, dim = cache.k_codes.shape
+    k_ld, v_ld = _rows_ld(k, heads, dim, "k"), _rows_ld(v, heads, dim, "v")
+    if k.shape[0] != v.shape[0]:
+        raise ValueError(f"k, v: {k.shape[0]} and {v.shape[0]} tokens")
+    c, s, dev = _kv_structs(cache, batch, k.shape[0])
+    _same_device(dev, (k, "k"), (v, "v"))
+    check(_on(dev, lambda: lib().qlin_kv_write_q8(ctypes.byref(c), ctypes.byref(s), k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+                                                  _stream(dev))), "qlin_kv_write_q8")
+
+
+def qlin_kv_read_q8(cache: KVCache, batch: KVBatch, tokens: int, k=None, v=None):
+    """The last cu[b + 1] - cu[b] tokens of each sequence read back: (k, v), bf16
+    [tokens][heads][dim].  Rows that belong to no sequence are not written."""
+    torch = _torch()
+    c, s, dev = _kv_structs(cache, batch, tokens)
+    shape = (tokens, c.heads, c.dim)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(k, torch.bfloat16, shape, "k")
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(v, torch.bfloat16, shape, "v")
+    _same_device(dev, (k, "k"), (v, "v"))
+    check(_on(dev, lambda: lib().qlin_kv_read_q8(ctypes.byref(c), ctypes.byref(s), k.data_ptr(), v.data_ptr(),
+                                                 _stream(dev))), "qlin_kv_read_q8")
+    return k, v
+
+
+def qlin_attn_q8(q, cache: KVCache, batch: KVBatch, scale: Optional[float] = None, max_len: Optional[int] = None,
+                 out=None, ws=None):
+    """Attention of a batch's new tokens (bf16 [tokens][heads_q][dim]) over the
+    cache, which holds their keys and values already; each sees its sequence up
+    to itself.  max_len: no sequence is longer (default: what the table
+    holds); the nearer to the longest, the better the work is split.  Returns
+    bf16 [tokens][heads_q][dim]; rows that belong to no sequence are not
+    written."""
+    torch = _torch()
+    dim = cache.k_codes.shape[-1]
+    q_ld = _rows_ld(q, None, dim, "q")
+    T, Hq, _ = q.shape
+    c, s, dev = _kv_structs(cache, batch, T)
+    if out is None:
+        out = torch.empty((T, Hq, dim), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, torch.bfloat16, (T, Hq, dim), "out")
+    _same_device(dev, (q, "q"), (out, "out"), (ws, "ws"))
+    scale = dim ** -0.5 if scale is None else float(scale)
+    held = s.table_len * c.page
+    max_len = held if max_len is None else min(int(max_len), held)
+    st, L, cr, sr = _stream(dev), lib(), ctypes.byref(c), ctypes.byref(s)
+
+    def call(ws):
+        return L.qlin_attn_q8(cr, sr, q.data_ptr(), q_ld, Hq, scale, max_len, out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+
+    check(_on(dev, lambda: _call_with_workspace(call, lambda: L.qlin_attn_q8_workspace_bytes(cr, sr, Hq, max_len), dev,
+                                                st, ws)), "qlin_attn_q8")
+    return out
 
 
 def qlin_profile_next_launch(kernel: Optional[str], start=None, stop=None) -> None:

@@ -41,6 +41,13 @@ EXPORTS = (
     "qlin_w8a8_fwd",
     "qlin_bwd_q8_workspace_bytes",
     "qlin_bwd_q8",
+    "qlin_attn_fwd",
+    "qlin_attn_bwd_workspace_bytes",
+    "qlin_attn_bwd",
+    "qlin_kv_write_q8",
+    "qlin_kv_read_q8",
+    "qlin_attn_q8_workspace_bytes",
+    "qlin_attn_q8",
     "qlin_profile_next_launch",
     "qlin_status_string",
 )
@@ -62,6 +69,30 @@ class QWeightStruct(ctypes.Structure):
     ]
 
 
+class KVCacheStruct(ctypes.Structure):
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+    ]
+
+
+class KVBatchStruct(ctypes.Structure):
+    _fields_ = [
+        ("cu", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("batch", ctypes.c_int32),
+        ("table_len", ctypes.c_int32),
+        ("tokens", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -78,6 +109,7 @@ def lib() -> ctypes.CDLL:
     vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                              ctypes.c_size_t)
     qp = ctypes.POINTER(QWeightStruct)
+    cp, bp = ctypes.POINTER(KVCacheStruct), ctypes.POINTER(KVBatchStruct)
     sig = {
         "qlin_nf4_codebook": (ctypes.c_int, [vp]),
         "qlin_quantize_nf4": (ctypes.c_int, [vp, i64, i64, i32, i32, vp, vp, vp, vp]),
@@ -106,6 +138,14 @@ def lib() -> ctypes.CDLL:
         "qlin_bwd_q8_workspace_bytes": (sz, [qp, i64, i32, i32]),
         "qlin_bwd_q8": (ctypes.c_int,
                         [qp, vp, vp, i64, vp, vp, i32, f32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "qlin_attn_fwd": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i32, i64, i32, i32, i32, f32, vp, vp, vp]),
+        "qlin_attn_bwd_workspace_bytes": (sz, [i32, i64, i32, i32, i32]),
+        "qlin_attn_bwd": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, i64, i32, i32, i32, f32,
+                                         vp, i64, vp, i64, vp, i64, vp, sz, vp]),
+        "qlin_kv_write_q8": (ctypes.c_int, [cp, bp, vp, i64, vp, i64, vp]),
+        "qlin_kv_read_q8": (ctypes.c_int, [cp, bp, vp, vp, vp]),
+        "qlin_attn_q8_workspace_bytes": (sz, [cp, bp, i32, i64]),
+        "qlin_attn_q8": (ctypes.c_int, [cp, bp, vp, i64, i32, f32, i64, vp, vp, sz, vp]),
         "qlin_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     }
     for name, (res, args) in sig.items():

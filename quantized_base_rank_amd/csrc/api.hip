@@ -1162,6 +1162,233 @@ int qlin_bwd_q8(const qlin_qweight* w, const int8_t* xq, const float* x_scale, i
   return hip_status(hooked("k_dx_gemm", stream, [&] { return launch_dx_gemm(a, fmt, stream); }));
 }
 
+// ---------------------------------------------------------------- attention
+
+namespace {
+
+constexpr int32_t kMaxShare = 128;  // query heads of a key head: small_div's range
+
+// Rows of `width` bytes, `pitch` apart (dense memory: one row).
+struct Area {
+  const void* p;
+  int64_t rows, width, pitch;
+};
+Area dense(const void* p, int64_t bytes) { return Area{p, 1, bytes, bytes}; }
+Area heads_area(const void* p, int64_t tokens, int64_t row, int64_t ld) { return Area{p, tokens, 2 * row, 2 * ld}; }
+
+bool areas_meet(const Area& a, const Area& b) {
+  if (a.p == nullptr || b.p == nullptr) return false;
+  const int64_t x = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p));
+  const int64_t y = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p));
+  if (x >= y + (b.rows - 1) * b.pitch + b.width || y >= x + (a.rows - 1) * a.pitch + a.width) return false;
+  if (a.pitch != b.pitch) return true;
+  const int64_t d = ((y - x) % a.pitch + a.pitch) % a.pitch;  // of the same distance: apart within a row?
+  return !(d >= a.width && d + b.width <= a.pitch);
+}
+bool areas_overlap(std::initializer_list<Area> outs, std::initializer_list<Area> ins) {
+  for (const Area* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Area* p = o + 1; p != outs.end(); ++p)
+      if (areas_meet(*o, *p)) return true;
+    for (const Area& i : ins)
+      if (areas_meet(*o, i)) return true;
+  }
+  return false;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_heads(int32_t batch, int64_t tokens, int32_t heads_q, int32_t heads_kv, int32_t dim) {
+  if (batch < 1 || batch > (1 << 20) || tokens < 0) return QLIN_E_SHAPE;
+  if (heads_kv < 1 || heads_q < heads_kv || heads_q > 4096 || heads_q % heads_kv != 0) return QLIN_E_SHAPE;
+  if (heads_q / heads_kv > kMaxShare) return QLIN_E_SHAPE;
+  if (tokens >= (int64_t{1} << 31) || tokens * heads_q >= (int64_t{1} << 31) - (1 << 16)) return QLIN_E_SHAPE;
+  if (dim < 16 || dim > 128 || dim % 16 != 0) return QLIN_E_SHAPE;
+  return QLIN_OK;
+}
+int check_ld(int64_t ld, int64_t row) {
+  return ld < row || ld % 8 != 0 || ld >= (int64_t{1} << 23) ? QLIN_E_SHAPE : QLIN_OK;
+}
+int check_scale(float scale) { return std::isfinite(scale) && scale > 0.0f ? QLIN_OK : QLIN_E_SHAPE; }
+
+int check_cache(const qlin_kv_cache* c, const qlin_kv_batch* s) {
+  if (c == nullptr || s == nullptr) return QLIN_E_NULL;
+  if (c->pages < 1 || c->pages > (int64_t{1} << 30) || c->heads < 1 || c->heads > 1024) return QLIN_E_SHAPE;
+  if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) != 0) return QLIN_E_SHAPE;
+  if (s->table_len < 1 || s->table_len > (1 << 24)) return QLIN_E_SHAPE;
+  return check_heads(s->batch, s->tokens, c->heads, c->heads, c->dim);
+}
+int check_cache_memory(const qlin_kv_cache* c, const qlin_kv_batch* s) {
+  if (c->k_codes == nullptr || c->v_codes == nullptr || c->k_scale == nullptr || c->v_scale == nullptr ||
+      s->cu == nullptr || s->lens == nullptr || s->table == nullptr)
+    return QLIN_E_NULL;
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
+      !aligned4(s->cu) || !aligned4(s->lens) || !aligned4(s->table))
+    return QLIN_E_ALIGN;
+  return QLIN_OK;
+}
+KvCacheArgs cache_args(const qlin_kv_cache* c) {
+  KvCacheArgs a{};
+  a.k = c->k_codes; a.v = c->v_codes; a.ks = c->k_scale; a.vs = c->v_scale;
+  a.pages = static_cast<int32_t>(c->pages); a.H = c->heads; a.page_shift = __builtin_ctz(static_cast<uint32_t>(c->page)); a.D = c->dim;
+  return a;
+}
+KvBatchArgs batch_args(const qlin_kv_batch* s) {
+  KvBatchArgs a{};
+  a.cu = s->cu; a.lens = s->lens; a.table = s->table; a.B = s->batch; a.table_len = s->table_len;
+  a.T = static_cast<int32_t>(s->tokens);
+  return a;
+}
+Area codes_area(const void* p, const qlin_kv_cache* c) { return dense(p, c->pages * c->heads * c->page * c->dim); }
+Area scale_area(const void* p, const qlin_kv_cache* c) { return dense(p, c->pages * c->heads * c->page * 4); }
+Area cu_area(const qlin_kv_batch* s) { return dense(s->cu, 4 * (static_cast<int64_t>(s->batch) + 1)); }
+Area lens_area(const qlin_kv_batch* s) { return dense(s->lens, 4 * static_cast<int64_t>(s->batch)); }
+Area table_area(const qlin_kv_batch* s) { return dense(s->table, 4 * static_cast<int64_t>(s->batch) * s->table_len); }
+
+}  // namespace
+
+int qlin_attn_fwd(const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld, const uint16_t* v, int64_t v_ld,
+                  const int32_t* cu, int32_t batch, int64_t tokens, int32_t heads_q, int32_t heads_kv, int32_t dim,
+                  float scale, uint16_t* o, float* lse, hipStream_t stream) {
+  const int st = check_heads(batch, tokens, heads_q, heads_kv, dim);
+  if (st != QLIN_OK) return st;
+  const int64_t row_q = static_cast<int64_t>(heads_q) * dim, row_kv = static_cast<int64_t>(heads_kv) * dim;
+  if (check_ld(q_ld, row_q) != QLIN_OK || check_ld(k_ld, row_kv) != QLIN_OK || check_ld(v_ld, row_kv) != QLIN_OK ||
+      check_scale(scale) != QLIN_OK)
+    return QLIN_E_SHAPE;
+  if (tokens == 0) return QLIN_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || cu == nullptr || o == nullptr) return QLIN_E_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned4(cu) || !aligned16(o) || !aligned16(lse))
+    return QLIN_E_ALIGN;
+  if (areas_overlap({dense(o, tokens * row_q * 2), dense(lse, tokens * heads_q * 4)},
+              {heads_area(q, tokens, row_q, q_ld), heads_area(k, tokens, row_kv, k_ld),
+               heads_area(v, tokens, row_kv, v_ld), dense(cu, 4 * (static_cast<int64_t>(batch) + 1))}))
+    return QLIN_E_OVERLAP;
+  AttnArgs a{};
+  a.q = q; a.k = k; a.v = v; a.q_ld = q_ld; a.k_ld = k_ld; a.v_ld = v_ld;
+  a.s.cu = cu; a.s.B = batch; a.s.T = static_cast<int32_t>(tokens);
+  a.Hq = heads_q; a.Hkv = heads_kv; a.D = dim; a.g = heads_q / heads_kv; a.g_inv = (65536 + a.g - 1) / a.g;
+  a.c2 = scale * 1.4426950408889634f; a.o = o; a.lse = lse;
+  return hip_status(hooked("k_attn_fwd", stream, [&] { return launch_attn(a, false, stream); }));
+}
+
+size_t qlin_attn_bwd_workspace_bytes(int32_t batch, int64_t tokens, int32_t heads_q, int32_t heads_kv, int32_t dim) {
+  if (check_heads(batch, tokens, heads_q, heads_kv, dim) != QLIN_OK) return 0;
+  return kCounterBytes + 2 * align256(static_cast<size_t>(tokens) * heads_q * sizeof(float));
+}
+
+int qlin_attn_bwd(const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld, const uint16_t* v, int64_t v_ld,
+                  const uint16_t* o, const float* lse, const uint16_t* dout, const int32_t* cu, int32_t batch,
+                  int64_t tokens, int32_t heads_q, int32_t heads_kv, int32_t dim, float scale, uint16_t* dq,
+                  int64_t dq_ld, uint16_t* dk, int64_t dk_ld, uint16_t* dv, int64_t dv_ld, void* workspace,
+                  size_t ws_bytes, hipStream_t stream) {
+  const int st = check_heads(batch, tokens, heads_q, heads_kv, dim);
+  if (st != QLIN_OK) return st;
+  const int64_t row_q = static_cast<int64_t>(heads_q) * dim, row_kv = static_cast<int64_t>(heads_kv) * dim;
+  if (check_ld(q_ld, row_q) != QLIN_OK || check_ld(k_ld, row_kv) != QLIN_OK || check_ld(v_ld, row_kv) != QLIN_OK ||
+      check_ld(dq_ld, row_q) != QLIN_OK || check_ld(dk_ld, row_kv) != QLIN_OK || check_ld(dv_ld, row_kv) != QLIN_OK ||
+      check_scale(scale) != QLIN_OK)
+    return QLIN_E_SHAPE;
+  if (tokens == 0) return QLIN_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || o == nullptr || lse == nullptr || dout == nullptr ||
+      cu == nullptr || dq == nullptr || dk == nullptr || dv == nullptr)
+    return QLIN_E_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dout) ||
+      !aligned4(cu) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return QLIN_E_ALIGN;
+  const size_t need = qlin_attn_bwd_workspace_bytes(batch, tokens, heads_q, heads_kv, dim);
+  if (workspace == nullptr || ws_bytes < need) return QLIN_E_WORKSPACE;
+  if (!aligned16(workspace)) return QLIN_E_ALIGN;
+  if (areas_overlap({heads_area(dq, tokens, row_q, dq_ld), heads_area(dk, tokens, row_kv, dk_ld),
+               heads_area(dv, tokens, row_kv, dv_ld), dense(workspace, static_cast<int64_t>(need))},
+              {heads_area(q, tokens, row_q, q_ld), heads_area(k, tokens, row_kv, k_ld),
+               heads_area(v, tokens, row_kv, v_ld), dense(o, tokens * row_q * 2), dense(lse, tokens * heads_q * 4),
+               dense(dout, tokens * row_q * 2), dense(cu, 4 * (static_cast<int64_t>(batch) + 1))}))
+    return QLIN_E_OVERLAP;
+  AttnBwdArgs a{};
+  a.q = q; a.k = k; a.v = v; a.o = o; a.dout = dout; a.lse = lse; a.q_ld = q_ld; a.k_ld = k_ld; a.v_ld = v_ld;
+  a.cu = cu; a.B = batch; a.T = static_cast<int32_t>(tokens); a.Hq = heads_q; a.Hkv = heads_kv; a.D = dim;
+  a.g = heads_q / heads_kv; a.g_inv = (65536 + a.g - 1) / a.g; a.c2 = scale * 1.4426950408889634f; a.scale = scale;
+  a.dq = dq; a.dk = dk; a.dv = dv; a.dq_ld = dq_ld; a.dk_ld = dk_ld; a.dv_ld = dv_ld;
+  a.lse2 = ws_at<float>(workspace, kCounterBytes);
+  a.delta = ws_at<float>(workspace, kCounterBytes + align256(static_cast<size_t>(tokens) * heads_q * sizeof(float)));
+  return hip_status(hooked("k_attn_bwd", stream, [&] { return launch_attn_bwd(a, stream); }));
+}
+
+int qlin_kv_write_q8(const qlin_kv_cache* cache, const qlin_kv_batch* batch, const uint16_t* k, int64_t k_ld,
+                     const uint16_t* v, int64_t v_ld, hipStream_t stream) {
+  const int st = check_cache(cache, batch);
+  if (st != QLIN_OK) return st;
+  const int64_t row = static_cast<int64_t>(cache->heads) * cache->dim;
+  if (check_ld(k_ld, row) != QLIN_OK || check_ld(v_ld, row) != QLIN_OK) return QLIN_E_SHAPE;
+  if (batch->tokens == 0) return QLIN_OK;
+  if (k == nullptr || v == nullptr) return QLIN_E_NULL;
+  const int sm = check_cache_memory(cache, batch);
+  if (sm != QLIN_OK) return sm;
+  if (!aligned16(k) || !aligned16(v)) return QLIN_E_ALIGN;
+  if (areas_overlap({codes_area(cache->k_codes, cache), codes_area(cache->v_codes, cache), scale_area(cache->k_scale, cache),
+               scale_area(cache->v_scale, cache)},
+              {heads_area(k, batch->tokens, row, k_ld), heads_area(v, batch->tokens, row, v_ld), cu_area(batch),
+               lens_area(batch), table_area(batch)}))
+    return QLIN_E_OVERLAP;
+  KvWriteArgs a{};
+  a.c = cache_args(cache); a.s = batch_args(batch); a.k = k; a.v = v; a.k_ld = k_ld; a.v_ld = v_ld;
+  return hip_status(hooked("k_kv_write", stream, [&] { return launch_kv_write(a, stream); }));
+}
+
+int qlin_kv_read_q8(const qlin_kv_cache* cache, const qlin_kv_batch* batch, uint16_t* k, uint16_t* v,
+                    hipStream_t stream) {
+  const int st = check_cache(cache, batch);
+  if (st != QLIN_OK) return st;
+  if (batch->tokens == 0) return QLIN_OK;
+  if (k == nullptr || v == nullptr) return QLIN_E_NULL;
+  const int sm = check_cache_memory(cache, batch);
+  if (sm != QLIN_OK) return sm;
+  if (!aligned16(k) || !aligned16(v)) return QLIN_E_ALIGN;
+  const int64_t bytes = batch->tokens * cache->heads * cache->dim * 2;
+  if (areas_overlap({dense(k, bytes), dense(v, bytes)},
+              {codes_area(cache->k_codes, cache), codes_area(cache->v_codes, cache), scale_area(cache->k_scale, cache),
+               scale_area(cache->v_scale, cache), cu_area(batch), lens_area(batch), table_area(batch)}))
+    return QLIN_E_OVERLAP;
+  KvReadArgs a{};
+  a.c = cache_args(cache); a.s = batch_args(batch); a.k = k; a.v = v;
+  return hip_status(hooked("k_kv_read", stream, [&] { return launch_kv_read(a, stream); }));
+}
+
+size_t qlin_attn_q8_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int32_t heads_q,
+                                    int64_t max_len) {
+  if (check_cache(cache, batch) != QLIN_OK || max_len < 1 || max_len > (int64_t{1} << 30)) return 0;
+  if (check_heads(batch->batch, batch->tokens, heads_q, cache->heads, cache->dim) != QLIN_OK) return 0;
+  return kCounterBytes;
+}
+
+int qlin_attn_q8(const qlin_kv_cache* cache, const qlin_kv_batch* batch, const uint16_t* q, int64_t q_ld,
+                 int32_t heads_q, float scale, int64_t max_len, uint16_t* o, void* workspace, size_t ws_bytes,
+                 hipStream_t stream) {
+  if (cache == nullptr || batch == nullptr) return QLIN_E_NULL;
+  const size_t need = qlin_attn_q8_workspace_bytes(cache, batch, heads_q, max_len);
+  const int64_t row = static_cast<int64_t>(heads_q) * cache->dim, tokens = batch->tokens;
+  if (need == 0 || check_ld(q_ld, row) != QLIN_OK || check_scale(scale) != QLIN_OK) return QLIN_E_SHAPE;
+  if (tokens == 0) return QLIN_OK;
+  if (q == nullptr || o == nullptr) return QLIN_E_NULL;
+  const int sm = check_cache_memory(cache, batch);
+  if (sm != QLIN_OK) return sm;
+  if (!aligned16(q) || !aligned16(o)) return QLIN_E_ALIGN;
+  if (workspace == nullptr || ws_bytes < need) return QLIN_E_WORKSPACE;
+  if (!aligned16(workspace)) return QLIN_E_ALIGN;
+  if (areas_overlap({dense(o, tokens * row * 2), dense(workspace, static_cast<int64_t>(need))},
+              {heads_area(q, tokens, row, q_ld), codes_area(cache->k_codes, cache), codes_area(cache->v_codes, cache),
+               scale_area(cache->k_scale, cache), scale_area(cache->v_scale, cache), cu_area(batch), lens_area(batch),
+               table_area(batch)}))
+    return QLIN_E_OVERLAP;
+  AttnArgs a{};
+  a.q = q; a.q_ld = q_ld; a.c = cache_args(cache); a.s = batch_args(batch);
+  a.Hq = heads_q; a.Hkv = cache->heads; a.D = cache->dim; a.g = heads_q / cache->heads; a.g_inv = (65536 + a.g - 1) / a.g;
+  // (places outside the table are not there)
+  a.max_len = static_cast<int32_t>(std::min<int64_t>(max_len, int64_t{1} << 30));
+  a.c2 = scale * 1.4426950408889634f; a.o = o;
+  return hip_status(hooked("k_attn_q8", stream, [&] { return launch_attn(a, true, stream); }));
+}
+
 int qlin_profile_next_launch(const char* kernel, hipEvent_t start, hipEvent_t stop) {
   ProfileHook& h = profile_hook();
   std::lock_guard<std::mutex> g(h.m);

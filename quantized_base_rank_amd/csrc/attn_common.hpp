@@ -1,0 +1,138 @@
+// Device helpers of the attention kernels: packed sequences, tiles of query
+// rows, LDS tiles that are read by rows and by columns.
+//
+// Query rows.  The tokens of a sequence times the g = Hq / Hkv query heads
+// that share a key head are one list of rows, r = token * g + head, so that a
+// tile of rows has one set of keys whatever g is, and a single token fills g
+// rows of it.
+#pragma once
+
+#include "device_common.hpp"
+#include "kernels.hpp"
+
+namespace qlin {
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMinusInf = -__builtin_huge_valf();
+
+// First packed token of sequence b.  Whatever the array holds, the tokens
+// named lie in the packed rows.
+__device__ __forceinline__ int seq_start(const int32_t* cu, int b, int T) {
+  const int v = cu[b];
+  return v < 0 ? 0 : v > T ? T : v;
+}
+
+// A tile of `tile` query rows of one sequence.
+struct RowTile {
+  int b;      // sequence
+  int s0, n;  // its first packed token, its tokens
+  int row0;   // first row of the tile
+  int rows;   // rows of the sequence
+};
+
+// Tile t of all sequences' tiles.  Sequence b's tiles are numbered from
+// floor(cu[b] g / tile) + b on: that leaves room for ceil(n g / tile) of them
+// and needs no count of the sequences before.  False: t has no rows.
+__device__ __forceinline__ bool find_rows(const int32_t* cu, int B, int T, int g, int tile, int t, RowTile* out) {
+  int lo = 0, hi = B;  // the last b whose first tile is at or before t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int>(static_cast<int64_t>(seq_start(cu, mid, T)) * g / tile) + mid <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int s0 = seq_start(cu, lo, T), s1 = seq_start(cu, lo + 1, T);
+  const int64_t index = t - (static_cast<int64_t>(s0) * g / tile + lo);
+  out->b = lo;
+  out->s0 = s0;
+  out->n = s1 > s0 ? s1 - s0 : 0;
+  out->rows = out->n * g;
+  if (index < 0 || index * tile >= out->rows) return false;
+  out->row0 = static_cast<int>(index * tile);
+  return true;
+}
+
+// x / g for x < 65536 / g (x g < 65536), with m = ceil(65536 / g).
+__device__ __forceinline__ int small_div(int x, int m) { return (x * m) >> 16; }
+
+// LDS tiles: rows of DP bf16 elements in pieces of 16 bytes, piece c of row r
+// at c ^ piece_swizzle(r).  Eight consecutive rows then have a piece in eight
+// different bank groups (row reads), and the four rows of a transposing read
+// have their pairs of pieces in four.
+template <int DP>
+__device__ __forceinline__ int piece_swizzle(int r) {
+  return DP == 128 ? ((r & 7) << 1) | ((r >> 3) & 1) : ((r & 3) << 1) | ((r >> 2) & 1);
+}
+template <int DP>
+__device__ __forceinline__ int piece_at(int r, int c) {
+  return r * (2 * DP) + ((c ^ piece_swizzle<DP>(r)) << 4);
+}
+
+// Operand of 8 reduction elements from a tile's rows: rows k .. k + 3 and
+// k + 8 .. k + 11 (k = k0 + 4 (lane / 32)) of column c0 + lane % 32.  These are
+// the rows whose sums a 32 x 32 product leaves in this lane's registers
+// 0 .. 7, so that such sums are the other operand as they are.
+template <int DP>
+__device__ __forceinline__ u32x4 column_operand(const uint8_t* tile, int k0, int c0, int lane) {
+  const int p = lane & 15;
+  const int r = k0 + 4 * (lane >> 5) + (p >> 2);
+  const int c = c0 + 16 * ((lane >> 4) & 1) + 4 * (p & 3);
+  const u32x2 lo = ds_read_tr16(tile + piece_at<DP>(r, c >> 3) + (c & 7) * 2);
+  const u32x2 hi = ds_read_tr16(tile + piece_at<DP>(r + 8, c >> 3) + (c & 7) * 2);
+  return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
+
+// Sets the elements that are not finite to zero; 0 if there were none.
+__device__ __forceinline__ uint32_t clear_nonfinite(u32x4& v) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // an exponent of all ones carries into its half's top bit
+    const uint32_t m = ((v[j] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    any |= m;
+    v[j] &= ~((m >> 15) * 0xFFFFu);
+  }
+  return any;
+}
+
+// Registers 8 kg .. 8 kg + 7 of a 32 x 32 product as an operand in bf16.
+__device__ __forceinline__ u32x4 pack_operand(const f32x16& s, int kg) {
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(s[8 * kg + 2 * j], s[8 * kg + 2 * j + 1]);
+  return o;
+}
+
+// Row of a 32 x 32 product's register i in this half of the wave.
+__device__ __forceinline__ int acc_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+
+// Four bf16 codes of a dword of int8 codes, exact.
+__device__ __forceinline__ u32x2 codes_bf16(uint32_t w) {
+  u32x2 o;
+  const float a = static_cast<float>(static_cast<int8_t>(w)), b = static_cast<float>(static_cast<int8_t>(w >> 8));
+  const float c = static_cast<float>(static_cast<int8_t>(w >> 16)), d = static_cast<float>(static_cast<int8_t>(w >> 24));
+  o.x = perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+  o.y = perm(__float_as_uint(d), __float_as_uint(c), 0x07060302u);
+  return o;
+}
+
+// The page that holds place j of sequence b, or -1: a table entry outside the
+// cache, or a place outside the table, is a page that is not there.
+__device__ __forceinline__ int page_of(const int32_t* table, int table_len, int pages, int page_shift, int b, int j) {
+  const int at = j >> page_shift;
+  if (j < 0 || at >= table_len) return -1;
+  const int p = table[static_cast<int64_t>(b) * table_len + at];
+  return p < 0 || p >= pages ? -1 : p;
+}
+
+// Tokens of sequence b in the cache.
+__device__ __forceinline__ int cached_len(const int32_t* lens, int b, int max_len) {
+  const int v = lens[b];
+  return v < 0 ? 0 : v > max_len ? max_len : v;
+}
+
+}  // namespace qlin

@@ -416,4 +416,64 @@ int gemv_dx_tiles(int64_t K);
 int64_t gemv_dx_partial_floats(int64_t N, int64_t K);
 int64_t gemv_dx_dupart_floats(int64_t N, int64_t K, int r);
 
+// ------------------------------------------------------------------ attention
+
+// Packed new tokens of B sequences over a paged cache
+struct KvBatchArgs {
+  const int32_t* cu;     // [B + 1]
+  const int32_t* lens;   // [B]
+  const int32_t* table;  // [B][table_len]
+  int32_t B, table_len, T;
+};
+// 8-bit rows of keys and values: codes [pages][H][1 << page_shift][D], scales
+// [pages][H][1 << page_shift]
+struct KvCacheArgs {
+  int8_t *k, *v;
+  float *ks, *vs;
+  int32_t pages, H, page_shift, D;
+};
+struct KvWriteArgs {
+  KvCacheArgs c;
+  KvBatchArgs s;
+  const uint16_t *k, *v;  // [T] rows of [H][D], k_ld / v_ld elements apart
+  int64_t k_ld, v_ld;
+};
+hipError_t launch_kv_write(const KvWriteArgs& a, hipStream_t stream);
+struct KvReadArgs {
+  KvCacheArgs c;
+  KvBatchArgs s;
+  uint16_t *k, *v;        // [T][H][D]
+};
+hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t stream);
+
+// Causal attention of packed query rows, over packed keys and values or over
+// the cache
+struct AttnArgs {
+  const uint16_t *q, *k, *v;   // rows q_ld, k_ld, v_ld elements apart
+  int64_t q_ld, k_ld, v_ld;
+  KvCacheArgs c;               // (over the cache)
+  KvBatchArgs s;               // (lens, table: over the cache)
+  int32_t Hq, Hkv, D;
+  int32_t g, g_inv;            // Hq / Hkv, ceil(65536 / g)
+  int32_t max_len;
+  float c2;                    // scale log2(e)
+  uint16_t* o;                 // [T][Hq][D]
+  float* lse;                  // [T][Hq] or NULL
+};
+hipError_t launch_attn(const AttnArgs& a, bool paged, hipStream_t stream);
+
+// Its gradient (packed keys and values)
+struct AttnBwdArgs {
+  const uint16_t *q, *k, *v, *o, *dout;
+  const float* lse;
+  int64_t q_ld, k_ld, v_ld;
+  const int32_t* cu;
+  int32_t B, T, Hq, Hkv, D, g, g_inv;
+  float c2, scale;
+  uint16_t *dq, *dk, *dv;      // rows dq_ld, dk_ld, dv_ld elements apart
+  int64_t dq_ld, dk_ld, dv_ld;
+  float *lse2, *delta;         // [Hkv][T g]: lse log2(e), sum do o
+};
+hipError_t launch_attn_bwd(const AttnBwdArgs& a, hipStream_t stream);
+
 }  // namespace qlin

@@ -121,6 +121,21 @@ __device__ __forceinline__ RowScale row_scale(float mx) {
   return r;
 }
 
+// Codes of eight bf16 elements, exact.  p = x inv carries a relative error
+// below 2^-22, and 127 x / a is either exactly a tie or at least
+// 1 / (2 * 127 * 255) > 2^-16 relative away from one (bf16 has 8 significant
+// bits), so rounding p to 17 significant bits restores the ties and moves
+// nothing else onto one; then ties go to even.
+__device__ __forceinline__ u32x2 codes8(u32x4 v, const RowScale& s) {
+  uint32_t q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t p = __float_as_uint(elem8(v, e) * s.pre * s.inv);
+    q[e] = round_bits(__uint_as_float((p + 64u) & ~127u));
+  }
+  return u32x2{low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7])};
+}
+
 // Sizes of a row kernel's instantiations: threads per row, vectors of eight a
 // thread.  One wave per row up to 1024 columns (several rows share a workgroup
 // and nothing needs a barrier), then two or three vectors a thread up to 512

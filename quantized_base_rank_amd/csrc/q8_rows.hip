@@ -20,21 +20,6 @@ __device__ __forceinline__ uint32_t max2_u16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
 }
 
-// Codes of eight bf16 elements, exact.  p = x inv carries a relative error
-// below 2^-22, and 127 x / a is either exactly a tie or at least
-// 1 / (2 * 127 * 255) > 2^-16 relative away from one (bf16 has 8 significant
-// bits), so rounding p to 17 significant bits restores the ties and moves
-// nothing else onto one; then ties go to even.
-__device__ __forceinline__ u32x2 codes8(u32x4 v, const RowScale& s) {
-  uint32_t q[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t p = __float_as_uint(elem8(v, e) * s.pre * s.inv);
-    q[e] = round_bits(__uint_as_float((p + 64u) & ~127u));
-  }
-  return u32x2{low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7])};
-}
-
 // bf16 rows, held in registers between the maximum and the codes: one read
 // of x.  HBM-bound: 3 bytes per element (5 with the values).  4096 x 28672:
 // 59 us, 6.0 TB/s (reading the rows twice took 247 us); 16 rows of 28672, one
