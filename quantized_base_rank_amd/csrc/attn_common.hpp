@@ -99,6 +99,18 @@ __device__ __forceinline__ uint32_t clear_nonfinite(u32x4& v) {
   return any;
 }
 
+// The other half's value, and the larger of both, in each lane.
+__device__ __forceinline__ float swap_halves(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);  // (lower twice, upper twice)
+  return __uint_as_float(__lane_id() < 32 ? r[1] : r[0]);
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // Registers 8 kg .. 8 kg + 7 of a 32 x 32 product as an operand in bf16.
 __device__ __forceinline__ u32x4 pack_operand(const f32x16& s, int kg) {
   u32x4 o;

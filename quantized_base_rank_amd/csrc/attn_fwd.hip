@@ -2,18 +2,28 @@
 // or before token i's place, p the softmax of c q_i . k_j, in one pass over
 // the keys with a running maximum and sum per query row.
 //
-// A workgroup takes 128 query rows (32 per wave) of one sequence and key head
+// A workgroup takes 32 W query rows (32 per wave) of one sequence and key head
 // and walks the keys 64 at a time.  The products are formed transposed,
 // S^T = K Q^T and O^T = V^T P^T: a lane then holds scores of one query row
 // only, so maximum and sum need a single exchange between the wave's halves,
 // and the scores in its registers are, rounded to bf16, the operand of the
 // second product as they stand.
 //
-// Roundings: p (0 .. 1) to bf16 for the second product, relative 2^-9 at most
+// Steps are shifted by one: S of step j + 1 and O of step j are formed
+// together (32 matrix instructions at D = 128), then the softmax of step j + 1.
+// Of eight waves, two on each SIMD, four run their matrix phase while the
+// other four run their softmax, with a barrier between phases.  Keys and values
+// stream through three buffers each.
+//
+// Roundings: p (0 .. 1) to bf16 for the second product, relative 2^-8 at most
 // and independent from key to key, while the sum of p takes the unrounded
 // values; everything else is fp32.  Over the cache, keys and values enter as
 // their integer codes (exact in bf16); a key's scale multiplies its score and
 // a value's scale its p, both in fp32.
+//
+// The maximum that p refers to is raised only once a score passes it by 2^8:
+// p then stays below 2^8 (relative roundings do not change), and most steps
+// leave O and the sum as they are.
 //
 // What is masked does not count whatever it holds: scores behind the mask are
 // replaced, not multiplied, and in steps that the mask cuts, values that are
@@ -26,15 +36,38 @@ namespace qlin {
 
 namespace {
 
-constexpr int kBM = 128;  // query rows of a workgroup
-constexpr int kBN = 64;   // keys of a step
+constexpr int kBN = 64;          // keys of a step
+constexpr float kRaise = 8.0f;   // log2 of what p may reach
 
-template <int DP, bool PAGED>
-__global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
+// 16 bytes a lane from offset `at` of [base, base + bytes) straight into LDS:
+// 1 KB from dst on.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t bytes, uint8_t* dst, uint32_t at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(uniform_rsrc(base, bytes), (lds_ptr_t)dst, 16, at, 0, 0, 0);
+}
+
+// Waits until at most VM of this wave's loads and LG of its LDS accesses are
+// on their way (-1: any number), then meets the other waves.
+template <int VM, int LG>
+__device__ __forceinline__ void barrier() {
+  if constexpr (VM == 0 && LG == 0)
+    __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else if constexpr (VM == 0)
+    __asm__ volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  else if constexpr (LG == 0)
+    __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else
+    __asm__ volatile("s_barrier" ::: "memory");
+}
+
+template <int DP, bool PAGED, int W>
+__global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   constexpr int NP = DP / 8, KS = DP / 16, DB = DP / 32;
-  __shared__ __attribute__((aligned(16))) uint8_t sk[kBN * DP * 2];
-  __shared__ __attribute__((aligned(16))) uint8_t sv[kBN * DP * 2];
-  __shared__ __attribute__((aligned(16))) float s_ks[kBN], s_vs[kBN];
+  constexpr int kBM = 32 * W, kTile = kBN * DP * 2, kLoads = kTile / 1024 / W;
+  static_assert(kLoads >= 1, "every wave loads a part of each tile");
+  constexpr int kRowsPer = 64 / NP;  // rows of a load
+  // [buffer][keys, values]
+  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * 2 * kTile];
+  __shared__ __attribute__((aligned(16))) float s_scale[PAGED ? 3 * 2 * kBN : 1];
 
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -53,10 +86,12 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   const int tok = in ? tok0 + dt : tok0, hq = kvh * a.g + (in ? x - dt * a.g : 0);
   const int seen = in ? first + tok + 1 : 0;  // keys before this place count
   const int last_in = (rt.rows - rt.row0 < kBM ? rt.rows - rt.row0 : kBM) - 1;
-  const int end = first + (rt.row0 + last_in) / a.g + 1;  // keys of the tile's last row
+  const int end = first + tok0 + small_div(rem0 + last_in, a.g_inv) + 1;  // keys of the tile's last row
   const int w_last = wave * 32 + 31 < last_in ? wave * 32 + 31 : last_in;
+  // keys of the wave's last row, and keys that all its rows see
   const int w_end = wave * 32 > last_in ? 0 : first + tok0 + small_div(rem0 + w_last, a.g_inv) + 1;
   const int w_all = wave * 32 + 31 > last_in ? 0 : first + tok0 + small_div(rem0 + wave * 32, a.g_inv) + 1;
+  const int steps = end > 0 ? (end + kBN - 1) / kBN : 0;
 
   u32x4 qf[KS];
   const uint16_t* q = a.q + static_cast<int64_t>(rt.s0 + tok) * a.q_ld + hq * D;
@@ -64,128 +99,253 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   for (int s = 0; s < KS; ++s)
     qf[s] = 16 * s + 8 * h < D ? *reinterpret_cast<const u32x4*>(q + 16 * s + 8 * h) : u32x4{0, 0, 0, 0};
 
-  f32x16 o[DB];
+  // ---- loads of packed keys and values, straight into LDS: load i of a wave
+  // fills kRowsPer rows; rows past the sequence and elements past D lie outside
+  // the resource and read as zero
+  uint32_t vo_k[kLoads], vo_v[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = (wave * kLoads + i) * kRowsPer + lane / NP;
+    const int c = (lane % NP) ^ piece_swizzle<DP>(r);
+    const uint32_t out = 8 * c < D ? 0u : 0x80000000u;
+    vo_k[i] = (static_cast<uint32_t>(r) * static_cast<uint32_t>(a.k_ld * 2) + c * 16) | out;
+    vo_v[i] = (static_cast<uint32_t>(r) * static_cast<uint32_t>(a.v_ld * 2) + c * 16) | out;
+  }
+  auto load_packed = [&](int j, int buf, bool values) {
+    const int64_t ld = values ? a.v_ld : a.k_ld;
+    const int left = len - j * kBN;
+    const uint32_t bytes = left > 0 ? static_cast<uint32_t>(((left < kBN ? left : kBN) - 1) * ld + D) * 2u : 0u;
+    const uint16_t* const src = (values ? a.v : a.k) + (static_cast<int64_t>(rt.s0) + j * kBN) * ld + kvh * D;
+    uint8_t* const dst = lds + buf * (2 * kTile) + (values ? kTile : 0) + wave * kLoads * 1024;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load_to_lds(src, bytes, dst + i * 1024, values ? vo_v[i] : vo_k[i]);
+  };
+  // ---- keys and values from the cache: 16 codes a thread, held in registers
+  // for a step, then written to LDS as bf16.  A wave's rows of a load lie in
+  // one block of 16 keys, so in one page.
+  constexpr int kChunks = DP / 16, kHold = (kBN * kChunks + 64 * W - 1) / (64 * W);
+  const int row_t = tid / kChunks, chunk = tid % kChunks;
+  const int page_mask = (1 << a.c.page_shift) - 1;
+  const bool holds = (kBN * kChunks >= 64 * W || tid < kBN * kChunks) && 16 * chunk < D;
+  uint32_t queue = 0;  // blocks of 16 keys that are there, four bits a step
+  auto page_at = [&](int j, int blk) {
+    const int at = j * kBN + 16 * blk;
+    return at < len ? page_of(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, at) : -1;
+  };
+  auto blocks = [&](int j) {
+    uint32_t b = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b |= page_at(j, i) >= 0 ? 1u << i : 0u;
+    return b;
+  };
+  u32x4 held_k[kHold], held_v[kHold];
+  float held_ks[kHold], held_vs[kHold];
+  auto fetch = [&](int j, bool values) {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const int r = row_t + i * (64 * W / kChunks);
+      const int pg = page_at(j, __builtin_amdgcn_readfirstlane(r >> 4));
+      (values ? held_v : held_k)[i] = u32x4{0, 0, 0, 0};
+      if (pg >= 0 && holds) {
+        const int64_t row = ((static_cast<int64_t>(pg) * a.c.H + kvh) << a.c.page_shift) + ((j * kBN + r) & page_mask);
+        (values ? held_v : held_k)[i] = *reinterpret_cast<const u32x4*>((values ? a.c.v : a.c.k) + row * D + 16 * chunk);
+        if (!values && chunk == 0) {
+          held_ks[i] = a.c.ks[row];
+          held_vs[i] = a.c.vs[row];
+        }
+      }
+    }
+  };
+  auto put = [&](int buf, bool values) {
+    uint8_t* const dst = lds + buf * (2 * kTile) + (values ? kTile : 0);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      if (kBN * kChunks < 64 * W && tid >= kBN * kChunks) break;
+      const int r = row_t + i * (64 * W / kChunks);
+      const u32x4 c = (values ? held_v : held_k)[i];
+      const u32x2 w0 = codes_bf16(c.x), w1 = codes_bf16(c.y), w2 = codes_bf16(c.z), w3 = codes_bf16(c.w);
+      *reinterpret_cast<u32x4*>(dst + piece_at<DP>(r, 2 * chunk)) = u32x4{w0.x, w0.y, w1.x, w1.y};
+      *reinterpret_cast<u32x4*>(dst + piece_at<DP>(r, 2 * chunk + 1)) = u32x4{w2.x, w2.y, w3.x, w3.y};
+      if (!values && chunk == 0) {
+        s_scale[buf * 2 * kBN + r] = held_ks[i];
+        s_scale[buf * 2 * kBN + kBN + r] = held_vs[i];
+      }
+    }
+  };
+
+  // ---- fragments
+  const uint32_t k_at = static_cast<uint32_t>(piece_at<DP>(l32, h));
+  const int p16 = lane & 15, vr = 4 * h + (p16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (p16 & 3);
+  const uint32_t v_at = static_cast<uint32_t>(piece_at<DP>(vr, vc >> 3) + (vc & 7) * 2);
+
+  f32x16 o[DB], s[2];
+  u32x4 pf[4];
 #pragma unroll
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
   float m = kMinusInf, l = 0.0f;
 
-  for (int j0 = 0; j0 < end; j0 += kBN) {
-    uint32_t there = 0xF;  // blocks of 16 keys whose page is there
-    if constexpr (PAGED) {
-      int pg[4];
-      there = 0;
+  auto scores = [&](int buf) {
+    const uint8_t* const sk = lds + buf * (2 * kTile);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pg[i] = j0 + 16 * i < len
-                    ? page_of(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, j0 + 16 * i) : -1;
-        there |= pg[i] >= 0 ? 1u << i : 0u;
+    for (int kb = 0; kb < 2; ++kb) {
+      s[kb] = f32x16{};
+#pragma unroll
+      for (int t = 0; t < KS; ++t)
+        s[kb] = mfma32(*reinterpret_cast<const u32x4*>(sk + (k_at ^ (t << 5)) + kb * 32 * DP * 2), qf[t], s[kb]);
+    }
+  };
+  auto values = [&](int j, int buf) {
+    const uint8_t* const sv = lds + buf * (2 * kTile) + kTile;
+    const int j0 = j * kBN;
+    uint32_t odd = 0;  // non-finite values behind some row's mask
+    const bool cut = !PAGED && j0 + kBN > w_all;
+#pragma unroll
+    for (int kg = 0; kg < 4; ++kg)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        const uint8_t* const at = sv + (v_at ^ (d << 6)) + kg * 16 * DP * 2;
+        const uint8_t* const at8 = sv + (v_at ^ (d << 6) ^ (DP == 128 ? 16 : 0)) + 8 * DP * 2 + kg * 16 * DP * 2;
+        const u32x2 lo = ds_read_tr16(at), hi = ds_read_tr16(at8);
+        u32x4 v = {lo.x, lo.y, hi.x, hi.y};
+        if (!PAGED && cut) odd |= clear_nonfinite(v);
+        o[d] = mfma32(v, pf[kg], o[d]);
       }
+    if (!PAGED && cut && __ballot(odd != 0) != 0) {
+      // they reach, as they are, the rows that see them
+      for (int jj = 0; jj < kBN; ++jj) {
+        if (j0 + jj >= seen) break;
 #pragma unroll
-      for (int i = 0; i < kBN * NP / 256; ++i) {
-        const int idx = tid + 256 * i, r = idx / NP, c = idx % NP, blk = r >> 4;
-        const int p = blk == 0 ? pg[0] : blk == 1 ? pg[1] : blk == 2 ? pg[2] : pg[3];
-        u32x2 ck = {0, 0}, cv = {0, 0};
-        if (p >= 0 && 8 * c < D) {
-          const int64_t row = ((static_cast<int64_t>(p) * a.c.H + kvh) << a.c.page_shift) +
-                              ((j0 + r) & ((1 << a.c.page_shift) - 1));
-          ck = *reinterpret_cast<const u32x2*>(a.c.k + row * D + 8 * c);
-          cv = *reinterpret_cast<const u32x2*>(a.c.v + row * D + 8 * c);
-          if (c == 0) {
-            s_ks[r] = a.c.ks[row] * a.c2;
-            s_vs[r] = a.c.vs[row];
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = 32 * d + acc_row(i, h);
+            const float y = bf16_to_f32(*reinterpret_cast<const uint16_t*>(sv + piece_at<DP>(jj, c >> 3) + (c & 7) * 2));
+            if ((__float_as_uint(y) & 0x7F800000u) == 0x7F800000u) o[d][i] += y;
           }
-        }
-        const u32x2 k0 = codes_bf16(ck.x), k1 = codes_bf16(ck.y), v0 = codes_bf16(cv.x), v1 = codes_bf16(cv.y);
-        *reinterpret_cast<u32x4*>(sk + piece_at<DP>(r, c)) = u32x4{k0.x, k0.y, k1.x, k1.y};
-        *reinterpret_cast<u32x4*>(sv + piece_at<DP>(r, c)) = u32x4{v0.x, v0.y, v1.x, v1.y};
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kBN * NP / 256; ++i) {
-        const int idx = tid + 256 * i, r = idx / NP, c = idx % NP;
-        u32x4 k = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-        if (j0 + r < len && 8 * c < D) {
-          const int64_t row = rt.s0 + j0 + r;
-          k = *reinterpret_cast<const u32x4*>(a.k + row * a.k_ld + kvh * D + 8 * c);
-          v = *reinterpret_cast<const u32x4*>(a.v + row * a.v_ld + kvh * D + 8 * c);
-        }
-        *reinterpret_cast<u32x4*>(sk + piece_at<DP>(r, c)) = k;
-        *reinterpret_cast<u32x4*>(sv + piece_at<DP>(r, c)) = v;
       }
     }
-    __syncthreads();
-    if (j0 < w_end) {
-      f32x16 s[2];
+  };
+  auto softmax = [&](int j, int buf, uint32_t there) {
+    const int j0 = j * kBN;
+    const bool masked = j0 + kBN > w_all || there != 0xFu;
+    const float* const sks = s_scale + (PAGED ? buf * 2 * kBN : 0);
+    if constexpr (PAGED) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        s[kb] = f32x16{};
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int t = 0; t < KS; ++t)
-          s[kb] = mfma32(*reinterpret_cast<const u32x4*>(sk + piece_at<DP>(kb * 32 + l32, 2 * t + h)), qf[t], s[kb]);
-      }
-      const bool masked = j0 + kBN > w_all || there != 0xF;
-      float top = kMinusInf;
+        for (int i = 0; i < 16; i += 4) {
+          const f32x4 ks = *reinterpret_cast<const f32x4*>(sks + kb * 32 + acc_row(i, h));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[kb][i + e] *= ks[e];
+        }
+    }
+    if (masked) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int r = kb * 32 + acc_row(i, h);
-          float t = s[kb][i] * (PAGED ? s_ks[r] : a.c2);
-          if (masked && (j0 + r >= seen || (PAGED && (there >> (2 * kb + (i >> 3)) & 1) == 0))) t = kMinusInf;
-          s[kb][i] = t;
-          top = fmaxf(top, t);
+          if (j0 + r >= seen || (PAGED && (there >> (2 * kb + (i >> 3)) & 1) == 0)) s[kb][i] = kMinusInf;
         }
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float m_new = fmaxf(m, top), shift = m_new == kMinusInf ? 0.0f : m_new;
-      const float alpha = __builtin_amdgcn_exp2f(m - shift);
+    }
+    float top = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
+    top = max_halves(top) * a.c2;
+    if (__ballot(top > m + kRaise) != 0) {
+      const float m_new = top > m + kRaise ? top : m;
+      const float alpha = m_new == kMinusInf ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
       m = m_new;
-      float sum = 0.0f;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(s[kb][i] - shift);
-          sum += p;
-          if constexpr (PAGED) {
-            const int r = kb * 32 + acc_row(i, h);
-            s[kb][i] = masked && s[kb][i] == kMinusInf ? 0.0f : p * s_vs[r];
-          } else {
-            s[kb][i] = p;
-          }
-        }
-      l = l * alpha + sum;
+      l *= alpha;
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[d] *= alpha;
-      uint32_t odd = 0;  // non-finite values behind some row's mask
+    }
+    const float shift = m == kMinusInf ? 0.0f : m;
+    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int kg = 0; kg < 4; ++kg) {
-        const u32x4 p = pack_operand(s[kg >> 1], kg & 1);
+    for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          u32x4 v = column_operand<DP>(sv, 16 * kg, 32 * d, lane);
-          if (!PAGED && masked) odd |= clear_nonfinite(v);
-          o[d] = mfma32(v, p, o[d]);
-        }
-      }
-      if (!PAGED && masked && __ballot(odd != 0) != 0) {
-        // they reach, as they are, the rows that see them
-        for (int j = 0; j < kBN; ++j) {
-          if (j0 + j >= seen) break;
+      for (int i = 0; i < 16; i += 4) {
+        f32x4 vs;
+        if constexpr (PAGED) vs = *reinterpret_cast<const f32x4*>(sks + kBN + kb * 32 + acc_row(i, h));
 #pragma unroll
-          for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int c = 32 * d + acc_row(i, h);
-              const float x = bf16_to_f32(*reinterpret_cast<const uint16_t*>(sv + piece_at<DP>(j, c >> 3) + (c & 7) * 2));
-              if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u) o[d][i] += x;
-            }
+        for (int e = 0; e < 4; ++e) {
+          const float t = s[kb][i + e];
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t, a.c2, -shift));
+          sum[e & 1] += p;
+          // (a masked value's scale may be anything)
+          s[kb][i + e] = !PAGED ? p : masked && t == kMinusInf ? 0.0f : p * vs[e];
         }
       }
     }
-    __syncthreads();
-  }
+    l += sum[0] + sum[1];
+#pragma unroll
+    for (int kg = 0; kg < 4; ++kg) pf[kg] = pack_operand(s[kg >> 1], kg & 1);
+  };
 
-  l += __shfl_xor(l, 32, 64);
+  const bool second = W == 8 && wave >= 4;
+  if (steps > 0) {
+    if constexpr (PAGED) {
+      fetch(0, false);
+      fetch(0, true);
+      put(0, false);
+      put(0, true);
+      fetch(1, false);
+      fetch(1, true);
+      put(1, false);
+      put(1, true);
+      fetch(2, false);
+      put(2, false);
+      fetch(3, false);
+      fetch(2, true);
+      queue = blocks(1) | blocks(2) << 4 | blocks(3) << 8 | blocks(4) << 12;
+      barrier<-1, 0>();
+    } else {
+      load_packed(0, 0, false);
+      load_packed(0, 0, true);
+      load_packed(1, 1, false);
+      load_packed(1, 1, true);
+      load_packed(2, 2, false);
+      barrier<0, 0>();
+    }
+    if (0 < w_end) {
+      scores(0);
+      softmax(0, 0, PAGED ? blocks(0) : 0xFu);
+    }
+    if (second) barrier<-1, -1>();
+    int b0 = 0, b1 = 1, b2 = 2;
+    for (int j = 0; j < steps; ++j) {
+      if constexpr (W == 8) __builtin_amdgcn_s_setprio(1);
+      if ((j + 1) * kBN < w_end) scores(b1);
+      if (j * kBN < w_end) values(j, b0);
+      if constexpr (W == 8) __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      barrier<PAGED ? -1 : 0, -1>();
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (PAGED) {
+        put(b0, false);
+        put(b2, true);
+        fetch(j + 4, false);
+        fetch(j + 3, true);
+      } else {
+        load_packed(j + 3, b0, false);
+        load_packed(j + 2, b2, true);
+      }
+      if ((j + 1) * kBN < w_end) softmax(j + 1, b1, queue & 0xFu);
+      if constexpr (PAGED) queue = queue >> 4 | blocks(j + 5) << 12;
+      __builtin_amdgcn_sched_barrier(0);
+      barrier<-1, PAGED ? 0 : -1>();
+      __builtin_amdgcn_sched_barrier(0);
+      const int b = b0;
+      b0 = b1;
+      b1 = b2;
+      b2 = b;
+    }
+    if (!second && W == 8) barrier<-1, -1>();
+    // (loads on their way into LDS end before the workgroup does)
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+  l += swap_halves(l);
   if (!in) return;
   const int64_t row = static_cast<int64_t>(rt.s0 + tok) * a.Hq + hq;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (no key: 0; NaN stays)
@@ -201,22 +361,18 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   if (a.lse != nullptr && h == 0) a.lse[row] = l == 0.0f ? kMinusInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+template <int DP, bool PAGED, int W>
+hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+  const int64_t tiles = static_cast<int64_t>(a.s.T) * a.g / (32 * W) + a.s.B;
+  hipLaunchKernelGGL((k_attn<DP, PAGED, W>), dim3(static_cast<uint32_t>(tiles * a.Hkv)), dim3(64 * W), 0, stream, a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_attn(const AttnArgs& a, bool paged, hipStream_t stream) {
-  const int64_t tiles = static_cast<int64_t>(a.s.T) * a.g / kBM + a.s.B;
-  const dim3 grid(static_cast<uint32_t>(tiles * a.Hkv));
-  if (a.D <= 64) {
-    if (paged)
-      hipLaunchKernelGGL((k_attn<64, true>), grid, dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((k_attn<64, false>), grid, dim3(256), 0, stream, a);
-  } else if (paged) {
-    hipLaunchKernelGGL((k_attn<128, true>), grid, dim3(256), 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((k_attn<128, false>), grid, dim3(256), 0, stream, a);
-  }
-  return hipGetLastError();
+  if (a.D <= 64) return paged ? launch<64, true, 8>(a, stream) : launch<64, false, 8>(a, stream);
+  return paged ? launch<128, true, 8>(a, stream) : launch<128, false, 8>(a, stream);
 }
 
 }  // namespace qlin
