@@ -1354,11 +1354,47 @@ int qlin_kv_read_q8(const qlin_kv_cache* cache, const qlin_kv_batch* batch, uint
   return hip_status(hooked("k_kv_read", stream, [&] { return launch_kv_read(a, stream); }));
 }
 
+namespace {
+
+// How attention over the cache is split.
+struct ChunkPlan {
+  bool few = false;           // rows of 32 at a time (attn_few.hip)
+  int32_t splits = 1, per = 1 << 30;
+  size_t off_part = 0, off_ml = 0, total = 0;
+};
+
+ChunkPlan make_chunk_plan(const qlin_kv_cache* c, const qlin_kv_batch* s, int32_t heads_q, int64_t max_len) {
+  ChunkPlan p;
+  const int64_t T = s->tokens, g = heads_q / c->heads;
+  const int64_t len = std::min<int64_t>(max_len, static_cast<int64_t>(s->table_len) * c->page);
+  p.few = T * g <= 64 * static_cast<int64_t>(s->batch);
+  const int64_t tiles = (p.few ? s->batch : ceil_div(T * g, 256)) * c->heads;
+  const int64_t step = p.few ? 128 : 512;
+  const int64_t want = p.few ? 2048 : 512;
+  if (tiles < want) {
+    const int64_t per = align256(static_cast<size_t>(ceil_div(len * tiles, want)));
+    p.per = static_cast<int32_t>(std::max<int64_t>(step, per));
+    p.splits = static_cast<int32_t>(std::max<int64_t>(1, ceil_div(len, p.per)));
+  }
+  if (!p.few) p.splits = 1;
+  if (p.splits == 1) p.per = 1 << 30;
+  size_t off = kCounterBytes;
+  if (p.splits > 1) {
+    const size_t rows = static_cast<size_t>(p.splits) * T * heads_q;
+    p.off_part = off; off = align256(off + rows * c->dim * sizeof(float));
+    p.off_ml = off;   off = align256(off + rows * 2 * sizeof(float));
+  }
+  p.total = off;
+  return p;
+}
+
+}  // namespace
+
 size_t qlin_attn_q8_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_batch* batch, int32_t heads_q,
                                     int64_t max_len) {
   if (check_cache(cache, batch) != QLIN_OK || max_len < 1 || max_len > (int64_t{1} << 30)) return 0;
   if (check_heads(batch->batch, batch->tokens, heads_q, cache->heads, cache->dim) != QLIN_OK) return 0;
-  return kCounterBytes;
+  return make_chunk_plan(cache, batch, heads_q, max_len).total;
 }
 
 int qlin_attn_q8(const qlin_kv_cache* cache, const qlin_kv_batch* batch, const uint16_t* q, int64_t q_ld,
@@ -1386,7 +1422,15 @@ int qlin_attn_q8(const qlin_kv_cache* cache, const qlin_kv_batch* batch, const u
   // (places outside the table are not there)
   a.max_len = static_cast<int32_t>(std::min<int64_t>(max_len, int64_t{1} << 30));
   a.c2 = scale * 1.4426950408889634f; a.o = o;
-  return hip_status(hooked("k_attn_q8", stream, [&] { return launch_attn(a, true, stream); }));
+  const ChunkPlan p = make_chunk_plan(cache, batch, heads_q, max_len);
+  a.splits = p.splits;
+  a.per = p.per;
+  a.part = ws_at<float>(workspace, p.off_part);
+  a.ml = ws_at<float>(workspace, p.off_ml);
+  return hip_status(hooked("k_attn_q8", stream, [&] {
+    const hipError_t e = p.few ? launch_attn_few(a, stream) : launch_attn(a, true, stream);
+    return e != hipSuccess || p.splits == 1 ? e : launch_attn_join(a, stream);
+  }));
 }
 
 int qlin_profile_next_launch(const char* kernel, hipEvent_t start, hipEvent_t stop) {

@@ -56,6 +56,19 @@ __device__ __forceinline__ bool find_rows(const int32_t* cu, int B, int T, int g
   return true;
 }
 
+// Sequence of packed token t (-1: of none).
+__device__ __forceinline__ int seq_of(const int32_t* cu, int B, int T, int t) {
+  int lo = 0, hi = B;  // the last b that starts at or before t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (seq_start(cu, mid, T) <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return seq_start(cu, lo, T) <= t && t < seq_start(cu, lo + 1, T) ? lo : -1;
+}
+
 // x / g for x < 65536 / g (x g < 65536), with m = ceil(65536 / g).
 __device__ __forceinline__ int small_div(int x, int m) { return (x * m) >> 16; }
 

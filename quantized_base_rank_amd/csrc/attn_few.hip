@@ -1,0 +1,303 @@
+// Attention of few query rows over the cache (attn_fwd.hip has the formula and
+// the roundings): a decoding step, where the cache is read once and little is
+// computed with it.
+//
+// A workgroup takes 32 query rows of one sequence and key head and a share of
+// the keys; each of its four waves walks every fourth group of 32 keys on its
+// own, with no barrier, so that the loads of three groups per wave are on
+// their way at any time.  Codes go from memory to registers in the order in
+// which the matrix instructions want them:
+//   keys    lane (l, h) loads bytes 32 i + 16 h .. of key l, eight at a time the
+//           operand of one product (the query's elements are taken in the same
+//           order),
+//   values  lane (l, h) loads DP / 32 bytes, elements DP / 32 l .., of each of
+//           the 16 keys whose scores it holds; byte c of eight keys is the
+//           operand for elements DP / 32 l + c, so picking the byte as it is
+//           converted is all the transposing there is.
+// The waves' maxima, sums and O are joined in LDS, the shares' by k_attn_join.
+#include "attn_common.hpp"
+#include "kernels.hpp"
+#include "q8_common.hpp"
+
+namespace qlin {
+
+namespace {
+
+constexpr int kGroup = 32;   // keys of a wave's step
+constexpr int kWaves = 4;
+constexpr float kRaise = 8.0f;  // as in attn_fwd.hip
+
+// One group's codes and scales in registers.
+template <int DB>
+struct Group {
+  u32x4 k[DB];
+  uint32_t v[16];
+  float scale;      // of key l: the key's (h = 0), the value's (h = 1)
+  uint32_t there;   // two blocks of 16 keys
+};
+
+// A word (or half of one) at a lane's offset from a base that is the same for
+// the wave: a buffer load needs one register of address, not two.
+__device__ __forceinline__ uint32_t load_b32(const void* base, uint32_t bytes, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b32(uniform_rsrc(base, bytes), at, 0, 0);
+}
+__device__ __forceinline__ uint32_t load_b16(const void* base, uint32_t bytes, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b16(uniform_rsrc(base, bytes), at, 0, 0);
+}
+template <bool WORD>
+__device__ __forceinline__ uint32_t load_word(const void* base, uint32_t bytes, uint32_t at) {
+  return WORD ? load_b32(base, bytes, at) : load_b16(base, bytes, at);
+}
+
+// Codes 8 e .. 8 e + 7 of a piece of 16, in bf16.
+__device__ __forceinline__ u32x4 codes_operand(u32x4 w, int e) {
+  const u32x2 a = codes_bf16(w[2 * e]), b = codes_bf16(w[2 * e + 1]);
+  return u32x4{a.x, a.y, b.x, b.y};
+}
+// Byte c of eight words, in bf16.
+__device__ __forceinline__ u32x4 byte_operand(const uint32_t* w, int c) {
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = perm(__float_as_uint(static_cast<float>(static_cast<int8_t>(w[2 * j + 1] >> (8 * c)))),
+                __float_as_uint(static_cast<float>(static_cast<int8_t>(w[2 * j] >> (8 * c)))), 0x07060302u);
+  return o;
+}
+
+template <int DP>
+__global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
+  constexpr int KS = DP / 16, DB = DP / 32, kStride = DP + 4;
+  __shared__ __attribute__((aligned(16))) float s_o[kWaves * 32 * kStride];
+  __shared__ float s_m[kWaves * 32], s_l[kWaves * 32];
+
+  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kvh = static_cast<int>(blockIdx.x) % a.Hkv, rest = static_cast<int>(blockIdx.x) / a.Hkv;
+  const int share = rest % a.splits;
+  RowTile rt;
+  if (!find_rows(a.s.cu, a.s.B, a.s.T, a.g, 32, rest / a.splits, &rt)) return;
+  const int D = a.D, len = cached_len(a.s.lens, rt.b, a.max_len), first = len - rt.n;
+  const int begin = share * a.per;
+  if (begin >= len && share > 0) return;  // (shares of a sequence: k_attn_join counts them alike)
+
+  const int tok0 = rt.row0 / a.g, rem0 = rt.row0 - tok0 * a.g;
+  const bool in = rt.row0 + l32 < rt.rows;
+  const int x = rem0 + l32, dt = small_div(x, a.g_inv);
+  const int tok = in ? tok0 + dt : tok0, hq = kvh * a.g + (in ? x - dt * a.g : 0);
+  const int seen = in ? first + tok + 1 : 0;
+  const int last_in = (rt.rows - rt.row0 < 32 ? rt.rows - rt.row0 : 32) - 1;
+  int end = first + tok0 + small_div(rem0 + last_in, a.g_inv) + 1;  // keys of the tile's last row
+  const int all = last_in < 31 ? 0 : first + tok0 + 1;               // keys that every lane's row sees
+  end = end < begin + a.per ? end : begin + a.per;
+  const int page_mask = (1 << a.c.page_shift) - 1;
+
+  u32x4 qf[KS];
+  const uint16_t* q = a.q + static_cast<int64_t>(rt.s0 + tok) * a.q_ld + hq * D;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const int c = 32 * (s >> 1) + 16 * h + 8 * (s & 1);
+    qf[s] = c < D ? *reinterpret_cast<const u32x4*>(q + c) : u32x4{0, 0, 0, 0};
+  }
+
+  // Row (of the cache's rows) of place j0 and whether its page is there; one
+  // that is not is read as page 0 and masked.
+  struct Block {
+    int64_t row;
+    bool there;
+  };
+  auto block_at = [&](int j0) {
+    const int pg = __builtin_amdgcn_readfirstlane(
+        j0 < len ? page_of(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, j0) : -1);
+    return Block{((static_cast<int64_t>(pg < 0 ? 0 : pg) * a.c.H + kvh) << a.c.page_shift) + (j0 & page_mask), pg >= 0};
+  };
+  struct Pages {
+    Block b[2];
+  };
+  auto pages_at = [&](int j0) { return Pages{{block_at(j0), block_at(j0 + 16)}}; };
+  // (lanes past D read the row's start; their sums are not stored)
+  uint32_t v_off[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v_off[e] = acc_row(e, h) * D + (DB * l32 < D ? DB * l32 : 0);
+  auto load = [&](const Pages& p, Group<DB>& g) {
+    const int64_t row = (l32 < 16 ? p.b[0].row : p.b[1].row) + (l32 & 15);
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+      g.k[i] = 32 * i + 16 * h < D ? *reinterpret_cast<const u32x4*>(a.c.k + row * D + 32 * i + 16 * h) : u32x4{0, 0, 0, 0};
+    g.scale = (h == 0 ? a.c.ks : a.c.vs)[row];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g.v[i] = load_word<DB == 4>(a.c.v + p.b[i >> 3].row * D, 16 * D, v_off[i & 7]);
+    g.there = (p.b[0].there ? 1u : 0u) | (p.b[1].there ? 2u : 0u);
+  };
+
+  f32x16 o[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) o[d] = f32x16{};
+  float m = kMinusInf, l = 0.0f;
+  float* const s_scale = s_o + wave * 32 * kStride;  // this wave's, until the join
+  auto step = [&](int j0, const Group<DB>& g) {
+    s_scale[lane] = g.scale;  // [keys', values'][32]
+    f32x16 s = {};
+#pragma unroll
+    for (int t = 0; t < KS; ++t) s = mfma32(codes_operand(g.k[t >> 1], t & 1), qf[t], s);
+    __builtin_amdgcn_wave_barrier();
+    const bool masked = j0 + kGroup > all || g.there != 3u;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const f32x4 ks = *reinterpret_cast<const f32x4*>(s_scale + acc_row(i, h));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i + e] *= ks[e];
+    }
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (j0 + acc_row(i, h) >= seen || (g.there >> (i >> 3) & 1) == 0) s[i] = kMinusInf;
+    }
+    float top = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    top = max_halves(top) * a.c2;
+    if (__ballot(top > m + kRaise) != 0) {
+      const float m_new = top > m + kRaise ? top : m;
+      const float alpha = m_new == kMinusInf ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] *= alpha;
+    }
+    const float shift = m == kMinusInf ? 0.0f : m;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const f32x4 vs = *reinterpret_cast<const f32x4*>(s_scale + 32 + acc_row(i, h));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float t = s[i + e], p = __builtin_amdgcn_exp2f(__builtin_fmaf(t, a.c2, -shift));
+        l += p;
+        s[i + e] = masked && t == kMinusInf ? 0.0f : p * vs[e];  // (a masked value's scale may be anything)
+      }
+    }
+#pragma unroll
+    for (int kg = 0; kg < 2; ++kg) {
+      const u32x4 p = pack_operand(s, kg);
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] = mfma32(byte_operand(g.v + 8 * kg, d), p, o[d]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+
+  // Groups begin + 32 wave, + 128, ...: two in registers, the pages of a third
+  // looked up.  (Places past the end have no page and are masked.)
+  constexpr int kStep = kWaves * kGroup;
+  int j0 = begin + kGroup * wave;
+  if (j0 < end) {
+    Group<DB> g0, g1;
+    load(pages_at(j0), g0);
+    load(pages_at(j0 + kStep), g1);
+    Pages next = pages_at(j0 + 2 * kStep);
+    for (;; j0 += 2 * kStep) {
+      step(j0, g0);
+      if (j0 + kStep >= end) break;
+      load(next, g0);
+      next = pages_at(j0 + 3 * kStep);
+      step(j0 + kStep, g1);
+      if (j0 + 2 * kStep >= end) break;
+      load(next, g1);
+      next = pages_at(j0 + 4 * kStep);
+    }
+  }
+
+  // ---- the waves together
+  l += swap_halves(l);
+  if (h == 0) {
+    s_m[wave * 32 + l32] = m;
+    s_l[wave * 32 + l32] = l;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {  // elements DB r + c of row l32
+    float* const at = s_o + (wave * 32 + l32) * kStride + DB * acc_row(i, h);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) at[d] = o[d][i];
+  }
+  __syncthreads();
+  // thread t: row t / 8, elements 4 (t % 8) + 32 i ..
+  const int r = tid >> 3;
+  if (rt.row0 + r >= rt.rows) return;
+  float mw[kWaves], top = kMinusInf, sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    mw[w] = s_m[w * 32 + r];
+    top = fmaxf(top, mw[w]);
+  }
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    mw[w] = mw[w] == kMinusInf ? 0.0f : __builtin_amdgcn_exp2f(mw[w] - top);
+    sum += s_l[w * 32 + r] * mw[w];
+  }
+  const int xr = rem0 + r, dr = small_div(xr, a.g_inv);
+  const int64_t row = static_cast<int64_t>(rt.s0 + tok0 + dr) * a.Hq + kvh * a.g + xr - dr * a.g;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // (no key: 0; NaN stays)
+  const int64_t part = static_cast<int64_t>(share) * a.s.T * a.Hq + row;
+#pragma unroll
+  for (int i = 0; i < DB; ++i) {
+    const int c = 32 * i + 4 * (tid & 7);
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(s_o + (w * 32 + r) * kStride + c) * mw[w];
+    if (c >= D) continue;
+    if (a.splits == 1)
+      *reinterpret_cast<u32x2*>(a.o + row * D + c) = u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+    else
+      *reinterpret_cast<f32x4*>(a.part + part * D + c) = v;
+  }
+  if (a.splits > 1 && (tid & 7) == 0) *reinterpret_cast<f32x2*>(a.ml + 2 * part) = f32x2{top, sum};
+}
+
+// The shares' sums of a row: sixteen lanes take eight elements each.
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+  const int lane = threadIdx.x & 15;
+  const int64_t rows = static_cast<int64_t>(a.s.T) * a.Hq;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (row >= rows) return;
+  const int b = seq_of(a.s.cu, a.s.B, a.s.T, static_cast<int>(row / a.Hq));
+  if (b < 0) return;
+  const int len = cached_len(a.s.lens, b, a.max_len);
+  const int all = len <= a.per ? 1 : (len - 1) / a.per + 1, shares = all < a.splits ? all : a.splits;
+  float top = kMinusInf, sum = 0.0f;
+  for (int s = 0; s < shares; ++s) top = fmaxf(top, a.ml[2 * (s * rows + row)]);
+  f32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
+  const bool in = 8 * lane < a.D;
+  for (int s = 0; s < shares; ++s) {
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.ml + 2 * (s * rows + row));
+    const float w = ml.x == kMinusInf && ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x == kMinusInf ? 0.0f : ml.x - top);
+    sum += ml.y * w;
+    if (in) {
+      const float* const at = a.part + (s * rows + row) * a.D + 8 * lane;
+      v0 += *reinterpret_cast<const f32x4*>(at) * w;
+      v1 += *reinterpret_cast<const f32x4*>(at + 4) * w;
+    }
+  }
+  if (!in) return;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<u32x4*>(a.o + row * a.D + 8 * lane) =
+      u32x4{pack_bf16x2(v0[0] * inv, v0[1] * inv), pack_bf16x2(v0[2] * inv, v0[3] * inv),
+            pack_bf16x2(v1[0] * inv, v1[1] * inv), pack_bf16x2(v1[2] * inv, v1[3] * inv)};
+}
+
+}  // namespace
+
+hipError_t launch_attn_few(const AttnArgs& a, hipStream_t stream) {
+  const int64_t tiles = static_cast<int64_t>(a.s.T) * a.g / 32 + a.s.B;
+  const dim3 grid(static_cast<uint32_t>(tiles * a.splits * a.Hkv));
+  if (a.D <= 64)
+    hipLaunchKernelGGL((k_attn_few<64>), grid, dim3(64 * kWaves), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_attn_few<128>), grid, dim3(64 * kWaves), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.s.T) * a.Hq;
+  hipLaunchKernelGGL(k_attn_join, dim3(static_cast<uint32_t>((rows + 15) / 16)), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace qlin

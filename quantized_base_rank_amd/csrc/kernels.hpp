@@ -456,11 +456,16 @@ struct AttnArgs {
   int32_t Hq, Hkv, D;
   int32_t g, g_inv;            // Hq / Hkv, ceil(65536 / g)
   int32_t max_len;
+  int32_t splits, per;         // (over the cache) shares of the keys, keys of a share: ChunkPlan
+  float *part, *ml;            // [splits][T][Hq][D] sums, [splits][T][Hq][2] their maximum and total
   float c2;                    // scale log2(e)
   uint16_t* o;                 // [T][Hq][D]
   float* lse;                  // [T][Hq] or NULL
 };
 hipError_t launch_attn(const AttnArgs& a, bool paged, hipStream_t stream);
+// .. of few query rows over the cache, and the join of the shares of either
+hipError_t launch_attn_few(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream);
 
 // Its gradient (packed keys and values)
 struct AttnBwdArgs {

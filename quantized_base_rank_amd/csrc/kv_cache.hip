@@ -19,18 +19,11 @@ struct Place {
   int b, j;
 };
 __device__ __forceinline__ Place place_of(const KvBatchArgs& s, int t) {
-  int lo = 0, hi = s.B;  // the last b that starts at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_start(s.cu, mid, s.T) <= t)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int s0 = seq_start(s.cu, lo, s.T), s1 = seq_start(s.cu, lo + 1, s.T);
-  if (t < s0 || t >= s1) return Place{-1, 0};
-  const int64_t j = static_cast<int64_t>(s.lens[lo]) - (s1 - s0) + (t - s0);
-  return Place{lo, j < 0 || j > 0x7FFFFFFF ? -1 : static_cast<int>(j)};
+  const int b = seq_of(s.cu, s.B, s.T, t);
+  if (b < 0) return Place{-1, 0};
+  const int s0 = seq_start(s.cu, b, s.T), s1 = seq_start(s.cu, b + 1, s.T);
+  const int64_t j = static_cast<int64_t>(s.lens[b]) - (s1 - s0) + (t - s0);
+  return Place{b, j < 0 || j > 0x7FFFFFFF ? -1 : static_cast<int>(j)};
 }
 
 __global__ __launch_bounds__(256) void k_kv_write(KvWriteArgs a) {
