@@ -18,10 +18,25 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMinusInf = -__builtin_huge_valf();
 
+// An element of an int32 array at an index that is the same for the whole wave,
+// by a scalar load: it does not queue behind the wave's loads of keys.
+__device__ __forceinline__ int uniform_i32(const int32_t* p, int64_t i) {
+  typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
+  const uint64_t at = reinterpret_cast<uint64_t>(p + i);
+  const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(at))));
+  const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(at >> 32)));
+  return *(scalar_ptr)((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
 // First packed token of sequence b.  Whatever the array holds, the tokens
 // named lie in the packed rows.
 __device__ __forceinline__ int seq_start(const int32_t* cu, int b, int T) {
   const int v = cu[b];
+  return v < 0 ? 0 : v > T ? T : v;
+}
+
+__device__ __forceinline__ int uniform_start(const int32_t* cu, int b, int T) {
+  const int v = uniform_i32(cu, b);
   return v < 0 ? 0 : v > T ? T : v;
 }
 
@@ -40,12 +55,12 @@ __device__ __forceinline__ bool find_rows(const int32_t* cu, int B, int T, int g
   int lo = 0, hi = B;  // the last b whose first tile is at or before t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (static_cast<int>(static_cast<int64_t>(seq_start(cu, mid, T)) * g / tile) + mid <= t)
+    if (static_cast<int>(static_cast<int64_t>(uniform_start(cu, mid, T)) * g / tile) + mid <= t)
       lo = mid;
     else
       hi = mid;
   }
-  const int s0 = seq_start(cu, lo, T), s1 = seq_start(cu, lo + 1, T);
+  const int s0 = uniform_start(cu, lo, T), s1 = uniform_start(cu, lo + 1, T);
   const int64_t index = t - (static_cast<int64_t>(s0) * g / tile + lo);
   out->b = lo;
   out->s0 = s0;
@@ -154,10 +169,15 @@ __device__ __forceinline__ int page_of(const int32_t* table, int table_len, int 
   return p < 0 || p >= pages ? -1 : p;
 }
 
-// Tokens of sequence b in the cache.
-__device__ __forceinline__ int cached_len(const int32_t* lens, int b, int max_len) {
-  const int v = lens[b];
-  return v < 0 ? 0 : v > max_len ? max_len : v;
+// The same for a place that is the wave's.
+__device__ __forceinline__ int uniform_page(const int32_t* table, int table_len, int pages, int page_shift, int b, int j) {
+  const int at = j >> page_shift;
+  if (j < 0 || at >= table_len) return -1;
+  const int p = uniform_i32(table, static_cast<int64_t>(b) * table_len + at);
+  return p < 0 || p >= pages ? -1 : p;
 }
+
+// A sequence's tokens in the cache as given, in range.
+__device__ __forceinline__ int clamp_len(int v, int max_len) { return v < 0 ? 0 : v > max_len ? max_len : v; }
 
 }  // namespace qlin

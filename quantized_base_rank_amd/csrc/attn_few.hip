@@ -4,16 +4,15 @@
 //
 // A workgroup takes 32 query rows of one sequence and key head and a share of
 // the keys; each of its four waves walks every fourth group of 32 keys on its
-// own, with no barrier, so that the loads of three groups per wave are on
-// their way at any time.  Codes go from memory to registers in the order in
-// which the matrix instructions want them:
-//   keys    lane (l, h) loads bytes 32 i + 16 h .. of key l, eight at a time the
-//           operand of one product (the query's elements are taken in the same
-//           order),
-//   values  lane (l, h) loads DP / 32 bytes, elements DP / 32 l .., of each of
-//           the 16 keys whose scores it holds; byte c of eight keys is the
-//           operand for elements DP / 32 l + c, so picking the byte as it is
-//           converted is all the transposing there is.
+// own, with no barrier, and has the loads of two more groups on their way.
+//   keys    go to registers in the order in which the matrix instructions want
+//           them: lane (l, h) loads bytes 32 i + 16 h .. of key l, eight at a
+//           time the operand of one product (the query's elements are taken
+//           in the same order);
+//   values  go straight to LDS; lane (l, h) reads DP / 32 bytes, elements
+//           DP / 32 l .., of each of the 16 keys whose scores it holds, and
+//           byte c of eight keys is the operand for elements DP / 32 l + c:
+//           picking the byte as it is converted is all the transposing.
 // The waves' maxima, sums and O are joined in LDS, the shares' by k_attn_join.
 #include "attn_common.hpp"
 #include "kernels.hpp"
@@ -27,26 +26,17 @@ constexpr int kGroup = 32;   // keys of a wave's step
 constexpr int kWaves = 4;
 constexpr float kRaise = 8.0f;  // as in attn_fwd.hip
 
-// One group's codes and scales in registers.
+// One group's keys and scales in registers.
 template <int DB>
 struct Group {
   u32x4 k[DB];
-  uint32_t v[16];
   float scale;      // of key l: the key's (h = 0), the value's (h = 1)
   uint32_t there;   // two blocks of 16 keys
 };
 
-// A word (or half of one) at a lane's offset from a base that is the same for
-// the wave: a buffer load needs one register of address, not two.
-__device__ __forceinline__ uint32_t load_b32(const void* base, uint32_t bytes, uint32_t at) {
-  return __builtin_amdgcn_raw_buffer_load_b32(uniform_rsrc(base, bytes), at, 0, 0);
-}
-__device__ __forceinline__ uint32_t load_b16(const void* base, uint32_t bytes, uint32_t at) {
-  return __builtin_amdgcn_raw_buffer_load_b16(uniform_rsrc(base, bytes), at, 0, 0);
-}
-template <bool WORD>
-__device__ __forceinline__ uint32_t load_word(const void* base, uint32_t bytes, uint32_t at) {
-  return WORD ? load_b32(base, bytes, at) : load_b16(base, bytes, at);
+// 1 KB, 16 bytes a lane from offset `at` of [base, base + bytes), into LDS.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t bytes, uint8_t* dst, uint32_t at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(uniform_rsrc(base, bytes), (lds_ptr_t)dst, 16, at, 0, 0, 0);
 }
 
 // Codes 8 e .. 8 e + 7 of a piece of 16, in bf16.
@@ -66,7 +56,12 @@ __device__ __forceinline__ u32x4 byte_operand(const uint32_t* w, int c) {
 
 template <int DP>
 __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
-  constexpr int KS = DP / 16, DB = DP / 32, kStride = DP + 4;
+  constexpr int KS = DP / 16, DB = DP / 32, kTile = kGroup * DP, kStride = 36;
+  // values of three groups a wave (an array each: a read of one is not held
+  // for loads into another)
+  __shared__ __attribute__((aligned(16))) uint8_t sv0[kWaves * kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sv1[kWaves * kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sv2[kWaves * kTile];
   __shared__ __attribute__((aligned(16))) float s_o[kWaves * 32 * kStride];
   __shared__ float s_m[kWaves * 32], s_l[kWaves * 32];
 
@@ -76,7 +71,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
   const int share = rest % a.splits;
   RowTile rt;
   if (!find_rows(a.s.cu, a.s.B, a.s.T, a.g, 32, rest / a.splits, &rt)) return;
-  const int D = a.D, len = cached_len(a.s.lens, rt.b, a.max_len), first = len - rt.n;
+  const int D = a.D, len = clamp_len(uniform_i32(a.s.lens, rt.b), a.max_len), first = len - rt.n;
   const int begin = share * a.per;
   if (begin >= len && share > 0) return;  // (shares of a sequence: k_attn_join counts them alike)
 
@@ -84,11 +79,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
   const bool in = rt.row0 + l32 < rt.rows;
   const int x = rem0 + l32, dt = small_div(x, a.g_inv);
   const int tok = in ? tok0 + dt : tok0, hq = kvh * a.g + (in ? x - dt * a.g : 0);
-  const int seen = in ? first + tok + 1 : 0;
+  const int share_end = begin + a.per;  // (per is 2^30 at most, begin 0 then)
+  const int seen_all = in ? first + tok + 1 : 0, seen = seen_all < share_end ? seen_all : share_end;
   const int last_in = (rt.rows - rt.row0 < 32 ? rt.rows - rt.row0 : 32) - 1;
-  int end = first + tok0 + small_div(rem0 + last_in, a.g_inv) + 1;  // keys of the tile's last row
-  const int all = last_in < 31 ? 0 : first + tok0 + 1;               // keys that every lane's row sees
-  end = end < begin + a.per ? end : begin + a.per;
+  // keys of the tile's last row, and keys that every lane's row sees
+  const int end_all = first + tok0 + small_div(rem0 + last_in, a.g_inv) + 1, end = end_all < share_end ? end_all : share_end;
+  const int all_all = last_in < 31 ? 0 : first + tok0 + 1, all = all_all < share_end ? all_all : share_end;
   const int page_mask = (1 << a.c.page_shift) - 1;
 
   u32x4 qf[KS];
@@ -106,27 +102,33 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
     bool there;
   };
   auto block_at = [&](int j0) {
-    const int pg = __builtin_amdgcn_readfirstlane(
-        j0 < len ? page_of(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, j0) : -1);
+    const int pg = j0 < len ? uniform_page(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, j0) : -1;
     return Block{((static_cast<int64_t>(pg < 0 ? 0 : pg) * a.c.H + kvh) << a.c.page_shift) + (j0 & page_mask), pg >= 0};
   };
   struct Pages {
     Block b[2];
   };
   auto pages_at = [&](int j0) { return Pages{{block_at(j0), block_at(j0 + 16)}}; };
-  // (lanes past D read the row's start; their sums are not stored)
-  uint32_t v_off[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v_off[e] = acc_row(e, h) * D + (DB * l32 < D ? DB * l32 : 0);
-  auto load = [&](const Pages& p, Group<DB>& g) {
+  // load i of a group's values: rows of one block of 16 keys, 1 KB
+  constexpr int kPieces = DP / 16, kRows = 64 / kPieces, kLoads = kTile / 1024;
+  const uint32_t v_load = static_cast<uint32_t>((lane / kPieces) * D + (lane % kPieces) * 16) |
+                          (16 * (lane % kPieces) < D ? 0u : 0x80000000u);
+  auto load = [&](const Pages& p, Group<DB>& g, uint8_t* sv) __attribute__((always_inline)) {
+    // (lanes past D read the row's start: the query's elements are zero there)
     const int64_t row = (l32 < 16 ? p.b[0].row : p.b[1].row) + (l32 & 15);
+    const int8_t* const k = a.c.k + row * D;
 #pragma unroll
-    for (int i = 0; i < DB; ++i)
-      g.k[i] = 32 * i + 16 * h < D ? *reinterpret_cast<const u32x4*>(a.c.k + row * D + 32 * i + 16 * h) : u32x4{0, 0, 0, 0};
+    for (int i = 0; i < DB; ++i) g.k[i] = *reinterpret_cast<const u32x4*>(k + (32 * i + 16 * h < D ? 32 * i + 16 * h : 0));
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      load_to_lds(a.c.v + (p.b[i * kRows / 16].row + i * kRows % 16) * D, p.b[i * kRows / 16].there ? static_cast<uint32_t>(kRows * D) : 0u,
+                  sv + wave * kTile + i * 1024, v_load);
     g.scale = (h == 0 ? a.c.ks : a.c.vs)[row];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) g.v[i] = load_word<DB == 4>(a.c.v + p.b[i >> 3].row * D, 16 * D, v_off[i & 7]);
     g.there = (p.b[0].there ? 1u : 0u) | (p.b[1].there ? 2u : 0u);
+  };
+  // waits for a group's loads, N groups' on their way behind them
+  auto landed = [&](auto n) __attribute__((always_inline)) {
+    __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(n)::value * (DB + kLoads + 1)) : "memory");
   };
 
   f32x16 o[DB];
@@ -134,7 +136,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
   float m = kMinusInf, l = 0.0f;
   float* const s_scale = s_o + wave * 32 * kStride;  // this wave's, until the join
-  auto step = [&](int j0, const Group<DB>& g) {
+  const uint32_t v_at = static_cast<uint32_t>(wave * kTile + 4 * h * DP + DB * l32);
+  auto step = [&](int j0, const Group<DB>& g, const uint8_t* sv) __attribute__((always_inline)) {
     s_scale[lane] = g.scale;  // [keys', values'][32]
     f32x16 s = {};
 #pragma unroll
@@ -178,32 +181,46 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
 #pragma unroll
     for (int kg = 0; kg < 2; ++kg) {
       const u32x4 p = pack_operand(s, kg);
+      uint32_t v[8];
 #pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] = mfma32(byte_operand(g.v + 8 * kg, d), p, o[d]);
+      for (int e = 0; e < 8; ++e) {
+        const uint8_t* const at = sv + v_at + (16 * kg + acc_row(e, 0)) * DP;
+        v[e] = DB == 4 ? *reinterpret_cast<const uint32_t*>(at) : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at));
+      }
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] = mfma32(byte_operand(v, d), p, o[d]);
     }
     __builtin_amdgcn_wave_barrier();
   };
 
-  // Groups begin + 32 wave, + 128, ...: two in registers, the pages of a third
-  // looked up.  (Places past the end have no page and are masked.)
+  // Groups begin + 32 wave, + 128, ...: the pages of a fourth are looked up.
+  // (Places past the end are masked.)
   constexpr int kStep = kWaves * kGroup;
   int j0 = begin + kGroup * wave;
   if (j0 < end) {
-    Group<DB> g0, g1;
-    load(pages_at(j0), g0);
-    load(pages_at(j0 + kStep), g1);
-    Pages next = pages_at(j0 + 2 * kStep);
-    for (;; j0 += 2 * kStep) {
-      step(j0, g0);
-      if (j0 + kStep >= end) break;
-      load(next, g0);
-      next = pages_at(j0 + 3 * kStep);
-      step(j0 + kStep, g1);
-      if (j0 + 2 * kStep >= end) break;
-      load(next, g1);
+    Group<DB> g0, g1, g2;
+    load(pages_at(j0), g0, sv0);
+    load(pages_at(j0 + kStep), g1, sv1);
+    load(pages_at(j0 + 2 * kStep), g2, sv2);
+    Pages next = pages_at(j0 + 3 * kStep);
+    constexpr std::integral_constant<int, 2> two{};
+    for (; j0 < end; j0 += 3 * kStep) {  // (no way out in between: it would move O about)
+      landed(two);
+      step(j0, g0, sv0);
+      load(next, g0, sv0);
       next = pages_at(j0 + 4 * kStep);
+      landed(two);
+      step(j0 + kStep, g1, sv1);
+      load(next, g1, sv1);
+      next = pages_at(j0 + 5 * kStep);
+      landed(two);
+      step(j0 + 2 * kStep, g2, sv2);
+      load(next, g2, sv2);
+      next = pages_at(j0 + 6 * kStep);
     }
   }
+  // (loads on their way into LDS end before the workgroup does)
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // ---- the waves together
   l += swap_halves(l);
@@ -211,16 +228,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
     s_m[wave * 32 + l32] = m;
     s_l[wave * 32 + l32] = l;
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {  // elements DB r + c of row l32
-    float* const at = s_o + (wave * 32 + l32) * kStride + DB * acc_row(i, h);
-#pragma unroll
-    for (int d = 0; d < DB; ++d) at[d] = o[d][i];
-  }
+  // thread t: row t / 8, elements 4 (t % 8) .. of each 32
   __syncthreads();
-  // thread t: row t / 8, elements 4 (t % 8) + 32 i ..
   const int r = tid >> 3;
-  if (rt.row0 + r >= rt.rows) return;
   float mw[kWaves], top = kMinusInf, sum = 0.0f;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
@@ -232,23 +242,35 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
     mw[w] = mw[w] == kMinusInf ? 0.0f : __builtin_amdgcn_exp2f(mw[w] - top);
     sum += s_l[w * 32 + r] * mw[w];
   }
+  const bool stored = rt.row0 + r < rt.rows;
   const int xr = rem0 + r, dr = small_div(xr, a.g_inv);
   const int64_t row = static_cast<int64_t>(rt.s0 + tok0 + dr) * a.Hq + kvh * a.g + xr - dr * a.g;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // (no key: 0; NaN stays)
   const int64_t part = static_cast<int64_t>(share) * a.s.T * a.Hq + row;
 #pragma unroll
   for (int i = 0; i < DB; ++i) {
+    // the rows' elements 32 i ..: a lane has DB elements of each acc_row, of
+    // which 32 / DB rows are in this part
+    if (i > 0) __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (acc_row(e, 0) * DB / 32 == i) {  // (the other half's rows lie in the same part)
+        float* const at = s_o + (wave * 32 + l32) * kStride + DB * acc_row(e, h) - 32 * i;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) at[d] = o[d][e];
+      }
+    __syncthreads();
     const int c = 32 * i + 4 * (tid & 7);
     f32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(s_o + (w * 32 + r) * kStride + c) * mw[w];
-    if (c >= D) continue;
+    for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(s_o + (w * 32 + r) * kStride + c - 32 * i) * mw[w];
+    if (c >= D || !stored) continue;
     if (a.splits == 1)
       *reinterpret_cast<u32x2*>(a.o + row * D + c) = u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
     else
       *reinterpret_cast<f32x4*>(a.part + part * D + c) = v;
   }
-  if (a.splits > 1 && (tid & 7) == 0) *reinterpret_cast<f32x2*>(a.ml + 2 * part) = f32x2{top, sum};
+  if (a.splits > 1 && stored && (tid & 7) == 0) *reinterpret_cast<f32x2*>(a.ml + 2 * part) = f32x2{top, sum};
 }
 
 // The shares' sums of a row: sixteen lanes take eight elements each.
@@ -259,7 +281,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   if (row >= rows) return;
   const int b = seq_of(a.s.cu, a.s.B, a.s.T, static_cast<int>(row / a.Hq));
   if (b < 0) return;
-  const int len = cached_len(a.s.lens, b, a.max_len);
+  const int len = clamp_len(a.s.lens[b], a.max_len);
   const int all = len <= a.per ? 1 : (len - 1) / a.per + 1, shares = all < a.splits ? all : a.splits;
   float top = kMinusInf, sum = 0.0f;
   for (int s = 0; s < shares; ++s) top = fmaxf(top, a.ml[2 * (s * rows + row)]);

@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   const int tiles = static_cast<int>(gridDim.x) / a.Hkv;
   RowTile rt;
   if (!find_rows(a.s.cu, a.s.B, a.s.T, a.g, kBM, tiles - 1 - static_cast<int>(blockIdx.x) / a.Hkv, &rt)) return;
-  const int D = a.D, len = PAGED ? cached_len(a.s.lens, rt.b, a.max_len) : rt.n;
+  const int D = a.D, len = PAGED ? clamp_len(uniform_i32(a.s.lens, rt.b), a.max_len) : rt.n;
   const int first = len - rt.n;  // place of the first new token
 
   // this lane's query row
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   uint32_t queue = 0;  // blocks of 16 keys that are there, four bits a step
   auto page_at = [&](int j, int blk) {
     const int at = j * kBN + 16 * blk;
-    return at < len ? page_of(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, at) : -1;
+    return at < len ? uniform_page(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, at) : -1;
   };
   auto blocks = [&](int j) {
     uint32_t b = 0;
