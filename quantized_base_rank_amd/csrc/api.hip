@@ -1356,6 +1356,8 @@ int qlin_kv_read_q8(const qlin_kv_cache* cache, const qlin_kv_batch* batch, uint
 
 namespace {
 
+constexpr int64_t kFewChunkRows = 64;
+
 // How attention over the cache is split.
 struct ChunkPlan {
   bool few = false;           // rows of 32 at a time (attn_few.hip)
@@ -1367,16 +1369,13 @@ ChunkPlan make_chunk_plan(const qlin_kv_cache* c, const qlin_kv_batch* s, int32_
   ChunkPlan p;
   const int64_t T = s->tokens, g = heads_q / c->heads;
   const int64_t len = std::min<int64_t>(max_len, static_cast<int64_t>(s->table_len) * c->page);
-  p.few = T * g <= 64 * static_cast<int64_t>(s->batch);
-  const int64_t tiles = (p.few ? s->batch : ceil_div(T * g, 256)) * c->heads;
-  const int64_t step = p.few ? 128 : 512;
-  const int64_t want = p.few ? 2048 : 512;
+  p.few = T * g <= kFewChunkRows * static_cast<int64_t>(s->batch);
+  const int64_t tiles = std::max<int64_t>(s->batch, ceil_div(T * g, 256)) * c->heads;
+  const int64_t want = p.few ? 1536 : 256, unit = p.few ? 128 : 64, least = p.few ? 128 : 512;
   if (tiles < want) {
-    const int64_t per = align256(static_cast<size_t>(ceil_div(len * tiles, want)));
-    p.per = static_cast<int32_t>(std::max<int64_t>(step, per));
-    p.splits = static_cast<int32_t>(std::max<int64_t>(1, ceil_div(len, p.per)));
+    p.per = static_cast<int32_t>(std::max<int64_t>(least, unit * ceil_div(ceil_div(len * tiles, want), unit)));
+    p.splits = static_cast<int32_t>(ceil_div(len, p.per));
   }
-  if (!p.few) p.splits = 1;
   if (p.splits == 1) p.per = 1 << 30;
   size_t off = kCounterBytes;
   if (p.splits > 1) {

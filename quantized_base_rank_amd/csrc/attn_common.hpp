@@ -40,6 +40,21 @@ __device__ __forceinline__ int uniform_start(const int32_t* cu, int b, int T) {
   return v < 0 ? 0 : v > T ? T : v;
 }
 
+// The last b < B for which f holds (f holds up to some b and no further; 0 if
+// it never does), by a whole wave with one b for all: 64 candidates at a time.
+template <typename F>
+__device__ __forceinline__ int last_of(int B, F f) {
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int stride = (n + 63) >> 6, at = lo + static_cast<int>(__lane_id()) * stride;
+    const int yes = __popcll(__ballot(at < lo + n && f(at)));
+    const int skip = yes > 0 ? (yes - 1) * stride : 0;
+    lo += skip;
+    n = n - skip < stride ? n - skip : stride;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // A tile of `tile` query rows of one sequence.
 struct RowTile {
   int b;      // sequence
@@ -52,14 +67,9 @@ struct RowTile {
 // floor(cu[b] g / tile) + b on: that leaves room for ceil(n g / tile) of them
 // and needs no count of the sequences before.  False: t has no rows.
 __device__ __forceinline__ bool find_rows(const int32_t* cu, int B, int T, int g, int tile, int t, RowTile* out) {
-  int lo = 0, hi = B;  // the last b whose first tile is at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (static_cast<int>(static_cast<int64_t>(uniform_start(cu, mid, T)) * g / tile) + mid <= t)
-      lo = mid;
-    else
-      hi = mid;
-  }
+  const int lo = last_of(B, [&](int b) {
+    return static_cast<int>(static_cast<int64_t>(seq_start(cu, b, T)) * g / tile) + b <= t;
+  });
   const int s0 = uniform_start(cu, lo, T), s1 = uniform_start(cu, lo + 1, T);
   const int64_t index = t - (static_cast<int64_t>(s0) * g / tile + lo);
   out->b = lo;
@@ -71,17 +81,10 @@ __device__ __forceinline__ bool find_rows(const int32_t* cu, int B, int T, int g
   return true;
 }
 
-// Sequence of packed token t (-1: of none).
+// Sequence of packed token t (-1: of none), one t for the whole wave.
 __device__ __forceinline__ int seq_of(const int32_t* cu, int B, int T, int t) {
-  int lo = 0, hi = B;  // the last b that starts at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_start(cu, mid, T) <= t)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return seq_start(cu, lo, T) <= t && t < seq_start(cu, lo + 1, T) ? lo : -1;
+  const int b = last_of(B, [&](int i) { return seq_start(cu, i, T) <= t; });
+  return uniform_start(cu, b, T) <= t && t < uniform_start(cu, b + 1, T) ? b : -1;
 }
 
 // x / g for x < 65536 / g (x g < 65536), with m = ceil(65536 / g).

@@ -102,7 +102,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
     bool there;
   };
   auto block_at = [&](int j0) {
-    const int pg = j0 < len ? uniform_page(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, j0) : -1;
+    const int pg = j0 < end ? uniform_page(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, j0) : -1;
     return Block{((static_cast<int64_t>(pg < 0 ? 0 : pg) * a.c.H + kvh) << a.c.page_shift) + (j0 & page_mask), pg >= 0};
   };
   struct Pages {
@@ -204,7 +204,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
     load(pages_at(j0 + 2 * kStep), g2, sv2);
     Pages next = pages_at(j0 + 3 * kStep);
     constexpr std::integral_constant<int, 2> two{};
-    for (; j0 < end; j0 += 3 * kStep) {  // (no way out in between: it would move O about)
+    constexpr std::integral_constant<int, 1> one{};
+    // whole turns of the three, then what is left (a way out inside the loop
+    // would move O about)
+    for (; j0 + 2 * kStep < end; j0 += 3 * kStep) {
       landed(two);
       step(j0, g0, sv0);
       load(next, g0, sv0);
@@ -217,6 +220,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
       step(j0 + 2 * kStep, g2, sv2);
       load(next, g2, sv2);
       next = pages_at(j0 + 6 * kStep);
+    }
+    if (j0 < end) {
+      landed(two);
+      step(j0, g0, sv0);
+    }
+    if (j0 + kStep < end) {
+      landed(one);
+      step(j0 + kStep, g1, sv1);
     }
   }
   // (loads on their way into LDS end before the workgroup does)
@@ -273,33 +284,46 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_few(AttnArgs a) {
   if (a.splits > 1 && stored && (tid & 7) == 0) *reinterpret_cast<f32x2*>(a.ml + 2 * part) = f32x2{top, sum};
 }
 
-// The shares' sums of a row: sixteen lanes take eight elements each.
+// The shares' sums of a row, in a wave: its quarters take every fourth share,
+// sixteen lanes eight elements each.
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  const int lane = threadIdx.x & 15;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
   const int64_t rows = static_cast<int64_t>(a.s.T) * a.Hq;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   if (row >= rows) return;
   const int b = seq_of(a.s.cu, a.s.B, a.s.T, static_cast<int>(row / a.Hq));
   if (b < 0) return;
-  const int len = clamp_len(a.s.lens[b], a.max_len);
-  const int all = len <= a.per ? 1 : (len - 1) / a.per + 1, shares = all < a.splits ? all : a.splits;
+  const int len = clamp_len(uniform_i32(a.s.lens, b), a.max_len);
+  const int held = len <= a.per ? 1 : (len - 1) / a.per + 1, shares = held < a.splits ? held : a.splits;
   float top = kMinusInf, sum = 0.0f;
-  for (int s = 0; s < shares; ++s) top = fmaxf(top, a.ml[2 * (s * rows + row)]);
+  for (int s = lane; s < shares; s += 64) top = fmaxf(top, a.ml[2 * (s * rows + row)]);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  const float shift = top == kMinusInf ? 0.0f : top;
   f32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
-  const bool in = 8 * lane < a.D;
-  for (int s = 0; s < shares; ++s) {
+  const int c = 8 * l16 < a.D ? 8 * l16 : 0;  // (lanes past D: sums that are not stored)
+#pragma unroll 4
+  for (int s = quarter; s < shares; s += 4) {
     const f32x2 ml = *reinterpret_cast<const f32x2*>(a.ml + 2 * (s * rows + row));
-    const float w = ml.x == kMinusInf && ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x == kMinusInf ? 0.0f : ml.x - top);
+    const float* const at = a.part + (s * rows + row) * a.D + c;
+    const f32x4 x0 = *reinterpret_cast<const f32x4*>(at), x1 = *reinterpret_cast<const f32x4*>(at + 4);
+    const float w = __builtin_amdgcn_exp2f(ml.x - shift);
     sum += ml.y * w;
-    if (in) {
-      const float* const at = a.part + (s * rows + row) * a.D + 8 * lane;
-      v0 += *reinterpret_cast<const f32x4*>(at) * w;
-      v1 += *reinterpret_cast<const f32x4*>(at + 4) * w;
+    v0 += x0 * w;
+    v1 += x1 * w;
+  }
+#pragma unroll
+  for (int o = 16; o <= 32; o <<= 1) {
+    sum += __shfl_xor(sum, o, 64);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v0[e] += __shfl_xor(v0[e], o, 64);
+      v1[e] += __shfl_xor(v1[e], o, 64);
     }
   }
-  if (!in) return;
+  if (quarter != 0 || 8 * l16 >= a.D) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  *reinterpret_cast<u32x4*>(a.o + row * a.D + 8 * lane) =
+  *reinterpret_cast<u32x4*>(a.o + row * a.D + c) =
       u32x4{pack_bf16x2(v0[0] * inv, v0[1] * inv), pack_bf16x2(v0[2] * inv, v0[3] * inv),
             pack_bf16x2(v1[0] * inv, v1[1] * inv), pack_bf16x2(v1[2] * inv, v1[3] * inv)};
 }
@@ -318,7 +342,7 @@ hipError_t launch_attn_few(const AttnArgs& a, hipStream_t stream) {
 
 hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.s.T) * a.Hq;
-  hipLaunchKernelGGL(k_attn_join, dim3(static_cast<uint32_t>((rows + 15) / 16)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(k_attn_join, dim3(static_cast<uint32_t>((rows + 3) / 4)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

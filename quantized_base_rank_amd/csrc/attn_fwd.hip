@@ -71,12 +71,19 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
 
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // the last tiles, which see the most keys, first
   const int kvh = static_cast<int>(blockIdx.x) % a.Hkv;
-  const int tiles = static_cast<int>(gridDim.x) / a.Hkv;
+  int rest = static_cast<int>(gridDim.x / a.Hkv) - 1 - static_cast<int>(blockIdx.x) / a.Hkv;
+  const int share = PAGED ? rest % a.splits : 0;
+  if constexpr (PAGED) rest /= a.splits;
   RowTile rt;
-  if (!find_rows(a.s.cu, a.s.B, a.s.T, a.g, kBM, tiles - 1 - static_cast<int>(blockIdx.x) / a.Hkv, &rt)) return;
+  if (!find_rows(a.s.cu, a.s.B, a.s.T, a.g, kBM, rest, &rt)) return;
   const int D = a.D, len = PAGED ? clamp_len(uniform_i32(a.s.lens, rt.b), a.max_len) : rt.n;
   const int first = len - rt.n;  // place of the first new token
+  // this share's keys: places base .. base + per - 1 (steps count from base)
+  const int base = PAGED ? share * a.per : 0, until = PAGED ? base + a.per : 0x7FFFFFFF;
+  if (base > 0 && base >= len) return;  // (k_attn_join counts a sequence's shares alike)
+  auto inside = [&](int v) { return v < until ? v : until; };
 
   // this lane's query row
   const int tok0 = rt.row0 / a.g, rem0 = rt.row0 - tok0 * a.g;
@@ -84,14 +91,14 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   const bool in = rt.row0 + in_tile < rt.rows;
   const int x = rem0 + in_tile, dt = small_div(x, a.g_inv);
   const int tok = in ? tok0 + dt : tok0, hq = kvh * a.g + (in ? x - dt * a.g : 0);
-  const int seen = in ? first + tok + 1 : 0;  // keys before this place count
+  const int seen = in ? inside(first + tok + 1) : 0;  // keys before this place count
   const int last_in = (rt.rows - rt.row0 < kBM ? rt.rows - rt.row0 : kBM) - 1;
-  const int end = first + tok0 + small_div(rem0 + last_in, a.g_inv) + 1;  // keys of the tile's last row
+  const int end = inside(first + tok0 + small_div(rem0 + last_in, a.g_inv) + 1);  // keys of the tile's last row
   const int w_last = wave * 32 + 31 < last_in ? wave * 32 + 31 : last_in;
   // keys of the wave's last row, and keys that all its rows see
-  const int w_end = wave * 32 > last_in ? 0 : first + tok0 + small_div(rem0 + w_last, a.g_inv) + 1;
-  const int w_all = wave * 32 + 31 > last_in ? 0 : first + tok0 + small_div(rem0 + wave * 32, a.g_inv) + 1;
-  const int steps = end > 0 ? (end + kBN - 1) / kBN : 0;
+  const int w_end = wave * 32 > last_in ? 0 : inside(first + tok0 + small_div(rem0 + w_last, a.g_inv) + 1);
+  const int w_all = wave * 32 + 31 > last_in ? 0 : inside(first + tok0 + small_div(rem0 + wave * 32, a.g_inv) + 1);
+  const int steps = end > base ? (end - base + kBN - 1) / kBN : 0;
 
   u32x4 qf[KS];
   const uint16_t* q = a.q + static_cast<int64_t>(rt.s0 + tok) * a.q_ld + hq * D;
@@ -129,8 +136,8 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   const bool holds = (kBN * kChunks >= 64 * W || tid < kBN * kChunks) && 16 * chunk < D;
   uint32_t queue = 0;  // blocks of 16 keys that are there, four bits a step
   auto page_at = [&](int j, int blk) {
-    const int at = j * kBN + 16 * blk;
-    return at < len ? uniform_page(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, at) : -1;
+    const int at = base + j * kBN + 16 * blk;
+    return at < end ? uniform_page(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, at) : -1;
   };
   auto blocks = [&](int j) {
     uint32_t b = 0;
@@ -147,7 +154,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
       const int pg = page_at(j, __builtin_amdgcn_readfirstlane(r >> 4));
       (values ? held_v : held_k)[i] = u32x4{0, 0, 0, 0};
       if (pg >= 0 && holds) {
-        const int64_t row = ((static_cast<int64_t>(pg) * a.c.H + kvh) << a.c.page_shift) + ((j * kBN + r) & page_mask);
+        const int64_t row = ((static_cast<int64_t>(pg) * a.c.H + kvh) << a.c.page_shift) + ((base + j * kBN + r) & page_mask);
         (values ? held_v : held_k)[i] = *reinterpret_cast<const u32x4*>((values ? a.c.v : a.c.k) + row * D + 16 * chunk);
         if (!values && chunk == 0) {
           held_ks[i] = a.c.ks[row];
@@ -196,7 +203,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   };
   auto values = [&](int j, int buf) {
     const uint8_t* const sv = lds + buf * (2 * kTile) + kTile;
-    const int j0 = j * kBN;
+    const int j0 = base + j * kBN;
     uint32_t odd = 0;  // non-finite values behind some row's mask
     const bool cut = !PAGED && j0 + kBN > w_all;
 #pragma unroll
@@ -226,7 +233,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
     }
   };
   auto softmax = [&](int j, int buf, uint32_t there) {
-    const int j0 = j * kBN;
+    const int j0 = base + j * kBN;
     const bool masked = j0 + kBN > w_all || there != 0xFu;
     const float* const sks = s_scale + (PAGED ? buf * 2 * kBN : 0);
     if constexpr (PAGED) {
@@ -308,7 +315,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
       load_packed(2, 2, false);
       barrier<0, 0>();
     }
-    if (0 < w_end) {
+    if (base < w_end) {
       scores(0);
       softmax(0, 0, PAGED ? blocks(0) : 0xFu);
     }
@@ -316,8 +323,8 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
     int b0 = 0, b1 = 1, b2 = 2;
     for (int j = 0; j < steps; ++j) {
       if constexpr (W == 8) __builtin_amdgcn_s_setprio(1);
-      if ((j + 1) * kBN < w_end) scores(b1);
-      if (j * kBN < w_end) values(j, b0);
+      if (base + (j + 1) * kBN < w_end) scores(b1);
+      if (base + j * kBN < w_end) values(j, b0);
       if constexpr (W == 8) __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
       barrier<PAGED ? -1 : 0, -1>();
@@ -331,7 +338,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
         load_packed(j + 3, b0, false);
         load_packed(j + 2, b2, true);
       }
-      if ((j + 1) * kBN < w_end) softmax(j + 1, b1, queue & 0xFu);
+      if (base + (j + 1) * kBN < w_end) softmax(j + 1, b1, queue & 0xFu);
       if constexpr (PAGED) queue = queue >> 4 | blocks(j + 5) << 12;
       __builtin_amdgcn_sched_barrier(0);
       barrier<-1, PAGED ? 0 : -1>();
@@ -348,6 +355,18 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   l += swap_halves(l);
   if (!in) return;
   const int64_t row = static_cast<int64_t>(rt.s0 + tok) * a.Hq + hq;
+  if (PAGED && a.splits > 1) {
+    const int64_t part = static_cast<int64_t>(share) * a.s.T * a.Hq + row;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int c = 32 * d + acc_row(i, h);
+        if (c < D) *reinterpret_cast<f32x4*>(a.part + part * D + c) = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+      }
+    if (h == 0) *reinterpret_cast<f32x2*>(a.ml + 2 * part) = f32x2{m, l};
+    return;
+  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (no key: 0; NaN stays)
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -364,7 +383,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
 template <int DP, bool PAGED, int W>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   const int64_t tiles = static_cast<int64_t>(a.s.T) * a.g / (32 * W) + a.s.B;
-  hipLaunchKernelGGL((k_attn<DP, PAGED, W>), dim3(static_cast<uint32_t>(tiles * a.Hkv)), dim3(64 * W), 0, stream, a);
+  hipLaunchKernelGGL((k_attn<DP, PAGED, W>), dim3(static_cast<uint32_t>(tiles * (PAGED ? a.splits : 1) * a.Hkv)), dim3(64 * W), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -3,8 +3,9 @@
 // [page][D] and scales [pages][heads][page].  Rounding and non-finite rows are
 // those of the 8-bit rows (q8_rows.hip).
 //
-// Sixteen lanes take a row of up to 128 elements, eight each, so a wave's
-// four rows are four heads of one token or of neighbouring tokens.  HBM-bound.
+// A wave takes sixteen rows of one token (its key heads, then its value heads),
+// sixteen lanes a row of up to 128 elements, so the token's sequence, place and
+// page are looked up once for all of them.  HBM-bound.
 #include "attn_common.hpp"
 #include "kernels.hpp"
 #include "q8_common.hpp"
@@ -13,79 +14,105 @@ namespace qlin {
 
 namespace {
 
-// Place of packed token t: the sequence's new tokens are the last of its
-// cached ones.  b = -1: a row behind the last sequence.
+constexpr int kRows = 16;  // rows of a wave, four at a time
+
+// Row of the cache's rows, before the head's is added, of packed token t: the
+// sequence's new tokens are the last of its cached ones.
 struct Place {
-  int b, j;
+  bool known;  // t belongs to a sequence
+  int page;    // -1: not there
+  int row;     // in the page
 };
-__device__ __forceinline__ Place place_of(const KvBatchArgs& s, int t) {
+__device__ __forceinline__ Place place_of(const KvBatchArgs& s, const KvCacheArgs& c, int t) {
   const int b = seq_of(s.cu, s.B, s.T, t);
-  if (b < 0) return Place{-1, 0};
-  const int s0 = seq_start(s.cu, b, s.T), s1 = seq_start(s.cu, b + 1, s.T);
-  const int64_t j = static_cast<int64_t>(s.lens[b]) - (s1 - s0) + (t - s0);
-  return Place{b, j < 0 || j > 0x7FFFFFFF ? -1 : static_cast<int>(j)};
+  if (b < 0) return Place{false, -1, 0};
+  const int s0 = uniform_start(s.cu, b, s.T), s1 = uniform_start(s.cu, b + 1, s.T);
+  const int64_t j = static_cast<int64_t>(uniform_i32(s.lens, b)) - (s1 - s0) + (t - s0);
+  if (j < 0 || j > 0x7FFFFFFF) return Place{true, -1, 0};
+  const int at = static_cast<int>(j);
+  return Place{true, uniform_page(s.table, s.table_len, c.pages, c.page_shift, b, at), at & ((1 << c.page_shift) - 1)};
+}
+
+// f(token, first row) for every sixteen rows; a longer queue is walked.
+template <typename F>
+__device__ __forceinline__ void each_part(int T, int H, F f) {
+  const int parts = (2 * H + kRows - 1) / kRows;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const int64_t n = static_cast<int64_t>(T) * parts;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + wave; i < n; i += static_cast<int64_t>(gridDim.x) * 4) {
+    const int64_t t = i / parts;
+    f(static_cast<int>(t), static_cast<int>(i - t * parts) * kRows);
+  }
 }
 
 __global__ __launch_bounds__(256) void k_kv_write(KvWriteArgs a) {
-  const int lane = threadIdx.x & 15;
-  const int64_t rows = static_cast<int64_t>(a.s.T) * a.c.H * 2;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4); i < rows;
-       i += static_cast<int64_t>(gridDim.x) * 16) {
-    const int64_t th = i >> 1;
-    const int t = static_cast<int>(th / a.c.H), h = static_cast<int>(th % a.c.H);
-    const bool is_v = (i & 1) != 0;
-    const Place p = place_of(a.s, t);
-    const int pg = p.b < 0 ? -1 : page_of(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, p.b, p.j);
-    if (pg < 0) continue;  // (sixteen lanes alike)
-    const uint16_t* x = (is_v ? a.v + t * a.v_ld : a.k + t * a.k_ld) + h * a.c.D;
-    const bool in = 8 * lane < a.c.D;
-    const u32x4 v = in ? *reinterpret_cast<const u32x4*>(x + 8 * lane) : u32x4{0, 0, 0, 0};
-    float mx = 0.0f;
+  const int lane = threadIdx.x & 15, sub = (threadIdx.x & 63) >> 4, H = a.c.H, D = a.c.D;
+  const bool in = 8 * lane < D;
+  each_part(a.s.T, H, [&](int t, int r0) {
+    u32x4 x[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mx = max_abs_nan(mx, elem8(v, e));
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 4 * i + sub;
+      const uint16_t* const src = r < H ? a.k + t * a.k_ld + r * D : a.v + t * a.v_ld + (r - H) * D;
+      x[i] = in && r < 2 * H ? *reinterpret_cast<const u32x4*>(src + 8 * lane) : u32x4{0, 0, 0, 0};
+    }
+    const Place p = place_of(a.s, a.c, t);
+    if (p.page < 0) return;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) mx = max_abs_nan(mx, __shfl_xor(mx, o, 16));
-    const RowScale s = row_scale(mx);
-    const int64_t row = ((static_cast<int64_t>(pg) * a.c.H + h) << a.c.page_shift) + (p.j & ((1 << a.c.page_shift) - 1));
-    if (in)
-      *reinterpret_cast<u32x2*>((is_v ? a.c.v : a.c.k) + row * a.c.D + 8 * lane) =
-          finite_f32(mx) ? codes8(v, s) : u32x2{0u, 0u};
-    if (lane == 0) (is_v ? a.c.vs : a.c.ks)[row] = s.scale;
-  }
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 4 * i + sub, head = r < H ? r : r - H;
+      float mx = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = max_abs_nan(mx, elem8(x[i], e));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mx = max_abs_nan(mx, __shfl_xor(mx, o, 16));
+      if (r >= 2 * H) continue;
+      const RowScale s = row_scale(mx);
+      const int64_t row = ((static_cast<int64_t>(p.page) * H + head) << a.c.page_shift) + p.row;
+      if (in)
+        *reinterpret_cast<u32x2*>((r < H ? a.c.k : a.c.v) + row * D + 8 * lane) =
+            finite_f32(mx) ? codes8(x[i], s) : u32x2{0u, 0u};
+      if (lane == 0) (r < H ? a.c.ks : a.c.vs)[row] = s.scale;
+    }
+  });
 }
 
 __global__ __launch_bounds__(256) void k_kv_read(KvReadArgs a) {
-  const int lane = threadIdx.x & 15;
-  const int64_t rows = static_cast<int64_t>(a.s.T) * a.c.H * 2;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4); i < rows;
-       i += static_cast<int64_t>(gridDim.x) * 16) {
-    const int64_t th = i >> 1;
-    const int t = static_cast<int>(th / a.c.H), h = static_cast<int>(th % a.c.H);
-    const bool is_v = (i & 1) != 0;
-    const Place p = place_of(a.s, t);
-    if (p.b < 0 || 8 * lane >= a.c.D) continue;
-    const int pg = page_of(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, p.b, p.j);
-    u32x4 out = {0, 0, 0, 0};
-    if (pg >= 0) {
-      const int64_t row = ((static_cast<int64_t>(pg) * a.c.H + h) << a.c.page_shift) + (p.j & ((1 << a.c.page_shift) - 1));
-      out = values8(*reinterpret_cast<const u32x2*>((is_v ? a.c.v : a.c.k) + row * a.c.D + 8 * lane),
-                    (is_v ? a.c.vs : a.c.ks)[row]);
+  const int lane = threadIdx.x & 15, sub = (threadIdx.x & 63) >> 4, H = a.c.H, D = a.c.D;
+  if (8 * lane >= D) return;
+  each_part(a.s.T, H, [&](int t, int r0) {
+    const Place p = place_of(a.s, a.c, t);
+    if (!p.known) return;
+    u32x2 c[4];
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 4 * i + sub, head = r < H ? r : r - H;
+      const int64_t row = ((static_cast<int64_t>(p.page) * H + head) << a.c.page_shift) + p.row;
+      const bool there = p.page >= 0 && r < 2 * H;
+      c[i] = there ? *reinterpret_cast<const u32x2*>((r < H ? a.c.k : a.c.v) + row * D + 8 * lane) : u32x2{0u, 0u};
+      s[i] = there ? (r < H ? a.c.ks : a.c.vs)[row] : 0.0f;
     }
-    *reinterpret_cast<u32x4*>((is_v ? a.v : a.k) + th * a.c.D + 8 * lane) = out;
-  }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 4 * i + sub, head = r < H ? r : r - H;
+      if (r < 2 * H)
+        *reinterpret_cast<u32x4*>((r < H ? a.k : a.v) + (static_cast<int64_t>(t) * H + head) * D + 8 * lane) = values8(c[i], s[i]);
+    }
+  });
 }
 
-// Workgroups for the rows of T tokens, sixteen rows each.
-uint32_t kv_grid(int64_t rows) { return row_grid(rows, 16); }
+// Workgroups for T tokens, four waves each.
+uint32_t kv_grid(int64_t T, int H) { return row_grid(T * ((2 * H + kRows - 1) / kRows), 4); }
 
 }  // namespace
 
 hipError_t launch_kv_write(const KvWriteArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(k_kv_write, dim3(kv_grid(2LL * a.s.T * a.c.H)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(k_kv_write, dim3(kv_grid(a.s.T, a.c.H)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(k_kv_read, dim3(kv_grid(2LL * a.s.T * a.c.H)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(k_kv_read, dim3(kv_grid(a.s.T, a.c.H)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
