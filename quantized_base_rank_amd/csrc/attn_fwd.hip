@@ -27,8 +27,8 @@
 //
 // What is masked does not count whatever it holds: scores behind the mask are
 // replaced, not multiplied, and in steps that the mask cuts, values that are
-// not finite are left out of the product (0 times them is not 0) and added to
-// the rows that see them.
+// not finite are set to zero for the product (0 times them is not 0) and added
+// to the rows that see them.
 #include "attn_common.hpp"
 #include "kernels.hpp"
 
@@ -65,9 +65,19 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   constexpr int kBM = 32 * W, kTile = kBN * DP * 2, kLoads = kTile / 1024 / W;
   static_assert(kLoads >= 1, "every wave loads a part of each tile");
   constexpr int kRowsPer = 64 / NP;  // rows of a load
-  // [buffer][keys, values]
-  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * 2 * kTile];
+  // three buffers of keys and of values (an array each: a read of one is not
+  // held for loads into another), and the scales of cached ones
+  __shared__ __attribute__((aligned(16))) uint8_t sk0[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sk1[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sk2[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sv0[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sv1[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sv2[kTile];
   __shared__ __attribute__((aligned(16))) float s_scale[PAGED ? 3 * 2 * kBN : 1];
+  __shared__ int s_odd[3];  // 1 + the step whose values in this buffer were not finite
+  if (threadIdx.x < 3) s_odd[threadIdx.x] = 0;
+  auto sk = [&](int buf) { return buf % 3 == 0 ? sk0 : buf % 3 == 1 ? sk1 : sk2; };
+  auto sv = [&](int buf) { return buf % 3 == 0 ? sv0 : buf % 3 == 1 ? sv1 : sv2; };
 
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -123,7 +133,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
     const int left = len - j * kBN;
     const uint32_t bytes = left > 0 ? static_cast<uint32_t>(((left < kBN ? left : kBN) - 1) * ld + D) * 2u : 0u;
     const uint16_t* const src = (values ? a.v : a.k) + (static_cast<int64_t>(rt.s0) + j * kBN) * ld + kvh * D;
-    uint8_t* const dst = lds + buf * (2 * kTile) + (values ? kTile : 0) + wave * kLoads * 1024;
+    uint8_t* const dst = (values ? sv(buf) : sk(buf)) + wave * kLoads * 1024;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) load_to_lds(src, bytes, dst + i * 1024, values ? vo_v[i] : vo_k[i]);
   };
@@ -134,7 +144,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   const int row_t = tid / kChunks, chunk = tid % kChunks;
   const int page_mask = (1 << a.c.page_shift) - 1;
   const bool holds = (kBN * kChunks >= 64 * W || tid < kBN * kChunks) && 16 * chunk < D;
-  uint32_t queue = 0;  // blocks of 16 keys that are there, four bits a step
+  uint32_t queue = 0xFFFF;  // blocks of 16 keys that are there, four bits a step
   auto page_at = [&](int j, int blk) {
     const int at = base + j * kBN + 16 * blk;
     return at < end ? uniform_page(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, at) : -1;
@@ -164,7 +174,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
     }
   };
   auto put = [&](int buf, bool values) {
-    uint8_t* const dst = lds + buf * (2 * kTile) + (values ? kTile : 0);
+    uint8_t* const dst = values ? sv(buf) : sk(buf);
 #pragma unroll
     for (int i = 0; i < kHold; ++i) {
       if (kBN * kChunks < 64 * W && tid >= kBN * kChunks) break;
@@ -174,8 +184,8 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
       *reinterpret_cast<u32x4*>(dst + piece_at<DP>(r, 2 * chunk)) = u32x4{w0.x, w0.y, w1.x, w1.y};
       *reinterpret_cast<u32x4*>(dst + piece_at<DP>(r, 2 * chunk + 1)) = u32x4{w2.x, w2.y, w3.x, w3.y};
       if (!values && chunk == 0) {
-        s_scale[buf * 2 * kBN + r] = held_ks[i];
-        s_scale[buf * 2 * kBN + kBN + r] = held_vs[i];
+        s_scale[buf % 3 * 2 * kBN + r] = held_ks[i];
+        s_scale[buf % 3 * 2 * kBN + kBN + r] = held_vs[i];
       }
     }
   };
@@ -191,51 +201,62 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
   float m = kMinusInf, l = 0.0f;
 
-  auto scores = [&](int buf) {
-    const uint8_t* const sk = lds + buf * (2 * kTile);
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      s[kb] = f32x16{};
-#pragma unroll
-      for (int t = 0; t < KS; ++t)
-        s[kb] = mfma32(*reinterpret_cast<const u32x4*>(sk + (k_at ^ (t << 5)) + kb * 32 * DP * 2), qf[t], s[kb]);
-    }
+  auto key = [&](int buf, int kb, int t) {
+    return *reinterpret_cast<const u32x4*>(sk(buf) + (k_at ^ (t << 5)) + kb * 32 * DP * 2);
   };
-  auto values = [&](int j, int buf) {
-    const uint8_t* const sv = lds + buf * (2 * kTile) + kTile;
-    const int j0 = base + j * kBN;
-    uint32_t odd = 0;  // non-finite values behind some row's mask
-    const bool cut = !PAGED && j0 + kBN > w_all;
+  auto value = [&](int buf, int kg, int d) {
+    const uint8_t* const at = sv(buf) + (v_at ^ (d << 6)) + kg * 16 * DP * 2;
+    const uint8_t* const at8 = sv(buf) + (v_at ^ (d << 6) ^ (DP == 128 ? 16 : 0)) + (kg * 16 + 8) * DP * 2;
+    const u32x2 lo = ds_read_tr16(at), hi = ds_read_tr16(at8);
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+  };
+  auto scores = [&](int buf) __attribute__((always_inline)) {
+    s[0] = s[1] = f32x16{};
+#pragma unroll
+    for (int t = 0; t < KS; ++t)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) s[kb] = mfma32(key(buf, kb, t), qf[t], s[kb]);
+  };
+  auto values = [&](int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int kg = 0; kg < 4; ++kg)
 #pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        const uint8_t* const at = sv + (v_at ^ (d << 6)) + kg * 16 * DP * 2;
-        const uint8_t* const at8 = sv + (v_at ^ (d << 6) ^ (DP == 128 ? 16 : 0)) + 8 * DP * 2 + kg * 16 * DP * 2;
-        const u32x2 lo = ds_read_tr16(at), hi = ds_read_tr16(at8);
-        u32x4 v = {lo.x, lo.y, hi.x, hi.y};
-        if (!PAGED && cut) odd |= clear_nonfinite(v);
-        o[d] = mfma32(v, pf[kg], o[d]);
-      }
-    if (!PAGED && cut && __ballot(odd != 0) != 0) {
-      // they reach, as they are, the rows that see them
-      for (int jj = 0; jj < kBN; ++jj) {
-        if (j0 + jj >= seen) break;
+      for (int d = 0; d < DB; ++d) o[d] = mfma32(value(buf, kg, d), pf[kg], o[d]);
+  };
+  // Values of step j that are not finite, where the mask cuts the step: set to
+  // zero in LDS, by each wave in the part that it loaded, and noted ..
+  auto clear_values = [&](int j, int buf) __attribute__((always_inline)) {
+    uint32_t odd = 0;
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+    for (int i = 0; i < kLoads; ++i) {
+      u32x4* const at = reinterpret_cast<u32x4*>(sv(buf) + (wave * kLoads + i) * 1024 + lane * 16);
+      u32x4 v = *at;
+      const uint32_t bad = clear_nonfinite(v);
+      if (bad != 0) *at = v;
+      odd |= bad;
+    }
+    if (odd != 0) s_odd[buf % 3] = j + 1;
+  };
+  // .. and, as they are, added to the rows that see them
+  auto add_nonfinite = [&](int j, int buf) {
+    if (PAGED || s_odd[buf % 3] != j + 1) return;
+    const int j0 = base + j * kBN;
+    for (int jj = 0; jj < kBN && j0 + jj < seen; ++jj) {
+      const uint16_t* const v = a.v + static_cast<int64_t>(rt.s0 + j0 + jj) * a.v_ld + kvh * D;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = 32 * d + acc_row(i, h);
-            const float y = bf16_to_f32(*reinterpret_cast<const uint16_t*>(sv + piece_at<DP>(jj, c >> 3) + (c & 7) * 2));
-            if ((__float_as_uint(y) & 0x7F800000u) == 0x7F800000u) o[d][i] += y;
-          }
-      }
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int c = 32 * d + acc_row(i, h);
+          const float y = c < D ? bf16_to_f32(v[c]) : 0.0f;
+          if ((__float_as_uint(y) & 0x7F800000u) == 0x7F800000u) o[d][i] += y;
+        }
     }
   };
-  auto softmax = [&](int j, int buf, uint32_t there) {
+  auto softmax = [&](int j, int buf, uint32_t there) __attribute__((always_inline)) {
     const int j0 = base + j * kBN;
     const bool masked = j0 + kBN > w_all || there != 0xFu;
-    const float* const sks = s_scale + (PAGED ? buf * 2 * kBN : 0);
+    const float* const sks = s_scale + (PAGED ? buf % 3 * 2 * kBN : 0);
     if constexpr (PAGED) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -315,38 +336,90 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
       load_packed(2, 2, false);
       barrier<0, 0>();
     }
+    // steps of which every row of the tile sees all keys, in whole turns of the
+    // buffers, and with the next step to come
+    const int sees_all = inside(first + tok0 + 1) - base;
+    const int whole = sees_all >= 2 * kBN ? (sees_all / kBN - 1) / 3 * 3 : 0;
+    if (!PAGED && whole == 0) {
+      clear_values(0, 0);
+      barrier<-1, 0>();
+    }
     if (base < w_end) {
       scores(0);
       softmax(0, 0, PAGED ? blocks(0) : 0xFu);
     }
     if (second) barrier<-1, -1>();
-    int b0 = 0, b1 = 1, b2 = 2;
-    for (int j = 0; j < steps; ++j) {
-      if constexpr (W == 8) __builtin_amdgcn_s_setprio(1);
-      if (base + (j + 1) * kBN < w_end) scores(b1);
-      if (base + j * kBN < w_end) values(j, b0);
+    // the end of step j's matrix phase, and the softmax phase
+    auto rest = [&](int j, int buf, bool cut) __attribute__((always_inline)) {
       if constexpr (W == 8) __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
-      barrier<PAGED ? -1 : 0, -1>();
+      if (!PAGED && cut) {
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        clear_values(j + 1, buf + 1);
+        barrier<-1, 0>();
+      } else {
+        barrier<PAGED ? -1 : 0, -1>();
+      }
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (PAGED) {
-        put(b0, false);
-        put(b2, true);
+        put(buf, false);
+        put(buf + 2, true);
         fetch(j + 4, false);
         fetch(j + 3, true);
       } else {
-        load_packed(j + 3, b0, false);
-        load_packed(j + 2, b2, true);
+        load_packed(j + 3, buf, false);
+        load_packed(j + 2, buf + 2, true);
       }
-      if (base + (j + 1) * kBN < w_end) softmax(j + 1, b1, queue & 0xFu);
+      if (base + (j + 1) * kBN < w_end) softmax(j + 1, buf + 1, queue & 0xFu);
       if constexpr (PAGED) queue = queue >> 4 | blocks(j + 5) << 12;
       __builtin_amdgcn_sched_barrier(0);
       barrier<-1, PAGED ? 0 : -1>();
       __builtin_amdgcn_sched_barrier(0);
-      const int b = b0;
-      b0 = b1;
-      b1 = b2;
-      b2 = b;
+    };
+    auto whole_step = [&](int j, int buf, bool last) __attribute__((always_inline)) {
+      if constexpr (W == 8) __builtin_amdgcn_s_setprio(1);
+      if (w_end > base) {
+        scores(buf + 1);
+        values(buf);
+        // reads some instructions ahead of their use
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * KS - 6; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * DB; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+      }
+      rest(j, buf, last);
+    };
+    auto cut_step = [&](int j, int buf) __attribute__((always_inline)) {
+      if constexpr (W == 8) __builtin_amdgcn_s_setprio(1);
+      if (base + (j + 1) * kBN < w_end) scores(buf + 1);
+      if (base + j * kBN < w_end) {
+        values(buf);
+        add_nonfinite(j, buf);
+      }
+      rest(j, buf, true);
+    };
+    int j = 0;
+    for (; j < whole; j += 3) {
+      whole_step(j, 0, false);
+      whole_step(j + 1, 1, false);
+      whole_step(j + 2, 2, j + 3 == whole);
+    }
+    for (; j < steps; j += 3) {  // (steps past the last compute nothing)
+      cut_step(j, 0);
+      cut_step(j + 1, 1);
+      cut_step(j + 2, 2);
     }
     if (!second && W == 8) barrier<-1, -1>();
     // (loads on their way into LDS end before the workgroup does)
