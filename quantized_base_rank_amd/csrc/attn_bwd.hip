@@ -3,11 +3,22 @@
 //     p_ij = exp(c q_i . k_j - lse_i),      delta_i = do_i . o_i,
 //     ds_ij = p_ij (do_i . v_j - delta_i),  dv_j = sum_i p_ij do_i,
 //     dk_j = c sum_i ds_ij q_i,             dq_i = c sum_j ds_ij k_j.
-// Three launches: delta (and lse in powers of two), rows of one key head one
-// behind the other; dk and dv, a workgroup for 128 keys, which walks the query
-// rows of all heads that share them; dq, a workgroup for 128 query rows, which
-// walks the keys.  Scores are formed twice; in return no sum needs atomics, so
-// the results are the same from run to run.
+// Two launches: dq, a workgroup for 128 query rows, which forms their delta and
+// walks the keys; then dk and dv, a workgroup for 128 keys, which walks the
+// query rows of all heads that share them.  Scores are formed twice; in return
+// no sum needs atomics, so the results are the same from run to run.
+//
+// Each wave holds 32 rows (or keys) as operands and their sums in registers, one
+// wave on a SIMD; the other side streams through LDS in tiles of 64, three
+// buffers deep, loaded directly.  As in the forward, a product's sums are the
+// next one's operand as they stand, and the tile is read by rows for one and by
+// columns for the other.
+//
+// A tile's two halves are worked off in turns that keep the matrix cores busy
+// while p and ds are formed: with X the products s and do . v, Y the step to p
+// and ds, Z the products that sum,
+//     X(second) beside Y(first);  Z(first) beside Y(second);
+//     barrier;  Z(second) and X(the next tile's first).
 //
 // Roundings: p and ds to bf16 as operands of the products that sum over
 // queries and keys; all sums fp32.
@@ -19,46 +30,252 @@ namespace qlin {
 
 namespace {
 
-constexpr int kBK = 128;  // keys, or query rows, of a workgroup
-constexpr int kBQ = 64;   // query rows, or keys, of a step
+constexpr int kBK = 128;  // rows, or keys, of a workgroup
+constexpr int kBT = 64;   // keys, or rows, of a step
 
-// Sixteen lanes take a row.
-__global__ __launch_bounds__(256) void k_attn_delta(AttnBwdArgs a) {
-  const int lane = threadIdx.x & 15;
-  const int64_t rows = static_cast<int64_t>(a.T) * a.Hq;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4); i < rows;
-       i += static_cast<int64_t>(gridDim.x) * 16) {
-    float sum = 0.0f;
-    if (8 * lane < a.D) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(a.o + i * a.D + 8 * lane);
-      const u32x4 y = *reinterpret_cast<const u32x4*>(a.dout + i * a.D + 8 * lane);
+// Waits for this wave's loads, then meets the other waves.
+__device__ __forceinline__ void tile_barrier() { __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Lane's offset within the tiles for its row and column operands.
+template <int DP>
+struct TileAt {
+  uint32_t row, col;
+};
+template <int DP>
+__device__ __forceinline__ TileAt<DP> tile_at(int lane) {
+  const int l32 = lane & 31, h = lane >> 5, p = lane & 15;
+  const int r = 4 * h + (p >> 2), c = 16 * ((lane >> 4) & 1) + 4 * (p & 3);
+  return TileAt<DP>{static_cast<uint32_t>(piece_at<DP>(l32, h)),
+                    static_cast<uint32_t>(piece_at<DP>(r, c >> 3) + (c & 7) * 2)};
+}
+// Row operand t (elements 16 t ..) of rows 32 b ..
+template <int DP>
+__device__ __forceinline__ u32x4 row_operand(const uint8_t* tile, TileAt<DP> at, int b, int t) {
+  return *reinterpret_cast<const u32x4*>(tile + (at.row ^ (t << 5)) + b * 32 * DP * 2);
+}
+// Column operand of elements 32 d .., rows 16 kg .. (column_operand's order)
+template <int DP>
+__device__ __forceinline__ u32x4 col_operand(const uint8_t* tile, TileAt<DP> at, int kg, int d) {
+  const u32x2 lo = ds_read_tr16(tile + (at.col ^ (d << 6)) + kg * 16 * DP * 2);
+  const u32x2 hi = ds_read_tr16(tile + (at.col ^ (d << 6) ^ (DP == 128 ? 16 : 0)) + (kg * 16 + 8) * DP * 2);
+  return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
+
+// Order of a turn's instructions: N matrix instructions, behind each of them V
+// others, T transcendental ones and R LDS reads.
+template <int N, int V, int T, int R>
+__device__ __forceinline__ void turn_order() {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += elem8(x, e) * elem8(y, e);
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 16);
-    if (lane == 0) {
-      const int t = static_cast<int>(i / a.Hq), hq = static_cast<int>(i % a.Hq);
-      const int64_t at = (static_cast<int64_t>(hq / a.g) * a.T + t) * a.g + hq % a.g;
-      a.lse2[at] = a.lse[i] * kLog2e;
-      a.delta[at] = sum;
-    }
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (R > 0) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    if constexpr (V > 0) __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+    if constexpr (T > 0) __builtin_amdgcn_sched_group_barrier(0x400, T, 0);
   }
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int DP>
-__global__ __launch_bounds__(256, 1) void k_attn_dkdv(AttnBwdArgs a) {
-  constexpr int NP = DP / 8, KS = DP / 16, DB = DP / 32;
-  __shared__ __attribute__((aligned(16))) uint8_t sq[kBQ * DP * 2];
-  __shared__ __attribute__((aligned(16))) uint8_t sdo[kBQ * DP * 2];
-  __shared__ __attribute__((aligned(16))) float s_lse[kBQ], s_delta[kBQ];
+__global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
+  constexpr int NP = DP / 8, KS = DP / 16, DB = DP / 32, kTile = kBT * DP * 2, kLoads = kTile / 4096, kRowsPer = 64 / NP;
+  // (an array per buffer: a read of one is not held for loads into another)
+  __shared__ __attribute__((aligned(16))) uint8_t sk0[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sk1[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sk2[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sv0[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sv1[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sv2[kTile];
+  auto sk = [&](int b) { return b % 3 == 0 ? sk0 : b % 3 == 1 ? sk1 : sk2; };
+  auto sv = [&](int b) { return b % 3 == 0 ? sv0 : b % 3 == 1 ? sv1 : sv2; };
 
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kvh = static_cast<int>(blockIdx.x) % a.Hkv, D = a.D, g = a.g;
-  RowTile rt;  // rows are keys here
+  const int tiles = static_cast<int>(gridDim.x) / a.Hkv;
+  RowTile rt;  // the last tiles, which see the most keys, first
+  if (!find_rows(a.cu, a.B, a.T, g, kBK, tiles - 1 - static_cast<int>(blockIdx.x) / a.Hkv, &rt)) return;
+
+  const int tok0 = rt.row0 / g, rem0 = rt.row0 - tok0 * g;
+  const int ahead = rem0 + wave * 32 + l32, dt = small_div(ahead, a.g_inv);
+  const bool in = rt.row0 + wave * 32 + l32 < rt.rows;
+  const int tok = in ? tok0 + dt : tok0, hg = in ? ahead - dt * g : 0, hq = kvh * g + hg;
+  const int seen = in ? tok + 1 : 0;
+  const int last_in = (rt.rows - rt.row0 < kBK ? rt.rows - rt.row0 : kBK) - 1;
+  const int end = tok0 + small_div(rem0 + last_in, a.g_inv) + 1;
+  uint32_t vo_k[kLoads], vo_v[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = (wave * kLoads + i) * kRowsPer + lane / NP;
+    const int c = (lane % NP) ^ piece_swizzle<DP>(r);
+    const uint32_t out = 8 * c < D ? 0u : 0x80000000u;
+    vo_k[i] = (static_cast<uint32_t>(r) * static_cast<uint32_t>(a.k_ld * 2) + c * 16) | out;
+    vo_v[i] = (static_cast<uint32_t>(r) * static_cast<uint32_t>(a.v_ld * 2) + c * 16) | out;
+  }
+  // rows past the sequence and elements past D lie outside the resource: zeros
+  auto load = [&](int tile, int buf) __attribute__((always_inline)) {
+    const int j0 = tile * kBT;
+    const int left = rt.n - j0, n = left < kBT ? left : kBT;
+    const uint32_t bk = left > 0 ? static_cast<uint32_t>((n - 1) * a.k_ld + D) * 2u : 0u;
+    const uint32_t bv = left > 0 ? static_cast<uint32_t>((n - 1) * a.v_ld + D) * 2u : 0u;
+    const uint16_t* const k = a.k + (static_cast<int64_t>(rt.s0) + j0) * a.k_ld + kvh * D;
+    const uint16_t* const v = a.v + (static_cast<int64_t>(rt.s0) + j0) * a.v_ld + kvh * D;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      load_to_lds(k, bk, sk(buf) + (wave * kLoads + i) * 1024, vo_k[i]);
+      load_to_lds(v, bv, sv(buf) + (wave * kLoads + i) * 1024, vo_v[i]);
+    }
+  };
+  load(0, 0);
+  load(1, 1);
+
+  u32x4 qf[KS], yf[KS];
+  const int64_t t_row = rt.s0 + tok, o_row = t_row * a.Hq + hq;
+  float delta = 0.0f;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const int c = 16 * s + 8 * h;
+    const bool ok = c < D;
+    qf[s] = ok ? *reinterpret_cast<const u32x4*>(a.q + t_row * a.q_ld + hq * D + c) : u32x4{0, 0, 0, 0};
+    yf[s] = ok ? *reinterpret_cast<const u32x4*>(a.dout + o_row * D + c) : u32x4{0, 0, 0, 0};
+    const u32x4 o = ok ? *reinterpret_cast<const u32x4*>(a.o + o_row * D + c) : u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) delta += elem8(o, e) * elem8(yf[s], e);
+  }
+  delta += swap_halves(delta);
+  const float lse2 = a.lse[o_row] * kLog2e;
+  if (in && h == 0) {  // for dk and dv, with their signs
+    const int64_t at = (static_cast<int64_t>(kvh) * a.T + t_row) * g + hg;
+    a.lse2[at] = -lse2;
+    a.delta[at] = -delta;
+  }
+
+  const TileAt<DP> at = tile_at<DP>(lane);
+  f32x16 dq[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) dq[d] = f32x16{};
+  f32x16 s0, p0, s1, p1;  // scores and do . v - delta of a tile's first and second 32 keys
+  u32x4 d0[2], d1[2];     // their ds
+  auto x = [&](int buf, int kb, f32x16& s, f32x16& dp) __attribute__((always_inline)) {
+    s = f32x16{};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dp[i] = -delta;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      s = mfma32(row_operand<DP>(sk(buf), at, kb, t), qf[t], s);
+      dp = mfma32(row_operand<DP>(sv(buf), at, kb, t), yf[t], dp);
+    }
+  };
+  auto y = [&](auto cut, int j0, f32x16& s, const f32x16& dp, u32x4 (&ds)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.c2, -lse2));
+      s[i] = decltype(cut)::value && j0 + acc_row(i, h) >= seen ? 0.0f : p * dp[i];
+    }
+    ds[0] = pack_operand(s, 0);
+    ds[1] = pack_operand(s, 1);
+  };
+  auto z = [&](int buf, int kb, const u32x4 (&ds)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kg = 0; kg < 2; ++kg)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) dq[d] = mfma32(col_operand<DP>(sk(buf), at, 2 * kb + kg, d), ds[kg], dq[d]);
+  };
+  auto step = [&](auto cut, int tile, int buf) __attribute__((always_inline)) {
+    const int j0 = tile * kBT;
+    constexpr int kMore = decltype(cut)::value ? 4 : 2;
+    x(buf, 1, s1, p1);
+    y(cut, j0, s0, p0, d0);
+    turn_order<2 * KS, kMore * 16 / KS, 16 / KS, 1>();
+    z(buf, 0, d0);
+    y(cut, j0 + 32, s1, p1, d1);
+    turn_order<2 * DB, kMore * 32 / DB, 32 / DB / 2, 2>();
+    tile_barrier();
+    load(tile + 2, buf + 2);
+    z(buf, 1, d1);
+    x(buf + 1, 0, s0, p0);
+    turn_order<2 * DB, 0, 0, 2>();
+  };
+  tile_barrier();
+  x(0, 0, s0, p0);
+  constexpr std::integral_constant<bool, true> cut{};
+  constexpr std::integral_constant<bool, false> whole{};
+  const int tiles_all = (tok0 + 1) / kBT, tiles_end = (end + kBT - 1) / kBT;
+  int t = 0;
+  for (; t + 3 <= tiles_all; t += 3) {
+    step(whole, t, 0);
+    step(whole, t + 1, 1);
+    step(whole, t + 2, 2);
+  }
+  for (; t + 3 <= tiles_end; t += 3) {
+    step(cut, t, 0);
+    step(cut, t + 1, 1);
+    step(cut, t + 2, 2);
+  }
+  if (t < tiles_end) step(cut, t, 0);
+  if (t + 1 < tiles_end) step(cut, t + 1, 1);
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (loads into LDS end before the workgroup does)
+  if (!in) return;
+  uint16_t* const out = a.dq + t_row * a.dq_ld + hq * D;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int c = 32 * d + acc_row(i, h);
+      if (c < D)
+        *reinterpret_cast<u32x2*>(out + c) = u32x2{pack_bf16x2(dq[d][i] * a.scale, dq[d][i + 1] * a.scale),
+                                                   pack_bf16x2(dq[d][i + 2] * a.scale, dq[d][i + 3] * a.scale)};
+    }
+}
+
+template <int DP>
+__global__ __launch_bounds__(256, 1) void k_attn_dkdv(AttnBwdArgs a) {
+  constexpr int NP = DP / 8, KS = DP / 16, DB = DP / 32, kTile = kBT * DP * 2, kLoads = kTile / 4096, kRowsPer = 64 / NP;
+  __shared__ __attribute__((aligned(16))) uint8_t sq0[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sq1[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sq2[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sy0[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sy1[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sy2[kTile];
+  __shared__ __attribute__((aligned(16))) float sl0[2 * kBT];  // -lse, -delta
+  __shared__ __attribute__((aligned(16))) float sl1[2 * kBT];
+  __shared__ __attribute__((aligned(16))) float sl2[2 * kBT];
+  auto sq = [&](int b) { return b % 3 == 0 ? sq0 : b % 3 == 1 ? sq1 : sq2; };
+  auto sy = [&](int b) { return b % 3 == 0 ? sy0 : b % 3 == 1 ? sy1 : sy2; };
+  auto sl = [&](int b) { return b % 3 == 0 ? sl0 : b % 3 == 1 ? sl1 : sl2; };
+
+  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kvh = static_cast<int>(blockIdx.x) % a.Hkv, D = a.D, g = a.g;
+  RowTile rt;  // rows are keys here; the first tiles, which most rows see, first
   if (!find_rows(a.cu, a.B, a.T, 1, kBK, static_cast<int>(blockIdx.x) / a.Hkv, &rt)) return;
   const int rows = rt.n * g;  // query rows of the sequence
+
+  // loads of 64 query rows (any heads): row r is token t0 + (rem + r) / g; rows
+  // past the sequence and elements past D get an offset outside the resource
+  const int begin = rt.row0 * g;
+  auto load = [&](int tile, int buf) __attribute__((always_inline)) {
+    const int r0 = begin + tile * kBT;
+    const int t0 = r0 / g, rem = r0 - t0 * g;
+    const uint16_t* const q = a.q + (static_cast<int64_t>(rt.s0) + t0) * a.q_ld + kvh * g * D;
+    const uint16_t* const y = a.dout + ((static_cast<int64_t>(rt.s0) + t0) * a.Hq + kvh * g) * D;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = (wave * kLoads + i) * kRowsPer + lane / NP;
+      const int c = (lane % NP) ^ piece_swizzle<DP>(r);
+      const int x = rem + r, dt = small_div(x, a.g_inv), hg = x - dt * g;
+      const uint32_t out = 8 * c < D && r0 + r < rows ? 0u : 0x80000000u;
+      const uint32_t in_row = static_cast<uint32_t>(hg * D * 2 + c * 16);
+      load_to_lds(q, 0x7FFFFFFF, sq(buf) + (wave * kLoads + i) * 1024, (static_cast<uint32_t>(dt) * static_cast<uint32_t>(a.q_ld * 2) + in_row) | out);
+      load_to_lds(y, 0x7FFFFFFF, sy(buf) + (wave * kLoads + i) * 1024, (static_cast<uint32_t>(dt) * static_cast<uint32_t>(a.Hq * D * 2) + in_row) | out);
+    }
+    const int left = rows - r0;
+    const uint32_t bytes = left > 0 ? static_cast<uint32_t>(left < kBT ? left : kBT) * 4u : 0u;
+    if (wave < 2)
+      load_word_to_lds((wave == 0 ? a.lse2 : a.delta) + (static_cast<int64_t>(kvh) * a.T + rt.s0) * g + r0, bytes,
+                       reinterpret_cast<uint8_t*>(sl(buf) + wave * kBT), static_cast<uint32_t>(lane * 4));
+  };
+  load(0, 0);
+  load(1, 1);
 
   const int key = rt.row0 + wave * 32 + l32;
   const bool in = key < rt.n;
@@ -70,63 +287,93 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkdv(AttnBwdArgs a) {
     kf[s] = in && c < D ? *reinterpret_cast<const u32x4*>(a.k + krow * a.k_ld + kvh * D + c) : u32x4{0, 0, 0, 0};
     vf[s] = in && c < D ? *reinterpret_cast<const u32x4*>(a.v + krow * a.v_ld + kvh * D + c) : u32x4{0, 0, 0, 0};
   }
+  const TileAt<DP> at = tile_at<DP>(lane);
   f32x16 dk[DB], dv[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) dk[d] = dv[d] = f32x16{};
 
-  const float* lse2 = a.lse2 + (static_cast<int64_t>(kvh) * a.T + rt.s0) * g;
-  const float* delta = a.delta + (static_cast<int64_t>(kvh) * a.T + rt.s0) * g;
-  for (int r0 = rt.row0 * g; r0 < rows; r0 += kBQ) {
-    const int t0 = r0 / g, rem = r0 - t0 * g;
+  f32x16 s0, p0, s1, p1;            // scores and do . v - delta of a tile's first and second 32 rows
+  u32x4 e0[2], d0[2], e1[2], d1[2];  // their p and ds
+  auto x = [&](int buf, int qb, f32x16& s, f32x16& dp) __attribute__((always_inline)) {
+    s = f32x16{};
 #pragma unroll
-    for (int i = 0; i < kBQ * NP / 256; ++i) {
-      const int idx = tid + 256 * i, r = idx / NP, c = idx % NP;
-      u32x4 q = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-      if (r0 + r < rows && 8 * c < D) {
-        const int dt = small_div(rem + r, a.g_inv), hq = kvh * g + rem + r - dt * g;
-        const int64_t row = rt.s0 + t0 + dt;
-        q = *reinterpret_cast<const u32x4*>(a.q + row * a.q_ld + hq * D + 8 * c);
-        y = *reinterpret_cast<const u32x4*>(a.dout + (row * a.Hq + hq) * D + 8 * c);
-      }
-      *reinterpret_cast<u32x4*>(sq + piece_at<DP>(r, c)) = q;
-      *reinterpret_cast<u32x4*>(sdo + piece_at<DP>(r, c)) = y;
+    for (int i = 0; i < 16; i += 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(sl(buf) + kBT + qb * 32 + acc_row(i, h));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dp[i + e] = v[e];
     }
-    if (tid < kBQ) {
-      const bool ok = r0 + tid < rows;
-      s_lse[tid] = ok ? lse2[r0 + tid] : 0.0f;
-      s_delta[tid] = ok ? delta[r0 + tid] : 0.0f;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      s = mfma32(row_operand<DP>(sq(buf), at, qb, t), kf[t], s);
+      dp = mfma32(row_operand<DP>(sy(buf), at, qb, t), vf[t], dp);
     }
-    __syncthreads();
-    // rows from key's own token on count: row (key g) is the first
-    const int64_t from = static_cast<int64_t>(key) * g - r0;
+  };
+  // rows key g on see the key; of those past the sequence do and delta are zero,
+  // and so is what they add
+  auto y = [&](auto cut, int r0, int buf, int qb, f32x16& s, f32x16& dp, u32x4 (&p)[2], u32x4 (&ds)[2])
+      __attribute__((always_inline)) {
+    const int64_t ahead = static_cast<int64_t>(key) * g - r0;
+    const int from = ahead > kBT ? kBT : static_cast<int>(ahead);
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
-      f32x16 s = {}, dp = {};
+    for (int i = 0; i < 16; i += 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(sl(buf) + qb * 32 + acc_row(i, h));
 #pragma unroll
-      for (int t = 0; t < KS; ++t) {
-        s = mfma32(*reinterpret_cast<const u32x4*>(sq + piece_at<DP>(qb * 32 + l32, 2 * t + h)), kf[t], s);
-        dp = mfma32(*reinterpret_cast<const u32x4*>(sdo + piece_at<DP>(qb * 32 + l32, 2 * t + h)), vf[t], dp);
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = qb * 32 + acc_row(i, h);
-        const bool on = in && r >= from && r0 + r < rows;
-        const float p = on ? __builtin_amdgcn_exp2f(s[i] * a.c2 - s_lse[r]) : 0.0f;
-        s[i] = p;
-        dp[i] = on ? p * (dp[i] - s_delta[r]) : 0.0f;
-      }
-#pragma unroll
-      for (int kg = 0; kg < 2; ++kg) {
-        const u32x4 p = pack_operand(s, kg), ds = pack_operand(dp, kg);
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          dv[d] = mfma32(column_operand<DP>(sdo, qb * 32 + 16 * kg, 32 * d, lane), p, dv[d]);
-          dk[d] = mfma32(column_operand<DP>(sq, qb * 32 + 16 * kg, 32 * d, lane), ds, dk[d]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], a.c2, v[e]));
+        s[i + e] = decltype(cut)::value && qb * 32 + acc_row(i + e, h) < from ? 0.0f : w;
+        dp[i + e] *= s[i + e];
       }
     }
-    __syncthreads();
+#pragma unroll
+    for (int kg = 0; kg < 2; ++kg) {
+      p[kg] = pack_operand(s, kg);
+      ds[kg] = pack_operand(dp, kg);
+    }
+  };
+  auto z = [&](int buf, int qb, const u32x4 (&p)[2], const u32x4 (&ds)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kg = 0; kg < 2; ++kg)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        dv[d] = mfma32(col_operand<DP>(sy(buf), at, 2 * qb + kg, d), p[kg], dv[d]);
+        dk[d] = mfma32(col_operand<DP>(sq(buf), at, 2 * qb + kg, d), ds[kg], dk[d]);
+      }
+  };
+  auto step = [&](auto cut, int tile, int buf) __attribute__((always_inline)) {
+    const int r0 = begin + tile * kBT;
+    constexpr int kMore = decltype(cut)::value ? 4 : 3;
+    x(buf, 1, s1, p1);
+    y(cut, r0, buf, 0, s0, p0, e0, d0);
+    turn_order<2 * KS, kMore * 16 / KS, 16 / KS, 1>();
+    z(buf, 0, e0, d0);
+    y(cut, r0, buf, 1, s1, p1, e1, d1);
+    turn_order<4 * DB, kMore * 8 / DB, 8 / DB / 2, 2>();
+    tile_barrier();
+    load(tile + 2, buf + 2);
+    z(buf, 1, e1, d1);
+    x(buf + 1, 0, s0, p0);
+    turn_order<4 * DB, 0, 0, 2>();
+  };
+  tile_barrier();
+  x(0, 0, s0, p0);
+  constexpr std::integral_constant<bool, true> cut{};
+  constexpr std::integral_constant<bool, false> whole{};
+  const int tiles = (rows - begin + kBT - 1) / kBT;
+  const int tiles_cut = (kBK * g + kBT - 1) / kBT;  // from there on every row sees every key
+  int t = 0;
+  for (; t + 3 <= tiles && t < tiles_cut; t += 3) {
+    step(cut, t, 0);
+    step(cut, t + 1, 1);
+    step(cut, t + 2, 2);
   }
+  for (; t + 3 <= tiles; t += 3) {
+    step(whole, t, 0);
+    step(whole, t + 1, 1);
+    step(whole, t + 2, 2);
+  }
+  if (t < tiles) step(cut, t, 0);
+  if (t + 1 < tiles) step(cut, t + 1, 1);
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   if (!in) return;
   uint16_t* const odk = a.dk + krow * a.dk_ld + kvh * D;
   uint16_t* const odv = a.dv + krow * a.dv_ld + kvh * D;
@@ -143,106 +390,18 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkdv(AttnBwdArgs a) {
 }
 
 template <int DP>
-__global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
-  constexpr int NP = DP / 8, KS = DP / 16, DB = DP / 32;
-  __shared__ __attribute__((aligned(16))) uint8_t sk[kBQ * DP * 2];
-  __shared__ __attribute__((aligned(16))) uint8_t sv[kBQ * DP * 2];
-
-  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kvh = static_cast<int>(blockIdx.x) % a.Hkv, D = a.D, g = a.g;
-  const int tiles = static_cast<int>(gridDim.x) / a.Hkv;
-  RowTile rt;
-  if (!find_rows(a.cu, a.B, a.T, g, kBK, tiles - 1 - static_cast<int>(blockIdx.x) / a.Hkv, &rt)) return;
-
-  const int tok0 = rt.row0 / g, rem0 = rt.row0 - tok0 * g;
-  const int x = rem0 + wave * 32 + l32, dt = small_div(x, a.g_inv);
-  const bool in = rt.row0 + wave * 32 + l32 < rt.rows;
-  const int tok = in ? tok0 + dt : tok0, hq = kvh * g + (in ? x - dt * g : 0);
-  const int seen = in ? tok + 1 : 0;
-  const int last = (rt.rows - rt.row0 < kBK ? rt.rows : rt.row0 + kBK) - 1;
-  const int end = last / g + 1;
-
-  u32x4 qf[KS], yf[KS];
-  const int64_t t_row = rt.s0 + tok, o_row = t_row * a.Hq + hq;
-#pragma unroll
-  for (int s = 0; s < KS; ++s) {
-    const int c = 16 * s + 8 * h;
-    qf[s] = c < D ? *reinterpret_cast<const u32x4*>(a.q + t_row * a.q_ld + hq * D + c) : u32x4{0, 0, 0, 0};
-    yf[s] = c < D ? *reinterpret_cast<const u32x4*>(a.dout + o_row * D + c) : u32x4{0, 0, 0, 0};
-  }
-  const int64_t at = (static_cast<int64_t>(kvh) * a.T + rt.s0 + tok) * g + (in ? x - dt * g : 0);
-  const float lse2 = a.lse2[at], delta = a.delta[at];
-  f32x16 dq[DB];
-#pragma unroll
-  for (int d = 0; d < DB; ++d) dq[d] = f32x16{};
-
-  for (int j0 = 0; j0 < end; j0 += kBQ) {
-#pragma unroll
-    for (int i = 0; i < kBQ * NP / 256; ++i) {
-      const int idx = tid + 256 * i, r = idx / NP, c = idx % NP;
-      u32x4 k = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-      if (j0 + r < rt.n && 8 * c < D) {
-        const int64_t row = rt.s0 + j0 + r;
-        k = *reinterpret_cast<const u32x4*>(a.k + row * a.k_ld + kvh * D + 8 * c);
-        v = *reinterpret_cast<const u32x4*>(a.v + row * a.v_ld + kvh * D + 8 * c);
-      }
-      *reinterpret_cast<u32x4*>(sk + piece_at<DP>(r, c)) = k;
-      *reinterpret_cast<u32x4*>(sv + piece_at<DP>(r, c)) = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      f32x16 s = {}, dp = {};
-#pragma unroll
-      for (int t = 0; t < KS; ++t) {
-        s = mfma32(*reinterpret_cast<const u32x4*>(sk + piece_at<DP>(kb * 32 + l32, 2 * t + h)), qf[t], s);
-        dp = mfma32(*reinterpret_cast<const u32x4*>(sv + piece_at<DP>(kb * 32 + l32, 2 * t + h)), yf[t], dp);
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const bool on = j0 + kb * 32 + acc_row(i, h) < seen;
-        const float p = __builtin_amdgcn_exp2f(s[i] * a.c2 - lse2);
-        s[i] = on ? p * (dp[i] - delta) : 0.0f;
-      }
-#pragma unroll
-      for (int kg = 0; kg < 2; ++kg) {
-        const u32x4 ds = pack_operand(s, kg);
-#pragma unroll
-        for (int d = 0; d < DB; ++d) dq[d] = mfma32(column_operand<DP>(sk, kb * 32 + 16 * kg, 32 * d, lane), ds, dq[d]);
-      }
-    }
-    __syncthreads();
-  }
-  if (!in) return;
-  uint16_t* const out = a.dq + t_row * a.dq_ld + hq * D;
-#pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int c = 32 * d + acc_row(i, h);
-      if (c < D)
-        *reinterpret_cast<u32x2*>(out + c) = u32x2{pack_bf16x2(dq[d][i] * a.scale, dq[d][i + 1] * a.scale),
-                                                   pack_bf16x2(dq[d][i + 2] * a.scale, dq[d][i + 3] * a.scale)};
-    }
-}
-
-template <int DP>
 hipError_t launch_bwd(const AttnBwdArgs& a, hipStream_t stream) {
   const int64_t key_tiles = static_cast<int64_t>(a.T) / kBK + a.B, row_tiles = static_cast<int64_t>(a.T) * a.g / kBK + a.B;
-  hipLaunchKernelGGL((k_attn_dkdv<DP>), dim3(static_cast<uint32_t>(key_tiles * a.Hkv)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((k_attn_dq<DP>), dim3(static_cast<uint32_t>(row_tiles * a.Hkv)), dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_attn_dq<DP>), dim3(static_cast<uint32_t>(row_tiles * a.Hkv)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((k_attn_dkdv<DP>), dim3(static_cast<uint32_t>(key_tiles * a.Hkv)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(k_attn_delta, dim3(row_grid(static_cast<int64_t>(a.T) * a.Hq, 16)), dim3(256), 0, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   return a.D <= 64 ? launch_bwd<64>(a, stream) : launch_bwd<128>(a, stream);
 }
 

@@ -103,18 +103,14 @@ __device__ __forceinline__ int piece_at(int r, int c) {
   return r * (2 * DP) + ((c ^ piece_swizzle<DP>(r)) << 4);
 }
 
-// Operand of 8 reduction elements from a tile's rows: rows k .. k + 3 and
-// k + 8 .. k + 11 (k = k0 + 4 (lane / 32)) of column c0 + lane % 32.  These are
-// the rows whose sums a 32 x 32 product leaves in this lane's registers
-// 0 .. 7, so that such sums are the other operand as they are.
-template <int DP>
-__device__ __forceinline__ u32x4 column_operand(const uint8_t* tile, int k0, int c0, int lane) {
-  const int p = lane & 15;
-  const int r = k0 + 4 * (lane >> 5) + (p >> 2);
-  const int c = c0 + 16 * ((lane >> 4) & 1) + 4 * (p & 3);
-  const u32x2 lo = ds_read_tr16(tile + piece_at<DP>(r, c >> 3) + (c & 7) * 2);
-  const u32x2 hi = ds_read_tr16(tile + piece_at<DP>(r + 8, c >> 3) + (c & 7) * 2);
-  return u32x4{lo.x, lo.y, hi.x, hi.y};
+// 16 bytes a lane from offset `at` of [base, base + bytes) straight into LDS:
+// 1 KB from dst on.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t bytes, uint8_t* dst, uint32_t at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(uniform_rsrc(base, bytes), (lds_ptr_t)dst, 16, at, 0, 0, 0);
+}
+// .. 4 bytes a lane, 256 in all.
+__device__ __forceinline__ void load_word_to_lds(const void* base, uint32_t bytes, uint8_t* dst, uint32_t at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(uniform_rsrc(base, bytes), (lds_ptr_t)dst, 4, at, 0, 0, 0);
 }
 
 // Sets the elements that are not finite to zero; 0 if there were none.
@@ -142,7 +138,10 @@ __device__ __forceinline__ float max_halves(float x) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// Registers 8 kg .. 8 kg + 7 of a 32 x 32 product as an operand in bf16.
+// Registers 8 kg .. 8 kg + 7 of a 32 x 32 product as an operand in bf16: eight
+// reduction elements, rows k .. k + 3 and k + 8 .. k + 11 (k = 16 kg + 4 (lane
+// / 32)) of the product, so the other operand takes the same rows of its tile,
+// by transposing reads.
 __device__ __forceinline__ u32x4 pack_operand(const f32x16& s, int kg) {
   u32x4 o;
 #pragma unroll

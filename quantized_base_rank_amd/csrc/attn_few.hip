@@ -34,11 +34,6 @@ struct Group {
   uint32_t there;   // two blocks of 16 keys
 };
 
-// 1 KB, 16 bytes a lane from offset `at` of [base, base + bytes), into LDS.
-__device__ __forceinline__ void load_to_lds(const void* base, uint32_t bytes, uint8_t* dst, uint32_t at) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(uniform_rsrc(base, bytes), (lds_ptr_t)dst, 16, at, 0, 0, 0);
-}
-
 // Codes 8 e .. 8 e + 7 of a piece of 16, in bf16.
 __device__ __forceinline__ u32x4 codes_operand(u32x4 w, int e) {
   const u32x2 a = codes_bf16(w[2 * e]), b = codes_bf16(w[2 * e + 1]);

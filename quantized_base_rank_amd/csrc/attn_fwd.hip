@@ -39,12 +39,6 @@ namespace {
 constexpr int kBN = 64;          // keys of a step
 constexpr float kRaise = 8.0f;   // log2 of what p may reach
 
-// 16 bytes a lane from offset `at` of [base, base + bytes) straight into LDS:
-// 1 KB from dst on.
-__device__ __forceinline__ void load_to_lds(const void* base, uint32_t bytes, uint8_t* dst, uint32_t at) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(uniform_rsrc(base, bytes), (lds_ptr_t)dst, 16, at, 0, 0, 0);
-}
-
 // Waits until at most VM of this wave's loads and LG of its LDS accesses are
 // on their way (-1: any number), then meets the other waves.
 template <int VM, int LG>

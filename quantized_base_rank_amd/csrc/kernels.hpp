@@ -477,7 +477,7 @@ struct AttnBwdArgs {
   float c2, scale;
   uint16_t *dq, *dk, *dv;      // rows dq_ld, dk_ld, dv_ld elements apart
   int64_t dq_ld, dk_ld, dv_ld;
-  float *lse2, *delta;         // [Hkv][T g]: lse log2(e), sum do o
+  float *lse2, *delta;         // [Hkv][T g] (scratch): -lse log2(e), -sum do o
 };
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, hipStream_t stream);
 
