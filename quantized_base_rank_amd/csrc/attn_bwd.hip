@@ -19,12 +19,17 @@
 // and ds, Z the products that sum,
 //     X(second) beside Y(first);  Z(first) beside Y(second);
 //     barrier;  Z(second) and X(the next tile's first).
+// The order of instructions is the source's: behind each matrix instruction
+// stand the LDS read of the operand some products further on and its share
+// of Y.
 //
 // Roundings: p and ds to bf16 as operands of the products that sum over
 // queries and keys; all sums fp32.
 #include "attn_common.hpp"
 #include "kernels.hpp"
 #include "q8_common.hpp"
+
+#include <utility>
 
 namespace qlin {
 
@@ -34,7 +39,7 @@ constexpr int kBK = 128;  // rows, or keys, of a workgroup
 constexpr int kBT = 64;   // keys, or rows, of a step
 
 // Waits for this wave's loads, then meets the other waves.
-__device__ __forceinline__ void tile_barrier() { __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+__device__ __forceinline__ void tile_barrier() { __asm__ volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Lane's offset within the tiles for its row and column operands.
 template <int DP>
@@ -61,19 +66,18 @@ __device__ __forceinline__ u32x4 col_operand(const uint8_t* tile, TileAt<DP> at,
   return u32x4{lo.x, lo.y, hi.x, hi.y};
 }
 
-// Order of a turn's instructions: N matrix instructions, behind each of them V
-// others, T transcendental ones and R LDS reads.
-template <int N, int V, int T, int R>
-__device__ __forceinline__ void turn_order() {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if constexpr (R > 0) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
-    if constexpr (V > 0) __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
-    if constexpr (T > 0) __builtin_amdgcn_sched_group_barrier(0x400, T, 0);
-  }
-  __builtin_amdgcn_sched_barrier(0);
+// f(0), f(1), ... f(N - 1) with the numbers as types.
+template <int... I, typename F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
 }
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  each(std::make_integer_sequence<int, N>{}, f);
+}
+
+// Nothing moves past this point.
+__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
 
 template <int DP>
 __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
@@ -153,50 +157,90 @@ __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
   f32x16 dq[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) dq[d] = f32x16{};
-  f32x16 s0, p0, s1, p1;  // scores and do . v - delta of a tile's first and second 32 keys
-  u32x4 d0[2], d1[2];     // their ds
-  auto x = [&](int buf, int kb, f32x16& s, f32x16& dp) __attribute__((always_inline)) {
-    s = f32x16{};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dp[i] = -delta;
-#pragma unroll
-    for (int t = 0; t < KS; ++t) {
-      s = mfma32(row_operand<DP>(sk(buf), at, kb, t), qf[t], s);
-      dp = mfma32(row_operand<DP>(sv(buf), at, kb, t), yf[t], dp);
-    }
+  // scores and do . v - delta of a tile's first and second 32 keys, then ds
+  f32x16 s0, p0, s1, p1;
+  u32x4 d0[2], d1[2];
+  // Operands of a tile's products in their order: X(second), Z(first),
+  // Z(second), X(first of the next tile), and X(second) of that one again
+  constexpr int NX = 2 * KS, NZ = 2 * DB, kAll = 2 * NX + 2 * NZ, kAhead = 8;
+  static_assert(kAll % kAhead == 0 && NX >= kAhead, "the ring goes on into the next tile");
+  u32x4 ring[kAhead];
+  auto operand = [&](int buf, int n) __attribute__((always_inline)) {
+    if (n < NX) return row_operand<DP>(n % 2 == 0 ? sk(buf) : sv(buf), at, 1, n / 2);
+    if (n < NX + 2 * NZ) return col_operand<DP>(sk(buf), at, (n - NX) / DB, (n - NX) % DB);
+    const int m = n - NX - 2 * NZ;
+    return row_operand<DP>(m % 2 == 0 ? sk(buf + 1) : sv(buf + 1), at, m < NX ? 0 : 1, m % NX / 2);
   };
-  auto y = [&](auto cut, int j0, f32x16& s, const f32x16& dp, u32x4 (&ds)[2]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.c2, -lse2));
-      s[i] = decltype(cut)::value && j0 + acc_row(i, h) >= seen ? 0.0f : p * dp[i];
-    }
-    ds[0] = pack_operand(s, 0);
-    ds[1] = pack_operand(s, 1);
+  auto value = [&](auto cut, int j0, f32x16& s, const f32x16& dp, int i) __attribute__((always_inline)) {
+    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.c2, -lse2));
+    s[i] = decltype(cut)::value && j0 + acc_row(i, h) >= seen ? 0.0f : p * dp[i];
   };
-  auto z = [&](int buf, int kb, const u32x4 (&ds)[2]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-      for (int d = 0; d < DB; ++d) dq[d] = mfma32(col_operand<DP>(sk(buf), at, 2 * kb + kg, d), ds[kg], dq[d]);
+  auto pack = [&](const f32x16& s, u32x4 (&ds)[2], int i) __attribute__((always_inline)) {  // values i, i + 1
+    ds[i / 8][i % 8 / 2] = pack_bf16x2(s[i], s[i + 1]);
   };
   auto step = [&](auto cut, int tile, int buf) __attribute__((always_inline)) {
     const int j0 = tile * kBT;
-    constexpr int kMore = decltype(cut)::value ? 4 : 2;
-    x(buf, 1, s1, p1);
-    y(cut, j0, s0, p0, d0);
-    turn_order<2 * KS, kMore * 16 / KS, 16 / KS, 1>();
-    z(buf, 0, d0);
-    y(cut, j0 + 32, s1, p1, d1);
-    turn_order<2 * DB, kMore * 32 / DB, 32 / DB / 2, 2>();
-    tile_barrier();
-    load(tile + 2, buf + 2);
-    z(buf, 1, d1);
-    x(buf + 1, 0, s0, p0);
-    turn_order<2 * DB, 0, 0, 2>();
+    each<kAll>([&](auto number) __attribute__((always_inline)) {
+      constexpr int n = decltype(number)::value;
+      if constexpr (n == NX + NZ) {
+        tile_barrier();
+        load(tile + 2, buf + 2);
+      }
+      const u32x4 f = ring[n % kAhead];
+      if constexpr (n < NX) {
+        if (n % 2 == 0)
+          s1 = mfma32(f, qf[n / 2], n == 0 ? f32x16{} : s1);
+        else
+          p1 = mfma32(f, yf[n / 2], p1);
+      } else if constexpr (n < NX + 2 * NZ) {
+        constexpr int m = n - NX, kg = m / DB;
+        dq[m % DB] = mfma32(f, kg < 2 ? d0[kg & 1] : d1[kg & 1], dq[m % DB]);
+      } else {
+        constexpr int m = n - NX - 2 * NZ;
+        if (m % 2 == 0)
+          s0 = mfma32(f, qf[m / 2], m == 0 ? f32x16{} : s0);
+        else
+          p0 = mfma32(f, yf[m / 2], p0);
+      }
+      // (the next tile's operands only behind the barrier)
+      if constexpr (n + kAhead < NX + 2 * NZ || n >= NX + NZ) ring[n % kAhead] = operand(buf, n + kAhead);
+      if constexpr (n == NX + NZ) {
+#pragma unroll
+        for (int m = NX + 2 * NZ; m < n + kAhead; ++m) ring[m % kAhead] = operand(buf, m);
+      }
+      if constexpr (n < NX) {
+#pragma unroll
+        for (int i = 16 * n / NX; i < 16 * (n + 1) / NX; ++i) {
+          value(cut, j0, s0, p0, i);
+          if (i % 2 == 1) pack(s0, d0, i - 1);
+        }
+      } else if constexpr (n < NX + NZ) {
+#pragma unroll
+        for (int i = 16 * (n - NX) / NZ; i < 16 * (n - NX + 1) / NZ; ++i) {
+          value(cut, j0 + 32, s1, p1, i);
+          if (i % 2 == 1) pack(s1, d1, i - 1);
+        }
+      } else if constexpr (n < NX + 2 * NZ) {
+#pragma unroll
+        for (int i = 16 * (n - NX - NZ) / NZ; i < 16 * (n - NX - NZ + 1) / NZ; ++i) p0[i] = p1[i] = -delta;
+      }
+      pin();
+    });
   };
   tile_barrier();
-  x(0, 0, s0, p0);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) p0[i] = p1[i] = -delta;
+#pragma unroll
+  for (int n = 0; n < NX; ++n) {
+    const u32x4 f = row_operand<DP>(n % 2 == 0 ? sk0 : sv0, at, 0, n / 2);
+    if (n % 2 == 0)
+      s0 = mfma32(f, qf[n / 2], n == 0 ? f32x16{} : s0);
+    else
+      p0 = mfma32(f, yf[n / 2], p0);
+  }
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) ring[n] = operand(0, n);
+  pin();
   constexpr std::integral_constant<bool, true> cut{};
   constexpr std::integral_constant<bool, false> whole{};
   const int tiles_all = (tok0 + 1) / kBT, tiles_end = (end + kBT - 1) / kBT;
@@ -270,9 +314,10 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkdv(AttnBwdArgs a) {
     }
     const int left = rows - r0;
     const uint32_t bytes = left > 0 ? static_cast<uint32_t>(left < kBT ? left : kBT) * 4u : 0u;
-    if (wave < 2)
-      load_word_to_lds((wave == 0 ? a.lse2 : a.delta) + (static_cast<int64_t>(kvh) * a.T + rt.s0) * g + r0, bytes,
-                       reinterpret_cast<uint8_t*>(sl(buf) + wave * kBT), static_cast<uint32_t>(lane * 4));
+    // (waves 2 and 3 load the same again: a branch here would break up the order
+    // of the instructions around it)
+    load_word_to_lds(((wave & 1) == 0 ? a.lse2 : a.delta) + (static_cast<int64_t>(kvh) * a.T + rt.s0) * g + r0, bytes,
+                     reinterpret_cast<uint8_t*>(sl(buf) + (wave & 1) * kBT), static_cast<uint32_t>(lane * 4));
   };
   load(0, 0);
   load(1, 1);
@@ -292,70 +337,115 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkdv(AttnBwdArgs a) {
 #pragma unroll
   for (int d = 0; d < DB; ++d) dk[d] = dv[d] = f32x16{};
 
-  f32x16 s0, p0, s1, p1;            // scores and do . v - delta of a tile's first and second 32 rows
-  u32x4 e0[2], d0[2], e1[2], d1[2];  // their p and ds
-  auto x = [&](int buf, int qb, f32x16& s, f32x16& dp) __attribute__((always_inline)) {
-    s = f32x16{};
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(sl(buf) + kBT + qb * 32 + acc_row(i, h));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dp[i + e] = v[e];
-    }
-#pragma unroll
-    for (int t = 0; t < KS; ++t) {
-      s = mfma32(row_operand<DP>(sq(buf), at, qb, t), kf[t], s);
-      dp = mfma32(row_operand<DP>(sy(buf), at, qb, t), vf[t], dp);
-    }
+  // scores and do . v - delta of a tile's first and second 32 rows, then p and ds
+  f32x16 s0, p0, s1, p1;
+  u32x4 e0[2], d0[2], e1[2], d1[2];
+  // Operands of a tile's products, in the order of k_attn_dq; those of Z for dv
+  // and dk in turns
+  constexpr int NX = 2 * KS, NZ = 4 * DB, kAll = 2 * NX + 2 * NZ, kAhead = 4;
+  static_assert(kAll % kAhead == 0 && NX >= kAhead, "the ring goes on into the next tile");
+  u32x4 ring[kAhead];
+  auto operand = [&](int buf, int n) __attribute__((always_inline)) {
+    if (n < NX) return row_operand<DP>(n % 2 == 0 ? sq(buf) : sy(buf), at, 1, n / 2);
+    if (n < NX + 2 * NZ) return col_operand<DP>(n % 2 == 0 ? sy(buf) : sq(buf), at, (n - NX) / (2 * DB), (n - NX) / 2 % DB);
+    const int m = n - NX - 2 * NZ;
+    return row_operand<DP>(m % 2 == 0 ? sq(buf + 1) : sy(buf + 1), at, m < NX ? 0 : 1, m % NX / 2);
   };
+  f32x4 lse[2];  // -lse of four rows, and of the next four
+  auto lse_at = [&](int buf, int r) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4*>(sl(buf) + r + 4 * h); };
   // rows key g on see the key; of those past the sequence do and delta are zero,
   // and so is what they add
-  auto y = [&](auto cut, int r0, int buf, int qb, f32x16& s, f32x16& dp, u32x4 (&p)[2], u32x4 (&ds)[2])
-      __attribute__((always_inline)) {
-    const int64_t ahead = static_cast<int64_t>(key) * g - r0;
-    const int from = ahead > kBT ? kBT : static_cast<int>(ahead);
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(sl(buf) + qb * 32 + acc_row(i, h));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], a.c2, v[e]));
-        s[i + e] = decltype(cut)::value && qb * 32 + acc_row(i + e, h) < from ? 0.0f : w;
-        dp[i + e] *= s[i + e];
-      }
-    }
-#pragma unroll
-    for (int kg = 0; kg < 2; ++kg) {
-      p[kg] = pack_operand(s, kg);
-      ds[kg] = pack_operand(dp, kg);
-    }
+  auto value = [&](auto cut, int r, int from, f32x16& s, f32x16& dp, int i) __attribute__((always_inline)) {
+    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.c2, lse[i / 4 & 1][i & 3]));
+    s[i] = decltype(cut)::value && r + acc_row(i, h) < from ? 0.0f : p;
+    dp[i] *= s[i];
   };
-  auto z = [&](int buf, int qb, const u32x4 (&p)[2], const u32x4 (&ds)[2]) __attribute__((always_inline)) {
+  auto pack = [&](const f32x16& s, u32x4 (&p)[2], int i) __attribute__((always_inline)) {  // values i, i + 1
+    p[i / 8][i % 8 / 2] = pack_bf16x2(s[i], s[i + 1]);
+  };
+  auto minus_delta = [&](int buf, int r, f32x16& dp, int i) __attribute__((always_inline)) {  // of four rows
+    const f32x4 v = *reinterpret_cast<const f32x4*>(sl(buf) + kBT + r + acc_row(i, h));
 #pragma unroll
-    for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        dv[d] = mfma32(col_operand<DP>(sy(buf), at, 2 * qb + kg, d), p[kg], dv[d]);
-        dk[d] = mfma32(col_operand<DP>(sq(buf), at, 2 * qb + kg, d), ds[kg], dk[d]);
-      }
+    for (int e = 0; e < 4; ++e) dp[i + e] = v[e];
   };
   auto step = [&](auto cut, int tile, int buf) __attribute__((always_inline)) {
-    const int r0 = begin + tile * kBT;
-    constexpr int kMore = decltype(cut)::value ? 4 : 3;
-    x(buf, 1, s1, p1);
-    y(cut, r0, buf, 0, s0, p0, e0, d0);
-    turn_order<2 * KS, kMore * 16 / KS, 16 / KS, 1>();
-    z(buf, 0, e0, d0);
-    y(cut, r0, buf, 1, s1, p1, e1, d1);
-    turn_order<4 * DB, kMore * 8 / DB, 8 / DB / 2, 2>();
-    tile_barrier();
-    load(tile + 2, buf + 2);
-    z(buf, 1, e1, d1);
-    x(buf + 1, 0, s0, p0);
-    turn_order<4 * DB, 0, 0, 2>();
+    const int64_t ahead = static_cast<int64_t>(key) * g - begin - static_cast<int64_t>(tile) * kBT;
+    const int from = ahead > kBT ? kBT : static_cast<int>(ahead);
+    each<kAll>([&](auto number) __attribute__((always_inline)) {
+      constexpr int n = decltype(number)::value;
+      if constexpr (n == NX + NZ) {
+        tile_barrier();
+        load(tile + 2, buf + 2);
+      }
+      const u32x4 f = ring[n % kAhead];
+      if constexpr (n < NX) {
+        if (n % 2 == 0)
+          s1 = mfma32(f, kf[n / 2], n == 0 ? f32x16{} : s1);
+        else
+          p1 = mfma32(f, vf[n / 2], p1);
+      } else if constexpr (n < NX + 2 * NZ) {
+        constexpr int m = n - NX, kg = m / (2 * DB), d = m / 2 % DB;
+        if (m % 2 == 0)
+          dv[d] = mfma32(f, kg < 2 ? e0[kg & 1] : e1[kg & 1], dv[d]);
+        else
+          dk[d] = mfma32(f, kg < 2 ? d0[kg & 1] : d1[kg & 1], dk[d]);
+      } else {
+        constexpr int m = n - NX - 2 * NZ;
+        if (m % 2 == 0)
+          s0 = mfma32(f, kf[m / 2], m == 0 ? f32x16{} : s0);
+        else
+          p0 = mfma32(f, vf[m / 2], p0);
+      }
+      // (the next tile's operands only behind the barrier)
+      if constexpr (n + kAhead < NX + 2 * NZ || n >= NX + NZ) ring[n % kAhead] = operand(buf, n + kAhead);
+      if constexpr (n < NX) {
+#pragma unroll
+        for (int i = 16 * n / NX; i < 16 * (n + 1) / NX; ++i) {
+          value(cut, 0, from, s0, p0, i);
+          if (i % 2 == 1) pack(s0, e0, i - 1), pack(p0, d0, i - 1);
+          if (i % 4 == 3) lse[i / 4 & 1] = lse_at(buf, i < 8 ? 8 * (i / 4) + 16 : 32 + 8 * (i / 4 - 2));
+        }
+      } else if constexpr (n < NX + NZ) {
+#pragma unroll
+        for (int i = 16 * (n - NX) / NZ; i < 16 * (n - NX + 1) / NZ; ++i) {
+          value(cut, 32, from, s1, p1, i);
+          if (i % 2 == 1) pack(s1, e1, i - 1), pack(p1, d1, i - 1);
+          if (i % 4 == 3 && i < 8) lse[i / 4 & 1] = lse_at(buf, 32 + 8 * (i / 4) + 16);
+        }
+      } else if constexpr (n < NX + 2 * NZ) {
+        constexpr int m = n - NX - NZ;  // the next tile's, in eight pieces and two
+#pragma unroll
+        for (int i = 10 * m / NZ; i < 10 * (m + 1) / NZ; ++i) {
+          if (i < 4)
+            minus_delta(buf + 1, 0, p0, 4 * i);
+          else if (i < 8)
+            minus_delta(buf + 1, 32, p1, 4 * (i - 4));
+          else
+            lse[i - 8] = lse_at(buf + 1, 8 * (i - 8));
+        }
+      }
+      pin();
+    });
   };
   tile_barrier();
-  x(0, 0, s0, p0);
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    minus_delta(0, 0, p0, i);
+    minus_delta(0, 32, p1, i);
+  }
+  lse[0] = lse_at(0, 0);
+  lse[1] = lse_at(0, 8);
+#pragma unroll
+  for (int n = 0; n < NX; ++n) {
+    const u32x4 f = row_operand<DP>(n % 2 == 0 ? sq0 : sy0, at, 0, n / 2);
+    if (n % 2 == 0)
+      s0 = mfma32(f, kf[n / 2], n == 0 ? f32x16{} : s0);
+    else
+      p0 = mfma32(f, vf[n / 2], p0);
+  }
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) ring[n] = operand(0, n);
+  pin();
   constexpr std::integral_constant<bool, true> cut{};
   constexpr std::integral_constant<bool, false> whole{};
   const int tiles = (rows - begin + kBT - 1) / kBT;
