@@ -139,23 +139,22 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   const int page_mask = (1 << a.c.page_shift) - 1;
   const bool holds = (kBN * kChunks >= 64 * W || tid < kBN * kChunks) && 16 * chunk < D;
   uint32_t queue = 0xFFFF;  // blocks of 16 keys that are there, four bits a step
-  auto page_at = [&](int j, int blk) {
-    const int at = base + j * kBN + 16 * blk;
-    return at < end ? uniform_page(a.s.table, a.s.table_len, a.c.pages, a.c.page_shift, rt.b, at) : -1;
+  // Lane i % 4: the page of block i % 4 of step j, -1 if it is not there.  (A
+  // vector load: waits for scalar ones would wait for LDS too.)
+  auto pages_of = [&](int j) {
+    const int place = base + j * kBN + 16 * (lane & 3), at = place >> a.c.page_shift;
+    if (place >= end || at >= a.s.table_len) return -1;
+    const int p = a.s.table[static_cast<int64_t>(rt.b) * a.s.table_len + at];
+    return p < a.c.pages ? p : -1;
   };
-  auto blocks = [&](int j) {
-    uint32_t b = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b |= page_at(j, i) >= 0 ? 1u << i : 0u;
-    return b;
-  };
+  auto blocks = [&](int p) { return static_cast<uint32_t>(__ballot(p >= 0)) & 0xFu; };
   u32x4 held_k[kHold], held_v[kHold];
   float held_ks[kHold], held_vs[kHold];
-  auto fetch = [&](int j, bool values) {
+  auto fetch = [&](int j, int p, bool values) {
 #pragma unroll
     for (int i = 0; i < kHold; ++i) {
       const int r = row_t + i * (64 * W / kChunks);
-      const int pg = page_at(j, __builtin_amdgcn_readfirstlane(r >> 4));
+      const int pg = __builtin_amdgcn_readlane(p, __builtin_amdgcn_readfirstlane(r >> 4) & 3);
       (values ? held_v : held_k)[i] = u32x4{0, 0, 0, 0};
       if (pg >= 0 && holds) {
         const int64_t row = ((static_cast<int64_t>(pg) * a.c.H + kvh) << a.c.page_shift) + ((base + j * kBN + r) & page_mask);
@@ -306,21 +305,25 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   };
 
   const bool second = W == 8 && wave >= 4;
+  int page_k = -1, page_v = -1;  // pages of steps j + 4 and j + 3
   if (steps > 0) {
     if constexpr (PAGED) {
-      fetch(0, false);
-      fetch(0, true);
+      const int q0 = pages_of(0), q1 = pages_of(1), q2 = pages_of(2), q3 = pages_of(3);
+      fetch(0, q0, false);
+      fetch(0, q0, true);
       put(0, false);
       put(0, true);
-      fetch(1, false);
-      fetch(1, true);
+      fetch(1, q1, false);
+      fetch(1, q1, true);
       put(1, false);
       put(1, true);
-      fetch(2, false);
+      fetch(2, q2, false);
       put(2, false);
-      fetch(3, false);
-      fetch(2, true);
-      queue = blocks(1) | blocks(2) << 4 | blocks(3) << 8 | blocks(4) << 12;
+      fetch(3, q3, false);
+      fetch(2, q2, true);
+      queue = blocks(q0) | blocks(q1) << 4 | blocks(q2) << 8 | blocks(q3) << 12;
+      page_v = q3;
+      page_k = pages_of(4);
       barrier<-1, 0>();
     } else {
       load_packed(0, 0, false);
@@ -340,7 +343,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
     }
     if (base < w_end) {
       scores(0);
-      softmax(0, 0, PAGED ? blocks(0) : 0xFu);
+      softmax(0, 0, queue & 0xFu);
     }
     if (second) barrier<-1, -1>();
     // the end of step j's matrix phase, and the softmax phase
@@ -358,14 +361,16 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
       if constexpr (PAGED) {
         put(buf, false);
         put(buf + 2, true);
-        fetch(j + 4, false);
-        fetch(j + 3, true);
+        queue = queue >> 4 | blocks(page_k) << 12;
+        fetch(j + 4, page_k, false);
+        fetch(j + 3, page_v, true);
+        page_v = page_k;
+        page_k = pages_of(j + 5);
       } else {
         load_packed(j + 3, buf, false);
         load_packed(j + 2, buf + 2, true);
       }
       if (base + (j + 1) * kBN < w_end) softmax(j + 1, buf + 1, queue & 0xFu);
-      if constexpr (PAGED) queue = queue >> 4 | blocks(j + 5) << 12;
       __builtin_amdgcn_sched_barrier(0);
       barrier<-1, PAGED ? 0 : -1>();
       __builtin_amdgcn_sched_barrier(0);
