@@ -29,8 +29,6 @@
 #include "kernels.hpp"
 #include "q8_common.hpp"
 
-#include <utility>
-
 namespace qlin {
 
 namespace {
@@ -65,19 +63,6 @@ __device__ __forceinline__ u32x4 col_operand(const uint8_t* tile, TileAt<DP> at,
   const u32x2 hi = ds_read_tr16(tile + (at.col ^ (d << 6) ^ (DP == 128 ? 16 : 0)) + (kg * 16 + 8) * DP * 2);
   return u32x4{lo.x, lo.y, hi.x, hi.y};
 }
-
-// f(0), f(1), ... f(N - 1) with the numbers as types.
-template <int... I, typename F>
-__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void each(F f) {
-  each(std::make_integer_sequence<int, N>{}, f);
-}
-
-// Nothing moves past this point.
-__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
 
 template <int DP>
 __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
@@ -258,17 +243,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
   if (t < tiles_end) step(cut, t, 0);
   if (t + 1 < tiles_end) step(cut, t + 1, 1);
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (loads into LDS end before the workgroup does)
-  if (!in) return;
-  uint16_t* const out = a.dq + t_row * a.dq_ld + hq * D;
-#pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int c = 32 * d + acc_row(i, h);
-      if (c < D)
-        *reinterpret_cast<u32x2*>(out + c) = u32x2{pack_bf16x2(dq[d][i] * a.scale, dq[d][i + 1] * a.scale),
-                                                   pack_bf16x2(dq[d][i + 2] * a.scale, dq[d][i + 3] * a.scale)};
-    }
+  store_row<DB>(dq, a.scale, a.dq + t_row * a.dq_ld + hq * D, D, in, h);
 }
 
 template <int DP>
@@ -464,19 +439,8 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkdv(AttnBwdArgs a) {
   if (t < tiles) step(cut, t, 0);
   if (t + 1 < tiles) step(cut, t + 1, 1);
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  if (!in) return;
-  uint16_t* const odk = a.dk + krow * a.dk_ld + kvh * D;
-  uint16_t* const odv = a.dv + krow * a.dv_ld + kvh * D;
-#pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int c = 32 * d + acc_row(i, h);
-      if (c >= D) continue;
-      *reinterpret_cast<u32x2*>(odv + c) = u32x2{pack_bf16x2(dv[d][i], dv[d][i + 1]), pack_bf16x2(dv[d][i + 2], dv[d][i + 3])};
-      *reinterpret_cast<u32x2*>(odk + c) = u32x2{pack_bf16x2(dk[d][i] * a.scale, dk[d][i + 1] * a.scale),
-                                                 pack_bf16x2(dk[d][i + 2] * a.scale, dk[d][i + 3] * a.scale)};
-    }
+  store_row<DB>(dk, a.scale, a.dk + krow * a.dk_ld + kvh * D, D, in, h);
+  store_row<DB>(dv, 1.0f, a.dv + krow * a.dv_ld + kvh * D, D, in, h);
 }
 
 template <int DP>

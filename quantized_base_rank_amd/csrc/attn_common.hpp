@@ -10,6 +10,8 @@
 #include "device_common.hpp"
 #include "kernels.hpp"
 
+#include <utility>
+
 namespace qlin {
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
@@ -90,6 +92,19 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int B, int T, int t) {
 // x / g for x < 65536 / g (x g < 65536), with m = ceil(65536 / g).
 __device__ __forceinline__ int small_div(int x, int m) { return (x * m) >> 16; }
 
+// f(0), f(1), ... f(N - 1) with the numbers as types.
+template <int... I, typename F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  each(std::make_integer_sequence<int, N>{}, f);
+}
+
+// No instruction moves past this point.
+__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
+
 // LDS tiles: rows of DP bf16 elements in pieces of 16 bytes, piece c of row r
 // at c ^ piece_swizzle(r).  Eight consecutive rows then have a piece in eight
 // different bank groups (row reads), and the four rows of a transposing read
@@ -160,6 +175,25 @@ __device__ __forceinline__ u32x2 codes_bf16(uint32_t w) {
   o.x = perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
   o.y = perm(__float_as_uint(d), __float_as_uint(c), 0x07060302u);
   return o;
+}
+
+// A row's elements from the sums of 32 x 32 products (register i of block d:
+// element 32 d + acc_row(i, h) of row lane % 32) times f, as bf16, to out[0 .. D).
+// The halves of the wave hold four elements of every eight: they change places
+// so that each lane stores eight.
+template <int DB>
+__device__ __forceinline__ void store_row(const f32x16 (&x)[DB], float f, uint16_t* out, int D, bool in, int h) {
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+      const auto y0 = __builtin_amdgcn_permlane32_swap(pack_bf16x2(x[d][i] * f, x[d][i + 1] * f),
+                                                       pack_bf16x2(x[d][i + 4] * f, x[d][i + 5] * f), false, false);
+      const auto y1 = __builtin_amdgcn_permlane32_swap(pack_bf16x2(x[d][i + 2] * f, x[d][i + 3] * f),
+                                                       pack_bf16x2(x[d][i + 6] * f, x[d][i + 7] * f), false, false);
+      const int c = 32 * d + 2 * i + 8 * h;
+      if (in && c < D) *reinterpret_cast<u32x4*>(out + c) = u32x4{y0[0], y1[0], y0[1], y1[1]};
+    }
 }
 
 // The page that holds place j of sequence b, or -1: a table entry outside the

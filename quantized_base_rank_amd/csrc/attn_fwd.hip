@@ -2,18 +2,21 @@
 // or before token i's place, p the softmax of c q_i . k_j, in one pass over
 // the keys with a running maximum and sum per query row.
 //
-// A workgroup takes 32 W query rows (32 per wave) of one sequence and key head
-// and walks the keys 64 at a time.  The products are formed transposed,
-// S^T = K Q^T and O^T = V^T P^T: a lane then holds scores of one query row
-// only, so maximum and sum need a single exchange between the wave's halves,
-// and the scores in its registers are, rounded to bf16, the operand of the
-// second product as they stand.
+// A workgroup takes 256 query rows of one sequence and key head, 64 per wave
+// and one wave on a SIMD, and walks the keys 64 at a time.  The products are
+// formed transposed, S^T = K Q^T and O^T = V^T P^T: a lane then holds scores of
+// one query row only, so maximum and sum need a single exchange between the
+// wave's halves, and the scores in its registers are, rounded to bf16, the
+// operand of the second product as they stand.
 //
-// Steps are shifted by one: S of step j + 1 and O of step j are formed
-// together (32 matrix instructions at D = 128), then the softmax of step j + 1.
-// Of eight waves, two on each SIMD, four run their matrix phase while the
-// other four run their softmax, with a barrier between phases.  Keys and values
-// stream through three buffers each.
+// A step's 64 keys and the wave's 64 rows are four units of 32 x 32.  With X the
+// scores of a unit, Y its softmax and Z its share of O, the matrix instructions
+// of X(next unit) and Z(last unit) stand between the parts of Y(unit), in the
+// source's order; each operand of keys and values is read from LDS once for
+// the two units that share it, in place of the one that was last used, which
+// is a unit or more ahead of its use.  Packed keys and values go straight to
+// LDS, three steps ahead; cached ones through registers, where they become
+// bf16, two steps ahead.
 //
 // Roundings: p (0 .. 1) to bf16 for the second product, relative 2^-8 at most
 // and independent from key to key, while the sum of p takes the unrounded
@@ -32,46 +35,44 @@
 #include "attn_common.hpp"
 #include "kernels.hpp"
 
+#include <type_traits>
+
 namespace qlin {
 
 namespace {
 
-constexpr int kBN = 64;          // keys of a step
-constexpr float kRaise = 8.0f;   // log2 of what p may reach
+constexpr int kBM = 256;        // query rows of a workgroup
+constexpr int kBN = 64;         // keys of a step
+constexpr float kRaise = 8.0f;  // log2 of what p may reach
 
-// Waits until at most VM of this wave's loads and LG of its LDS accesses are
-// on their way (-1: any number), then meets the other waves.
-template <int VM, int LG>
+// Waits until at most VM of this wave's loads and none of its LDS accesses are
+// on their way, then meets the other waves.
+template <int VM>
 __device__ __forceinline__ void barrier() {
-  if constexpr (VM == 0 && LG == 0)
-    __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  else if constexpr (VM == 0)
-    __asm__ volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-  else if constexpr (LG == 0)
-    __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  else
-    __asm__ volatile("s_barrier" ::: "memory");
+  __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
 }
 
-template <int DP, bool PAGED, int W>
-__global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
+template <int DP, bool PAGED>
+__global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   constexpr int NP = DP / 8, KS = DP / 16, DB = DP / 32;
-  constexpr int kBM = 32 * W, kTile = kBN * DP * 2, kLoads = kTile / 1024 / W;
-  static_assert(kLoads >= 1, "every wave loads a part of each tile");
+  constexpr int kTile = kBN * DP * 2, kLoads = kTile / 4096;
   constexpr int kRowsPer = 64 / NP;  // rows of a load
-  // three buffers of keys and of values (an array each: a read of one is not
-  // held for loads into another), and the scales of cached ones
+  // buffers of keys and of values (an array each: a read of one is not held for
+  // loads into another; arrays that are never named take no room), and the
+  // scales of cached ones
+  constexpr int R = PAGED ? 3 : 4;
   __shared__ __attribute__((aligned(16))) uint8_t sk0[kTile];
   __shared__ __attribute__((aligned(16))) uint8_t sk1[kTile];
   __shared__ __attribute__((aligned(16))) uint8_t sk2[kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t sk3[kTile];
   __shared__ __attribute__((aligned(16))) uint8_t sv0[kTile];
   __shared__ __attribute__((aligned(16))) uint8_t sv1[kTile];
   __shared__ __attribute__((aligned(16))) uint8_t sv2[kTile];
-  __shared__ __attribute__((aligned(16))) float s_scale[PAGED ? 3 * 2 * kBN : 1];
-  __shared__ int s_odd[3];  // 1 + the step whose values in this buffer were not finite
-  if (threadIdx.x < 3) s_odd[threadIdx.x] = 0;
-  auto sk = [&](int buf) { return buf % 3 == 0 ? sk0 : buf % 3 == 1 ? sk1 : sk2; };
-  auto sv = [&](int buf) { return buf % 3 == 0 ? sv0 : buf % 3 == 1 ? sv1 : sv2; };
+  __shared__ __attribute__((aligned(16))) uint8_t sv3[kTile];
+  __shared__ __attribute__((aligned(16))) float s_scale[PAGED ? R * 2 * kBN : 1];
+  __shared__ int s_odd[R];  // 1 + the step whose values in this buffer were not finite
+  auto sk = [&](int buf) { return buf % R == 0 ? sk0 : buf % R == 1 ? sk1 : R == 3 || buf % R == 2 ? sk2 : sk3; };
+  auto sv = [&](int buf) { return buf % R == 0 ? sv0 : buf % R == 1 ? sv1 : R == 3 || buf % R == 2 ? sv2 : sv3; };
 
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -88,31 +89,35 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   const int base = PAGED ? share * a.per : 0, until = PAGED ? base + a.per : 0x7FFFFFFF;
   if (base > 0 && base >= len) return;  // (k_attn_join counts a sequence's shares alike)
   auto inside = [&](int v) { return v < until ? v : until; };
+  if (tid < R) s_odd[tid] = 0;
 
-  // this lane's query row
+  // this lane's query rows, one of each 32 of the wave's
   const int tok0 = rt.row0 / a.g, rem0 = rt.row0 - tok0 * a.g;
-  const int in_tile = wave * 32 + l32;
-  const bool in = rt.row0 + in_tile < rt.rows;
-  const int x = rem0 + in_tile, dt = small_div(x, a.g_inv);
-  const int tok = in ? tok0 + dt : tok0, hq = kvh * a.g + (in ? x - dt * a.g : 0);
-  const int seen = in ? inside(first + tok + 1) : 0;  // keys before this place count
   const int last_in = (rt.rows - rt.row0 < kBM ? rt.rows - rt.row0 : kBM) - 1;
-  const int end = inside(first + tok0 + small_div(rem0 + last_in, a.g_inv) + 1);  // keys of the tile's last row
-  const int w_last = wave * 32 + 31 < last_in ? wave * 32 + 31 : last_in;
-  // keys of the wave's last row, and keys that all its rows see
-  const int w_end = wave * 32 > last_in ? 0 : inside(first + tok0 + small_div(rem0 + w_last, a.g_inv) + 1);
-  const int w_all = wave * 32 + 31 > last_in ? 0 : inside(first + tok0 + small_div(rem0 + wave * 32, a.g_inv) + 1);
-  const int steps = end > base ? (end - base + kBN - 1) / kBN : 0;
-
-  u32x4 qf[KS];
-  const uint16_t* q = a.q + static_cast<int64_t>(rt.s0 + tok) * a.q_ld + hq * D;
+  auto token = [&](int r) { return tok0 + small_div(rem0 + r, a.g_inv); };  // of row r of the tile
+  auto lane_row = [&](int b) { return wave * 64 + b * 32 + l32; };
+  int seen[2];  // keys before this place count
+  u32x4 qf[2][KS];
 #pragma unroll
-  for (int s = 0; s < KS; ++s)
-    qf[s] = 16 * s + 8 * h < D ? *reinterpret_cast<const u32x4*>(q + 16 * s + 8 * h) : u32x4{0, 0, 0, 0};
+  for (int b = 0; b < 2; ++b) {
+    const int r = lane_row(b) <= last_in ? lane_row(b) : 0, t = token(r);
+    seen[b] = lane_row(b) <= last_in ? inside(first + t + 1) : 0;
+    const uint16_t* const q = a.q + static_cast<int64_t>(rt.s0 + t) * a.q_ld + (kvh * a.g + rem0 + r - (t - tok0) * a.g) * D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      qf[b][s] = 16 * s + 8 * h < D ? *reinterpret_cast<const u32x4*>(q + 16 * s + 8 * h) : u32x4{0, 0, 0, 0};
+  }
+  // keys of the tile's last row and of the wave's, and keys that every row sees
+  const int end = inside(first + token(last_in) + 1);
+  const int w_last = wave * 64 + 63 < last_in ? wave * 64 + 63 : last_in;
+  const int w_end = wave * 64 > last_in ? 0 : inside(first + token(w_last) + 1);
+  const int sees_all = inside(first + tok0 + 1) - base;
+  const int steps = end > base ? (end - base + kBN - 1) / kBN : 0;
+  const int whole = sees_all >= 2 * kBN ? (sees_all / kBN - 1) / R * R : 0;  // steps that nothing cuts, nor the next
 
-  // ---- loads of packed keys and values, straight into LDS: load i of a wave
-  // fills kRowsPer rows; rows past the sequence and elements past D lie outside
-  // the resource and read as zero
+  // ---- packed keys and values, straight into LDS: load i of a wave fills
+  // kRowsPer rows; rows past the sequence and elements past D lie outside the
+  // resource and read as zero
   uint32_t vo_k[kLoads], vo_v[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
@@ -122,23 +127,24 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
     vo_k[i] = (static_cast<uint32_t>(r) * static_cast<uint32_t>(a.k_ld * 2) + c * 16) | out;
     vo_v[i] = (static_cast<uint32_t>(r) * static_cast<uint32_t>(a.v_ld * 2) + c * 16) | out;
   }
-  auto load_packed = [&](int j, int buf, bool values) {
-    const int64_t ld = values ? a.v_ld : a.k_ld;
-    const int left = len - j * kBN;
-    const uint32_t bytes = left > 0 ? static_cast<uint32_t>(((left < kBN ? left : kBN) - 1) * ld + D) * 2u : 0u;
-    const uint16_t* const src = (values ? a.v : a.k) + (static_cast<int64_t>(rt.s0) + j * kBN) * ld + kvh * D;
-    uint8_t* const dst = (values ? sv(buf) : sk(buf)) + wave * kLoads * 1024;
+  auto load_packed = [&](int j, int buf) __attribute__((always_inline)) {
+    const int left = len - j * kBN, n = left < kBN ? left : kBN;
+    const uint32_t bk = left > 0 ? static_cast<uint32_t>((n - 1) * a.k_ld + D) * 2u : 0u;
+    const uint32_t bv = left > 0 ? static_cast<uint32_t>((n - 1) * a.v_ld + D) * 2u : 0u;
+    const uint16_t* const k = a.k + (static_cast<int64_t>(rt.s0) + j * kBN) * a.k_ld + kvh * D;
+    const uint16_t* const v = a.v + (static_cast<int64_t>(rt.s0) + j * kBN) * a.v_ld + kvh * D;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_to_lds(src, bytes, dst + i * 1024, values ? vo_v[i] : vo_k[i]);
+    for (int i = 0; i < kLoads; ++i) load_to_lds(k, bk, sk(buf) + (wave * kLoads + i) * 1024, vo_k[i]);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load_to_lds(v, bv, sv(buf) + (wave * kLoads + i) * 1024, vo_v[i]);
   };
-  // ---- keys and values from the cache: 16 codes a thread, held in registers
-  // for a step, then written to LDS as bf16.  A wave's rows of a load lie in
-  // one block of 16 keys, so in one page.
-  constexpr int kChunks = DP / 16, kHold = (kBN * kChunks + 64 * W - 1) / (64 * W);
+
+  // ---- keys and values from the cache: 16 codes a thread and time, held in
+  // registers for a step, then written to LDS as bf16.  A wave's rows of a time
+  // lie in one block of 16 keys, so in one page.
+  constexpr int kChunks = DP / 16, kHold = kBN * kChunks / 256;
   const int row_t = tid / kChunks, chunk = tid % kChunks;
   const int page_mask = (1 << a.c.page_shift) - 1;
-  const bool holds = (kBN * kChunks >= 64 * W || tid < kBN * kChunks) && 16 * chunk < D;
-  uint32_t queue = 0xFFFF;  // blocks of 16 keys that are there, four bits a step
   // Lane i % 4: the page of block i % 4 of step j, -1 if it is not there.  (A
   // vector load: waits for scalar ones would wait for LDS too.)
   auto pages_of = [&](int j) {
@@ -150,72 +156,59 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
   auto blocks = [&](int p) { return static_cast<uint32_t>(__ballot(p >= 0)) & 0xFu; };
   u32x4 held_k[kHold], held_v[kHold];
   float held_ks[kHold], held_vs[kHold];
-  auto fetch = [&](int j, int p, bool values) {
+  auto fetch = [&](int j, int p) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kHold; ++i) {
-      const int r = row_t + i * (64 * W / kChunks);
+      const int r = row_t + i * (256 / kChunks);
       const int pg = __builtin_amdgcn_readlane(p, __builtin_amdgcn_readfirstlane(r >> 4) & 3);
-      (values ? held_v : held_k)[i] = u32x4{0, 0, 0, 0};
-      if (pg >= 0 && holds) {
-        const int64_t row = ((static_cast<int64_t>(pg) * a.c.H + kvh) << a.c.page_shift) + ((base + j * kBN + r) & page_mask);
-        (values ? held_v : held_k)[i] = *reinterpret_cast<const u32x4*>((values ? a.c.v : a.c.k) + row * D + 16 * chunk);
-        if (!values && chunk == 0) {
-          held_ks[i] = a.c.ks[row];
-          held_vs[i] = a.c.vs[row];
-        }
-      }
+      // (a page that is not there is read as page 0, whose rows exist, and masked)
+      const int64_t row = ((static_cast<int64_t>(pg < 0 ? 0 : pg) * a.c.H + kvh) << a.c.page_shift) + ((base + j * kBN + r) & page_mask);
+      const int64_t at = row * D + (16 * chunk < D ? 16 * chunk : 0);  // (past D: the query's elements are zero there)
+      held_k[i] = *reinterpret_cast<const u32x4*>(a.c.k + at);
+      held_v[i] = *reinterpret_cast<const u32x4*>(a.c.v + at);
+      held_ks[i] = a.c.ks[row];
+      held_vs[i] = a.c.vs[row];
     }
   };
-  auto put = [&](int buf, bool values) {
-    uint8_t* const dst = values ? sv(buf) : sk(buf);
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      if (kBN * kChunks < 64 * W && tid >= kBN * kChunks) break;
-      const int r = row_t + i * (64 * W / kChunks);
-      const u32x4 c = (values ? held_v : held_k)[i];
-      const u32x2 w0 = codes_bf16(c.x), w1 = codes_bf16(c.y), w2 = codes_bf16(c.z), w3 = codes_bf16(c.w);
-      *reinterpret_cast<u32x4*>(dst + piece_at<DP>(r, 2 * chunk)) = u32x4{w0.x, w0.y, w1.x, w1.y};
-      *reinterpret_cast<u32x4*>(dst + piece_at<DP>(r, 2 * chunk + 1)) = u32x4{w2.x, w2.y, w3.x, w3.y};
-      if (!values && chunk == 0) {
-        s_scale[buf % 3 * 2 * kBN + r] = held_ks[i];
-        s_scale[buf % 3 * 2 * kBN + kBN + r] = held_vs[i];
-      }
-    }
+  // part n of 4 kHold: eight codes of a thread's sixteen, keys first
+  auto put = [&](int buf, int n) __attribute__((always_inline)) {
+    const int i = n / 2 % kHold, half = n % 2;
+    const bool values = n >= 2 * kHold;
+    const u32x4 c = values ? held_v[i] : held_k[i];
+    const int r = row_t + i * (256 / kChunks);
+    const u32x2 w0 = codes_bf16(c[2 * half]), w1 = codes_bf16(c[2 * half + 1]);
+    *reinterpret_cast<u32x4*>((values ? sv(buf) : sk(buf)) + piece_at<DP>(r, 2 * chunk + half)) = u32x4{w0.x, w0.y, w1.x, w1.y};
+    // (the row's threads write the same word)
+    if (half == 0) s_scale[buf % R * 2 * kBN + (values ? kBN : 0) + r] = values ? held_vs[i] : held_ks[i];
   };
 
-  // ---- fragments
+  // ---- operands
   const uint32_t k_at = static_cast<uint32_t>(piece_at<DP>(l32, h));
   const int p16 = lane & 15, vr = 4 * h + (p16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (p16 & 3);
   const uint32_t v_at = static_cast<uint32_t>(piece_at<DP>(vr, vc >> 3) + (vc & 7) * 2);
-
-  f32x16 o[DB], s[2];
-  u32x4 pf[4];
-#pragma unroll
-  for (int d = 0; d < DB; ++d) o[d] = f32x16{};
-  float m = kMinusInf, l = 0.0f;
-
-  auto key = [&](int buf, int kb, int t) {
-    return *reinterpret_cast<const u32x4*>(sk(buf) + (k_at ^ (t << 5)) + kb * 32 * DP * 2);
+  auto key = [&](int buf, int half, int t) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u32x4*>(sk(buf) + (k_at ^ (t << 5)) + half * 32 * DP * 2);
   };
-  auto value = [&](int buf, int kg, int d) {
-    const uint8_t* const at = sv(buf) + (v_at ^ (d << 6)) + kg * 16 * DP * 2;
-    const uint8_t* const at8 = sv(buf) + (v_at ^ (d << 6) ^ (DP == 128 ? 16 : 0)) + (kg * 16 + 8) * DP * 2;
-    const u32x2 lo = ds_read_tr16(at), hi = ds_read_tr16(at8);
+  auto value = [&](int buf, int half, int n) __attribute__((always_inline)) {  // n = kg DB + d
+    const int kg = 2 * half + n / DB, d = n % DB;
+    const u32x2 lo = ds_read_tr16(sv(buf) + (v_at ^ (d << 6)) + kg * 16 * DP * 2);
+    const u32x2 hi = ds_read_tr16(sv(buf) + (v_at ^ (d << 6) ^ (DP == 128 ? 16 : 0)) + (kg * 16 + 8) * DP * 2);
     return u32x4{lo.x, lo.y, hi.x, hi.y};
   };
-  auto scores = [&](int buf) __attribute__((always_inline)) {
-    s[0] = s[1] = f32x16{};
+
+  u32x4 kf[KS], vf[2 * DB];  // of the unit at hand
+  f32x16 o[2][DB], s[2];
+  u32x4 p[2][2];
+  float m[2] = {kMinusInf, kMinusInf}, l[2] = {0.0f, 0.0f}, tops[4];
 #pragma unroll
-    for (int t = 0; t < KS; ++t)
+  for (int b = 0; b < 2; ++b) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) s[kb] = mfma32(key(buf, kb, t), qf[t], s[kb]);
-  };
-  auto values = [&](int buf) __attribute__((always_inline)) {
+    for (int d = 0; d < DB; ++d) o[b][d] = f32x16{};
+    p[b][0] = p[b][1] = u32x4{0, 0, 0, 0};
+  }
 #pragma unroll
-    for (int kg = 0; kg < 4; ++kg)
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] = mfma32(value(buf, kg, d), pf[kg], o[d]);
-  };
+  for (int n = 0; n < 2 * DB; ++n) vf[n] = u32x4{0, 0, 0, 0};
+
   // Values of step j that are not finite, where the mask cuts the step: set to
   // zero in LDS, by each wave in the part that it loaded, and noted ..
   auto clear_values = [&](int j, int buf) __attribute__((always_inline)) {
@@ -228,242 +221,227 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void k_attn(AttnArgs a) {
       if (bad != 0) *at = v;
       odd |= bad;
     }
-    if (odd != 0) s_odd[buf % 3] = j + 1;
+    if (odd != 0) s_odd[buf % R] = j + 1;
   };
   // .. and, as they are, added to the rows that see them
   auto add_nonfinite = [&](int j, int buf) {
-    if (PAGED || s_odd[buf % 3] != j + 1) return;
+    if (PAGED || s_odd[buf % R] != j + 1) return;
     const int j0 = base + j * kBN;
-    for (int jj = 0; jj < kBN && j0 + jj < seen; ++jj) {
-      const uint16_t* const v = a.v + static_cast<int64_t>(rt.s0 + j0 + jj) * a.v_ld + kvh * D;
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+    for (int b = 0; b < 2; ++b)
+      for (int jj = 0; jj < kBN && j0 + jj < seen[b]; ++jj) {
+        const uint16_t* const v = a.v + static_cast<int64_t>(rt.s0 + j0 + jj) * a.v_ld + kvh * D;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int c = 32 * d + acc_row(i, h);
-          const float y = c < D ? bf16_to_f32(v[c]) : 0.0f;
-          if ((__float_as_uint(y) & 0x7F800000u) == 0x7F800000u) o[d][i] += y;
-        }
-    }
-  };
-  auto softmax = [&](int j, int buf, uint32_t there) __attribute__((always_inline)) {
-    const int j0 = base + j * kBN;
-    const bool masked = j0 + kBN > w_all || there != 0xFu;
-    const float* const sks = s_scale + (PAGED ? buf % 3 * 2 * kBN : 0);
-    if constexpr (PAGED) {
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const f32x4 ks = *reinterpret_cast<const f32x4*>(sks + kb * 32 + acc_row(i, h));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[kb][i + e] *= ks[e];
-        }
-    }
-    if (masked) {
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = kb * 32 + acc_row(i, h);
-          if (j0 + r >= seen || (PAGED && (there >> (2 * kb + (i >> 3)) & 1) == 0)) s[kb][i] = kMinusInf;
-        }
-    }
-    float top = fmaxf(s[0][0], s[1][0]);
-#pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
-    top = max_halves(top) * a.c2;
-    if (__ballot(top > m + kRaise) != 0) {
-      const float m_new = top > m + kRaise ? top : m;
-      const float alpha = m_new == kMinusInf ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
-      m = m_new;
-      l *= alpha;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] *= alpha;
-    }
-    const float shift = m == kMinusInf ? 0.0f : m;
-    float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        f32x4 vs;
-        if constexpr (PAGED) vs = *reinterpret_cast<const f32x4*>(sks + kBN + kb * 32 + acc_row(i, h));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float t = s[kb][i + e];
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t, a.c2, -shift));
-          sum[e & 1] += p;
-          // (a masked value's scale may be anything)
-          s[kb][i + e] = !PAGED ? p : masked && t == kMinusInf ? 0.0f : p * vs[e];
-        }
+          for (int i = 0; i < 16; ++i) {
+            const int c = 32 * d + acc_row(i, h);
+            const float y = c < D ? bf16_to_f32(v[c]) : 0.0f;
+            if ((__float_as_uint(y) & 0x7F800000u) == 0x7F800000u) o[b][d][i] += y;
+          }
       }
-    }
-    l += sum[0] + sum[1];
-#pragma unroll
-    for (int kg = 0; kg < 4; ++kg) pf[kg] = pack_operand(s[kg >> 1], kg & 1);
   };
 
-  const bool second = W == 8 && wave >= 4;
-  int page_k = -1, page_v = -1;  // pages of steps j + 4 and j + 3
+  // Scores i .. i + 3 of a unit (step j, half, rows b) as they count, and their
+  // maximum
+  auto score4 = [&](auto cut, f32x16& x, int j0, int buf, int half, int b, uint32_t there, int i) __attribute__((always_inline)) {
+    if constexpr (PAGED) {
+      const f32x4 ks = *reinterpret_cast<const f32x4*>(s_scale + buf % R * 2 * kBN + half * 32 + acc_row(i, h));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i + e] *= ks[e];
+    }
+    if constexpr (decltype(cut)::value) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        bool on = j0 + half * 32 + acc_row(i + e, h) < seen[b];
+        if constexpr (PAGED) on = on && (there >> (2 * half + (i >> 3)) & 1) != 0;
+        x[i + e] = on ? x[i + e] : kMinusInf;
+      }
+    }
+    tops[i / 4] = fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3]));
+  };
+  // The maximum of rows b raised where a unit's scores ask for it
+  auto raise = [&](int b) __attribute__((always_inline)) {
+    const float top = max_halves(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]))) * a.c2;
+    if (__ballot(top > m[b] + kRaise) != 0) {
+      const float m_new = top > m[b] + kRaise ? top : m[b];
+      const float alpha = m_new == kMinusInf ? 1.0f : __builtin_amdgcn_exp2f(m[b] - m_new);
+      m[b] = m_new;
+      l[b] *= alpha;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[b][d] *= alpha;
+    }
+  };
+  f32x4 vs[2];  // scales of four values, and of the next four
+  auto vs_at = [&](int buf, int half, int q) __attribute__((always_inline)) {
+    return *reinterpret_cast<const f32x4*>(s_scale + buf % R * 2 * kBN + kBN + half * 32 + 8 * q + 4 * h);
+  };
+
+  int page_now = -1, page_k = -1;  // pages of steps j + 3 and j + 4
+  uint32_t queue = 0xFFFF;  // blocks of 16 keys that are there, four bits a step from step j on
+
+  // Unit u of step j: Y(u) between X(next) and Z(last)
+  auto unit = [&](auto cut, auto number, int j, int buf) __attribute__((always_inline)) {
+    constexpr int u = decltype(number)::value, b = u & 1, nb = b ^ 1, half = u >> 1, next_half = (u + 1 & 3) >> 1;
+    constexpr int NS = KS + 2 * DB;  // slots
+    constexpr bool reload = b == 0;
+    const int next_j = u == 3 ? j + 1 : j, next_buf = u == 3 ? buf + 1 : buf;
+    const float shift = m[b] == kMinusInf ? 0.0f : m[b];
+    if constexpr (PAGED) vs[0] = vs_at(buf, half, 0);
+    each<NS>([&](auto slot) __attribute__((always_inline)) {
+      constexpr int n = decltype(slot)::value;
+      if constexpr (n < KS) {
+        s[nb] = mfma32(kf[n], qf[nb][n], n == 0 ? f32x16{} : s[nb]);
+        if constexpr (reload) kf[n] = key(u == 0 ? buf : buf + 1, u == 0 ? 1 : 0, n);
+      } else {
+        constexpr int z = n - KS;
+        o[nb][z % DB] = mfma32(vf[z], p[nb][z / DB], o[nb][z % DB]);
+        if constexpr (reload) vf[z] = value(buf, u == 0 ? 0 : 1, z);
+      }
+#pragma unroll
+      for (int i = 16 * n / NS; i < 16 * (n + 1) / NS; ++i) {
+        if constexpr (PAGED) {
+          if (i % 4 == 0 && i < 12) vs[(i / 4 + 1) & 1] = vs_at(buf, half, i / 4 + 1);
+        }
+        const float t = s[b][i], w = __builtin_amdgcn_exp2f(__builtin_fmaf(t, a.c2, -shift));
+        l[b] += w;
+        // (a masked value's scale may be anything)
+        s[b][i] = !PAGED ? w : decltype(cut)::value && t == kMinusInf ? 0.0f : w * vs[i / 4 & 1][i & 3];
+        if (i % 2 == 1) p[b][i / 8][i % 8 / 2] = pack_bf16x2(s[b][i - 1], s[b][i]);
+      }
+      if constexpr (n >= NS - 4)
+        score4(cut, s[nb], base + next_j * kBN, next_buf, next_half, nb, u == 3 ? queue >> 4 : queue, 4 * (n - NS + 4));
+      if constexpr (PAGED && u >= 2) {  // the step after next's keys and values, in parts
+        constexpr int at = (u - 2) * NS + n, parts = 4 * kHold;
+#pragma unroll
+        for (int i = parts * at / (2 * NS); i < parts * (at + 1) / (2 * NS); ++i) put(buf + 2, i);
+      }
+      pin();
+    });
+    // (p and the sum belong to this side of the branch)
+    __asm__ volatile("" : "+v"(p[b][0]), "+v"(p[b][1]), "+v"(l[b])::"memory");
+    raise(nb);
+    pin();
+  };
+  const bool active = wave * 64 <= last_in;
+  auto step = [&](auto cut, int j, int buf) __attribute__((always_inline)) {
+    const bool on = active && (!decltype(cut)::value || base + j * kBN < w_end);
+    if (on) {
+      unit(cut, std::integral_constant<int, 0>{}, j, buf);
+      unit(cut, std::integral_constant<int, 1>{}, j, buf);
+    }
+    if constexpr (PAGED) {
+      barrier<63>();
+    } else {
+      if constexpr (decltype(cut)::value) {
+        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+        clear_values(j + 1, buf + 1);
+      }
+      barrier<2 * kLoads>();
+      load_packed(j + 3, buf + 3);
+    }
+    pin();
+    if (on) {
+      unit(cut, std::integral_constant<int, 2>{}, j, buf);
+      unit(cut, std::integral_constant<int, 3>{}, j, buf);
+      if constexpr (decltype(cut)::value && !PAGED) add_nonfinite(j, buf);
+    } else if constexpr (PAGED) {
+#pragma unroll
+      for (int n = 0; n < 4 * kHold; ++n) put(buf + 2, n);
+    }
+    if constexpr (PAGED) {
+      queue = queue >> 4 | blocks(page_k) << 12;
+      fetch(j + 3, page_now);
+      page_now = page_k;
+      page_k = pages_of(j + 5);
+    }
+  };
+
+  constexpr std::integral_constant<bool, true> cut{};
+  constexpr std::integral_constant<bool, false> uncut{};
   if (steps > 0) {
     if constexpr (PAGED) {
-      const int q0 = pages_of(0), q1 = pages_of(1), q2 = pages_of(2), q3 = pages_of(3);
-      fetch(0, q0, false);
-      fetch(0, q0, true);
-      put(0, false);
-      put(0, true);
-      fetch(1, q1, false);
-      fetch(1, q1, true);
-      put(1, false);
-      put(1, true);
-      fetch(2, q2, false);
-      put(2, false);
-      fetch(3, q3, false);
-      fetch(2, q2, true);
-      queue = blocks(q0) | blocks(q1) << 4 | blocks(q2) << 8 | blocks(q3) << 12;
-      page_v = q3;
+      const int q0 = pages_of(0), q1 = pages_of(1), q2 = pages_of(2);
+      page_now = pages_of(3);
       page_k = pages_of(4);
-      barrier<-1, 0>();
+      fetch(0, q0);
+#pragma unroll
+      for (int n = 0; n < 4 * kHold; ++n) put(0, n);
+      fetch(1, q1);
+#pragma unroll
+      for (int n = 0; n < 4 * kHold; ++n) put(1, n);
+      fetch(2, q2);
+      queue = blocks(q0) | blocks(q1) << 4 | blocks(q2) << 8 | blocks(page_now) << 12;
     } else {
-      load_packed(0, 0, false);
-      load_packed(0, 0, true);
-      load_packed(1, 1, false);
-      load_packed(1, 1, true);
-      load_packed(2, 2, false);
-      barrier<0, 0>();
-    }
-    // steps of which every row of the tile sees all keys, in whole turns of the
-    // buffers, and with the next step to come
-    const int sees_all = inside(first + tok0 + 1) - base;
-    const int whole = sees_all >= 2 * kBN ? (sees_all / kBN - 1) / 3 * 3 : 0;
-    if (!PAGED && whole == 0) {
+      load_packed(0, 0);
+      load_packed(1, 1);
+      load_packed(2, 2);
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * kLoads) : "memory");
       clear_values(0, 0);
-      barrier<-1, 0>();
     }
-    if (base < w_end) {
-      scores(0);
-      softmax(0, 0, queue & 0xFu);
+    barrier<63>();
+    if (active) {
+      // the first unit's scores; O takes nothing from the one before
+#pragma unroll
+      for (int n = 0; n < KS; ++n) kf[n] = key(0, 0, n);
+#pragma unroll
+      for (int n = 0; n < KS; ++n) s[0] = mfma32(kf[n], qf[0][n], n == 0 ? f32x16{} : s[0]);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) score4(cut, s[0], base, 0, 0, 0, queue, i);
+      raise(0);
     }
-    if (second) barrier<-1, -1>();
-    // the end of step j's matrix phase, and the softmax phase
-    auto rest = [&](int j, int buf, bool cut) __attribute__((always_inline)) {
-      if constexpr (W == 8) __builtin_amdgcn_s_setprio(0);
-      __builtin_amdgcn_sched_barrier(0);
-      if (!PAGED && cut) {
-        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        clear_values(j + 1, buf + 1);
-        barrier<-1, 0>();
-      } else {
-        barrier<PAGED ? -1 : 0, -1>();
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (PAGED) {
-        put(buf, false);
-        put(buf + 2, true);
-        queue = queue >> 4 | blocks(page_k) << 12;
-        fetch(j + 4, page_k, false);
-        fetch(j + 3, page_v, true);
-        page_v = page_k;
-        page_k = pages_of(j + 5);
-      } else {
-        load_packed(j + 3, buf, false);
-        load_packed(j + 2, buf + 2, true);
-      }
-      if (base + (j + 1) * kBN < w_end) softmax(j + 1, buf + 1, queue & 0xFu);
-      __builtin_amdgcn_sched_barrier(0);
-      barrier<-1, PAGED ? 0 : -1>();
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    auto whole_step = [&](int j, int buf, bool last) __attribute__((always_inline)) {
-      if constexpr (W == 8) __builtin_amdgcn_s_setprio(1);
-      if (w_end > base) {
-        scores(buf + 1);
-        values(buf);
-        // reads some instructions ahead of their use
-        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
-#pragma unroll
-        for (int i = 0; i < 2 * KS - 6; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 6; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4 * DB; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        }
-      }
-      rest(j, buf, last);
-    };
-    auto cut_step = [&](int j, int buf) __attribute__((always_inline)) {
-      if constexpr (W == 8) __builtin_amdgcn_s_setprio(1);
-      if (base + (j + 1) * kBN < w_end) scores(buf + 1);
-      if (base + j * kBN < w_end) {
-        values(buf);
-        add_nonfinite(j, buf);
-      }
-      rest(j, buf, true);
-    };
+    pin();
     int j = 0;
-    for (; j < whole; j += 3) {
-      whole_step(j, 0, false);
-      whole_step(j + 1, 1, false);
-      whole_step(j + 2, 2, j + 3 == whole);
-    }
-    for (; j < steps; j += 3) {  // (steps past the last compute nothing)
-      cut_step(j, 0);
-      cut_step(j + 1, 1);
-      cut_step(j + 2, 2);
-    }
-    if (!second && W == 8) barrier<-1, -1>();
+    for (; j < whole && (!PAGED || (queue & 0xFFFFu) == 0xFFFFu); j += R)
+      each<R>([&](auto i) __attribute__((always_inline)) { step(uncut, j + i, i); });
+    for (; j < steps; j += R)
+      each<R>([&](auto i) __attribute__((always_inline)) {
+        if (j + i < steps) step(cut, j + i, i);
+      });
+    // the last unit's share of O
+#pragma unroll
+    for (int z = 0; z < 2 * DB; ++z) o[1][z % DB] = mfma32(vf[z], p[1][z / DB], o[1][z % DB]);
     // (loads on their way into LDS end before the workgroup does)
     __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
-  l += swap_halves(l);
-  if (!in) return;
-  const int64_t row = static_cast<int64_t>(rt.s0 + tok) * a.Hq + hq;
-  if (PAGED && a.splits > 1) {
-    const int64_t part = static_cast<int64_t>(share) * a.s.T * a.Hq + row;
+
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+  for (int b = 0; b < 2; ++b) {
+    const float sum = l[b] + swap_halves(l[b]);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // (no key: 0; NaN stays)
+    const bool in = lane_row(b) <= last_in;
+    const int r = in ? lane_row(b) : 0, t = token(r);
+    const int64_t row = static_cast<int64_t>(rt.s0 + t) * a.Hq + kvh * a.g + rem0 + r - (t - tok0) * a.g;
+    if (PAGED && a.splits > 1) {
+      const int64_t part = static_cast<int64_t>(share) * a.s.T * a.Hq + row;
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int c = 32 * d + acc_row(i, h);
-        if (c < D) *reinterpret_cast<f32x4*>(a.part + part * D + c) = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
-      }
-    if (h == 0) *reinterpret_cast<f32x2*>(a.ml + 2 * part) = f32x2{m, l};
-    return;
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (no key: 0; NaN stays)
+      for (int d = 0; d < DB; ++d)
 #pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int c = 32 * d + acc_row(i, h);
-      if (c < D)
-        *reinterpret_cast<u32x2*>(a.o + row * D + c) =
-            u32x2{pack_bf16x2(o[d][i] * inv, o[d][i + 1] * inv), pack_bf16x2(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+        for (int i = 0; i < 16; i += 4) {
+          const int c = 32 * d + acc_row(i, h);
+          if (in && c < D)
+            *reinterpret_cast<f32x4*>(a.part + part * D + c) = f32x4{o[b][d][i], o[b][d][i + 1], o[b][d][i + 2], o[b][d][i + 3]};
+        }
+      if (in && h == 0) *reinterpret_cast<f32x2*>(a.ml + 2 * part) = f32x2{m[b], sum};
+      continue;
     }
-  if (a.lse != nullptr && h == 0) a.lse[row] = l == 0.0f ? kMinusInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    store_row<DB>(o[b], inv, a.o + row * D, D, in, h);
+    if (in && a.lse != nullptr && h == 0) a.lse[row] = sum == 0.0f ? kMinusInf : (m[b] + __builtin_amdgcn_logf(sum)) * kLn2;
+  }
 }
 
-template <int DP, bool PAGED, int W>
+template <int DP, bool PAGED>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-  const int64_t tiles = static_cast<int64_t>(a.s.T) * a.g / (32 * W) + a.s.B;
-  hipLaunchKernelGGL((k_attn<DP, PAGED, W>), dim3(static_cast<uint32_t>(tiles * (PAGED ? a.splits : 1) * a.Hkv)), dim3(64 * W), 0, stream, a);
+  const int64_t tiles = static_cast<int64_t>(a.s.T) * a.g / kBM + a.s.B;
+  hipLaunchKernelGGL((k_attn<DP, PAGED>), dim3(static_cast<uint32_t>(tiles * (PAGED ? a.splits : 1) * a.Hkv)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_attn(const AttnArgs& a, bool paged, hipStream_t stream) {
-  if (a.D <= 64) return paged ? launch<64, true, 8>(a, stream) : launch<64, false, 8>(a, stream);
-  return paged ? launch<128, true, 8>(a, stream) : launch<128, false, 8>(a, stream);
+  if (a.D <= 64) return paged ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
+  return paged ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
 }
 
 }  // namespace qlin
