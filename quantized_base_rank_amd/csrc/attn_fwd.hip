@@ -45,6 +45,14 @@ constexpr int kBM = 256;        // query rows of a workgroup
 constexpr int kBN = 64;         // keys of a step
 constexpr float kRaise = 8.0f;  // log2 of what p may reach
 
+// Loads at a lane's offset from a base that is the same for the wave.
+__device__ __forceinline__ u32x4 load_b128(const void* base, uint32_t bytes, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b128(uniform_rsrc(base, bytes), at, 0, 0);
+}
+__device__ __forceinline__ uint32_t load_b32(const void* base, uint32_t bytes, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b32(uniform_rsrc(base, bytes), at, 0, 0);
+}
+
 // Waits until at most VM of this wave's loads and none of its LDS accesses are
 // on their way, then meets the other waves.
 template <int VM>
@@ -127,16 +135,28 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
     vo_k[i] = (static_cast<uint32_t>(r) * static_cast<uint32_t>(a.k_ld * 2) + c * 16) | out;
     vo_v[i] = (static_cast<uint32_t>(r) * static_cast<uint32_t>(a.v_ld * 2) + c * 16) | out;
   }
-  auto load_packed = [&](int j, int buf) __attribute__((always_inline)) {
-    const int left = len - j * kBN, n = left < kBN ? left : kBN;
-    const uint32_t bk = left > 0 ? static_cast<uint32_t>((n - 1) * a.k_ld + D) * 2u : 0u;
-    const uint32_t bv = left > 0 ? static_cast<uint32_t>((n - 1) * a.v_ld + D) * 2u : 0u;
-    const uint16_t* const k = a.k + (static_cast<int64_t>(rt.s0) + j * kBN) * a.k_ld + kvh * D;
-    const uint16_t* const v = a.v + (static_cast<int64_t>(rt.s0) + j * kBN) * a.v_ld + kvh * D;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_to_lds(k, bk, sk(buf) + (wave * kLoads + i) * 1024, vo_k[i]);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_to_lds(v, bv, sv(buf) + (wave * kLoads + i) * 1024, vo_v[i]);
+  // the next step's: where its keys and values start, and its tokens
+  const uint16_t* k_next = a.k + static_cast<int64_t>(rt.s0) * a.k_ld + kvh * D;
+  const uint16_t* v_next = a.v + static_cast<int64_t>(rt.s0) * a.v_ld + kvh * D;
+  int left = len;
+  uint32_t k_bytes = 0, v_bytes = 0;
+  // load n of 2 kLoads, keys first
+  auto load_part = [&](int buf, int n) __attribute__((always_inline)) {
+    if (n == 0) {
+      const int rows = left < kBN ? left : kBN;
+      k_bytes = left > 0 ? static_cast<uint32_t>((rows - 1) * static_cast<int>(a.k_ld) + D) * 2u : 0u;
+      v_bytes = left > 0 ? static_cast<uint32_t>((rows - 1) * static_cast<int>(a.v_ld) + D) * 2u : 0u;
+    }
+    const int i = n % kLoads;
+    if (n < kLoads)
+      load_to_lds(k_next, k_bytes, sk(buf) + (wave * kLoads + i) * 1024, vo_k[i]);
+    else
+      load_to_lds(v_next, v_bytes, sv(buf) + (wave * kLoads + i) * 1024, vo_v[i]);
+    if (n == 2 * kLoads - 1) {
+      k_next += kBN * a.k_ld;
+      v_next += kBN * a.v_ld;
+      left -= kBN;
+    }
   };
 
   // ---- keys and values from the cache: 16 codes a thread and time, held in
@@ -156,18 +176,24 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   auto blocks = [&](int p) { return static_cast<uint32_t>(__ballot(p >= 0)) & 0xFu; };
   u32x4 held_k[kHold], held_v[kHold];
   float held_ks[kHold], held_vs[kHold];
-  auto fetch = [&](int j, int p) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      const int r = row_t + i * (256 / kChunks);
-      const int pg = __builtin_amdgcn_readlane(p, __builtin_amdgcn_readfirstlane(r >> 4) & 3);
-      // (a page that is not there is read as page 0, whose rows exist, and masked)
-      const int64_t row = ((static_cast<int64_t>(pg < 0 ? 0 : pg) * a.c.H + kvh) << a.c.page_shift) + ((base + j * kBN + r) & page_mask);
-      const int64_t at = row * D + (16 * chunk < D ? 16 * chunk : 0);  // (past D: the query's elements are zero there)
-      held_k[i] = *reinterpret_cast<const u32x4*>(a.c.k + at);
-      held_v[i] = *reinterpret_cast<const u32x4*>(a.c.v + at);
-      held_ks[i] = a.c.ks[row];
-      held_vs[i] = a.c.vs[row];
+  // part n of 2 kHold of step j, keys first; p its pages
+  const uint32_t at_codes = static_cast<uint32_t>((row_t & 15) * D + (16 * chunk < D ? 16 * chunk : 0));
+  const uint32_t at_scale = static_cast<uint32_t>((row_t & 15) * 4);
+  auto fetch = [&](int j, int p, int n) __attribute__((always_inline)) {
+    const int i = n % kHold;
+    const int block = __builtin_amdgcn_readfirstlane(row_t >> 4) + i * (256 / kChunks / 16);
+    const int pg = __builtin_amdgcn_readlane(p, block & 3);
+    // (a page that is not there is read as page 0, whose rows exist, and masked;
+    // threads past D read the row's start: the query's elements are zero there)
+    const int64_t row = ((static_cast<int64_t>(pg < 0 ? 0 : pg) * a.c.H + kvh) << a.c.page_shift) +
+                        ((base + j * kBN + 16 * block) & page_mask);
+    const uint32_t codes = static_cast<uint32_t>(16 * D);
+    if (n < kHold) {
+      held_k[i] = load_b128(a.c.k + row * D, codes, at_codes);
+      held_ks[i] = __uint_as_float(load_b32(a.c.ks + row, 64, at_scale));
+    } else {
+      held_v[i] = load_b128(a.c.v + row * D, codes, at_codes);
+      held_vs[i] = __uint_as_float(load_b32(a.c.vs + row, 64, at_scale));
     }
   };
   // part n of 4 kHold: eight codes of a thread's sixteen, keys first
@@ -199,7 +225,7 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   u32x4 kf[KS], vf[2 * DB];  // of the unit at hand
   f32x16 o[2][DB], s[2];
   u32x4 p[2][2];
-  float m[2] = {kMinusInf, kMinusInf}, l[2] = {0.0f, 0.0f}, tops[4];
+  float m[2] = {kMinusInf, kMinusInf}, l[2] = {0.0f, 0.0f}, top = kMinusInf;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
 #pragma unroll
@@ -258,11 +284,13 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
         x[i + e] = on ? x[i + e] : kMinusInf;
       }
     }
-    tops[i / 4] = fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3]));
+    top = fmaxf(fmaxf(i == 0 ? kMinusInf : top, x[i]), x[i + 1]);
+    top = fmaxf(fmaxf(top, x[i + 2]), x[i + 3]);
   };
-  // The maximum of rows b raised where a unit's scores ask for it
+  // The maximum of rows b raised where a unit's scores (top: their maximum, in
+  // powers of two) ask for it
+  auto whole_top = [&] { top = max_halves(top) * a.c2; };
   auto raise = [&](int b) __attribute__((always_inline)) {
-    const float top = max_halves(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]))) * a.c2;
     if (__ballot(top > m[b] + kRaise) != 0) {
       const float m_new = top > m[b] + kRaise ? top : m[b];
       const float alpha = m_new == kMinusInf ? 1.0f : __builtin_amdgcn_exp2f(m[b] - m_new);
@@ -288,6 +316,13 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
     const int next_j = u == 3 ? j + 1 : j, next_buf = u == 3 ? buf + 1 : buf;
     const float shift = m[b] == kMinusInf ? 0.0f : m[b];
     if constexpr (PAGED) vs[0] = vs_at(buf, half, 0);
+    bool gone[2] = {false, false};
+    auto settle = [&](int i) __attribute__((always_inline)) {
+      l[b] += s[b][i];
+      // (a masked value's scale may be anything)
+      if constexpr (PAGED) s[b][i] = decltype(cut)::value && gone[i & 1] ? 0.0f : s[b][i] * vs[i / 4 & 1][i & 3];
+      if (i % 2 == 1) p[b][i / 8][i % 8 / 2] = pack_bf16x2(s[b][i - 1], s[b][i]);
+    };
     each<NS>([&](auto slot) __attribute__((always_inline)) {
       constexpr int n = decltype(slot)::value;
       if constexpr (n < KS) {
@@ -300,21 +335,32 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
       }
 #pragma unroll
       for (int i = 16 * n / NS; i < 16 * (n + 1) / NS; ++i) {
+        // value i's power; value i - 1 on its way to the operand
         if constexpr (PAGED) {
-          if (i % 4 == 0 && i < 12) vs[(i / 4 + 1) & 1] = vs_at(buf, half, i / 4 + 1);
+          if (i % 4 == 1 && i < 12) vs[(i / 4 + 1) & 1] = vs_at(buf, half, i / 4 + 1);
         }
-        const float t = s[b][i], w = __builtin_amdgcn_exp2f(__builtin_fmaf(t, a.c2, -shift));
-        l[b] += w;
-        // (a masked value's scale may be anything)
-        s[b][i] = !PAGED ? w : decltype(cut)::value && t == kMinusInf ? 0.0f : w * vs[i / 4 & 1][i & 3];
-        if (i % 2 == 1) p[b][i / 8][i % 8 / 2] = pack_bf16x2(s[b][i - 1], s[b][i]);
+        const float t = s[b][i];
+        s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(t, a.c2, -shift));
+        if constexpr (PAGED && decltype(cut)::value) gone[i & 1] = t == kMinusInf;
+        if (i > 0) settle(i - 1);
       }
-      if constexpr (n >= NS - 4)
-        score4(cut, s[nb], base + next_j * kBN, next_buf, next_half, nb, u == 3 ? queue >> 4 : queue, 4 * (n - NS + 4));
-      if constexpr (PAGED && u >= 2) {  // the step after next's keys and values, in parts
-        constexpr int at = (u - 2) * NS + n, parts = 4 * kHold;
+      constexpr int kFirst = NS - 6 > KS + 1 ? NS - 6 : NS - 4;  // (the scores are there by then)
+      if constexpr (n >= kFirst && n < kFirst + 4)
+        score4(cut, s[nb], base + next_j * kBN, next_buf, next_half, nb, u == 3 ? queue >> 4 : queue, 4 * (n - kFirst));
+      if constexpr (n == NS - 1) {
+        settle(15);
+        whole_top();
+      }
+      if constexpr (u >= 2) {
+        constexpr int at = (u - 2) * NS + n;
+        if constexpr (PAGED) {  // the step after next's keys and values become bf16, the one after it is asked for
 #pragma unroll
-        for (int i = parts * at / (2 * NS); i < parts * (at + 1) / (2 * NS); ++i) put(buf + 2, i);
+          for (int i = 4 * kHold * at / (2 * NS); i < 4 * kHold * (at + 1) / (2 * NS); ++i) {
+            put(buf + 2, i);
+          }
+        } else if constexpr (at < 2 * kLoads) {
+          load_part(buf + 3, at);
+        }
       }
       pin();
     });
@@ -338,7 +384,6 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
         clear_values(j + 1, buf + 1);
       }
       barrier<2 * kLoads>();
-      load_packed(j + 3, buf + 3);
     }
     pin();
     if (on) {
@@ -348,10 +393,18 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
     } else if constexpr (PAGED) {
 #pragma unroll
       for (int n = 0; n < 4 * kHold; ++n) put(buf + 2, n);
+#pragma unroll
+      for (int n = 0; n < 2 * kHold; ++n) fetch(j + 3, page_now, n);
+    } else {
+#pragma unroll
+      for (int n = 0; n < 2 * kLoads; ++n) load_part(buf + 3, n);
     }
     if constexpr (PAGED) {
+      if (on) {
+#pragma unroll
+      for (int n = 0; n < 2 * kHold; ++n) fetch(j + 3, page_now, n);
+}
       queue = queue >> 4 | blocks(page_k) << 12;
-      fetch(j + 3, page_now);
       page_now = page_k;
       page_k = pages_of(j + 5);
     }
@@ -364,18 +417,21 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
       const int q0 = pages_of(0), q1 = pages_of(1), q2 = pages_of(2);
       page_now = pages_of(3);
       page_k = pages_of(4);
-      fetch(0, q0);
+      auto now = [&](int j, int pages, bool store) __attribute__((always_inline)) {
 #pragma unroll
-      for (int n = 0; n < 4 * kHold; ++n) put(0, n);
-      fetch(1, q1);
+        for (int n = 0; n < 2 * kHold; ++n) fetch(j, pages, n);
 #pragma unroll
-      for (int n = 0; n < 4 * kHold; ++n) put(1, n);
-      fetch(2, q2);
+        for (int n = 0; store && n < 4 * kHold; ++n) put(j, n);
+      };
+      now(0, q0, true);
+      now(1, q1, true);
+      now(2, q2, false);
       queue = blocks(q0) | blocks(q1) << 4 | blocks(q2) << 8 | blocks(page_now) << 12;
     } else {
-      load_packed(0, 0);
-      load_packed(1, 1);
-      load_packed(2, 2);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int n = 0; n < 2 * kLoads; ++n) load_part(i, n);
       __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * kLoads) : "memory");
       clear_values(0, 0);
     }
@@ -388,6 +444,7 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
       for (int n = 0; n < KS; ++n) s[0] = mfma32(kf[n], qf[0][n], n == 0 ? f32x16{} : s[0]);
 #pragma unroll
       for (int i = 0; i < 16; i += 4) score4(cut, s[0], base, 0, 0, 0, queue, i);
+      whole_top();
       raise(0);
     }
     pin();
