@@ -591,42 +591,48 @@ def qlin_bwd_q8(w: QWeight, x: Q8Rows, A, B, r: int, s: float, dy, u, pool: int 
 
 # --------------------------------------------------------------- attention
 
-def _rows_ld(t, heads, dim, name) -> int:
-    """Distance of the rows of a bf16 tensor [tokens][heads][dim] whose rows are
-    contiguous (a part of a wider matrix is fine)."""
+def _rows_ld(t, index, heads, dim, name) -> int:
+    """Distance of the rows of a bf16 tensor [tokens][heads][dim] on CUDA device
+    ``index`` whose rows are contiguous (a part of a wider matrix is fine)."""
     torch = _torch()
-    if t.dim() != 3 or t.dtype is not torch.bfloat16 or not t.is_cuda:
-        raise ValueError(f"{name}: expected a bfloat16 CUDA tensor [tokens][heads][dim], got {t.dtype} "
-                         f"{tuple(t.shape)} cuda={t.is_cuda}")
-    n, h, d = t.shape
+    shape = t.shape
+    if len(shape) != 3 or t.dtype is not torch.bfloat16 or t.get_device() != index or index < 0:
+        raise ValueError(f"{name}: expected a bfloat16 tensor [tokens][heads][dim] on CUDA device {index}, got {t.dtype} "
+                         f"{tuple(shape)} on {t.device}")
+    n, h, d = shape
     if (heads is not None and h != heads) or (dim is not None and d != dim):
-        raise ValueError(f"{name}: expected {heads} heads of {dim}, got {tuple(t.shape)}")
+        raise ValueError(f"{name}: expected {heads} heads of {dim}, got {tuple(shape)}")
     s0, s1, s2 = t.stride()
-    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name}: heads and elements of a row have to be contiguous, got strides {t.stride()}")
     return s0 if n > 1 else -(-h * d // 8) * 8
 
 
-def _i32(t, shape, device, name):
-    torch = _torch()
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: expected contiguous int32 tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
+def _dense(t, dtype, shape, index, name):
+    # (one test where all is well)
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return
+    raise ValueError(f"{name}: expected contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {index}, got "
+                     f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
 
 
-def _same_device(device, *named):
-    for t, name in named:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: on {t.device}, expected {device}")
+class _On:
+    """`index` as the current device during a call (its stream takes the
+    launches) if it is not already."""
+    __slots__ = ("index", "was")
 
+    def __init__(self, index):
+        self.index = index
 
-def _on(device, f):
-    """f() with `device` as the current one (its stream takes the launches)."""
-    torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        return f()
-    with torch.cuda.device(device):
-        return f()
+    def __enter__(self):
+        torch = _torch()
+        self.was = torch._C._cuda_getDevice()
+        if self.was != self.index:
+            torch._C._cuda_setDevice(self.index)
+
+    def __exit__(self, *_):
+        if self.was != self.index:
+            _torch()._C._cuda_setDevice(self.was)
 
 
 def qlin_attn_fwd(q, k, v, cu, scale: Optional[float] = None, out=None, lse=None):
@@ -638,28 +644,29 @@ def qlin_attn_fwd(q, k, v, cu, scale: Optional[float] = None, out=None, lse=None
     [tokens][heads_q], for qlin_attn_bwd.  Rows that belong to no sequence are
     not written."""
     torch = _torch()
-    q_ld = _rows_ld(q, None, None, "q")
+    at = q.get_device()
+    q_ld = _rows_ld(q, at, None, None, "q")
     T, Hq, D = q.shape
-    k_ld = _rows_ld(k, None, D, "k")
+    k_ld = _rows_ld(k, at, None, D, "k")
     Hkv = k.shape[1]
-    v_ld = _rows_ld(v, Hkv, D, "v")
+    v_ld = _rows_ld(v, at, Hkv, D, "v")
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError(f"q, k, v: {T}, {k.shape[0]} and {v.shape[0]} tokens")
+    n = cu.numel()
+    _dense(cu, torch.int32, (n,), at, "cu")
     dev = q.device
-    _i32(cu, (cu.numel(),), dev, "cu")
-    _same_device(dev, (k, "k"), (v, "v"), (out, "out"), (lse, "lse"))
     if out is None:
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
     else:
-        _need(out, torch.bfloat16, (T, Hq, D), "out")
+        _dense(out, torch.bfloat16, (T, Hq, D), at, "out")
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     else:
-        _need(lse, torch.float32, (T, Hq), "lse")
-    scale = D ** -0.5 if scale is None else float(scale)
-    check(_on(dev, lambda: lib().qlin_attn_fwd(q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
-                                               cu.data_ptr(), cu.numel() - 1, T, Hq, Hkv, D, scale, out.data_ptr(),
-                                               lse.data_ptr(), _stream(dev))), "qlin_attn_fwd")
+        _dense(lse, torch.float32, (T, Hq), at, "lse")
+    with _On(at):
+        check(lib().qlin_attn_fwd(q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, cu.data_ptr(), n - 1, T, Hq,
+                                  Hkv, D, D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
+                                  _stream(dev)), "qlin_attn_fwd")
     return out, lse
 
 
@@ -668,37 +675,44 @@ def qlin_attn_bwd(q, k, v, out, lse, dout, cu, scale: Optional[float] = None, dq
     forward's.  dq, dk, dv may be given, as parts of one matrix too; rows that
     belong to no sequence are not written."""
     torch = _torch()
-    q_ld = _rows_ld(q, None, None, "q")
+    at = q.get_device()
+    q_ld = _rows_ld(q, at, None, None, "q")
     T, Hq, D = q.shape
-    k_ld = _rows_ld(k, None, D, "k")
+    k_ld = _rows_ld(k, at, None, D, "k")
     Hkv = k.shape[1]
-    v_ld = _rows_ld(v, Hkv, D, "v")
+    v_ld = _rows_ld(v, at, Hkv, D, "v")
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError(f"q, k, v: {T}, {k.shape[0]} and {v.shape[0]} tokens")
+    n = cu.numel()
+    _dense(cu, torch.int32, (n,), at, "cu")
+    _dense(out, torch.bfloat16, (T, Hq, D), at, "out")
+    _dense(lse, torch.float32, (T, Hq), at, "lse")
+    _dense(dout, torch.bfloat16, (T, Hq, D), at, "dout")
     dev = q.device
-    _i32(cu, (cu.numel(),), dev, "cu")
-    _need(out, torch.bfloat16, (T, Hq, D), "out")
-    _need(lse, torch.float32, (T, Hq), "lse")
-    _need(dout, torch.bfloat16, (T, Hq, D), "dout")
-    bf = {"dtype": torch.bfloat16, "device": dev}
-    dq = torch.empty((T, Hq, D), **bf) if dq is None else dq
-    dk = torch.empty((T, Hkv, D), **bf) if dk is None else dk
-    dv = torch.empty((T, Hkv, D), **bf) if dv is None else dv
-    ld = [_rows_ld(t, h, D, n) for t, h, n in ((dq, Hq, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv"))]
-    if dq.shape[0] != T or dk.shape[0] != T or dv.shape[0] != T:
-        raise ValueError(f"dq, dk, dv: expected {T} tokens")
-    _same_device(dev, (k, "k"), (v, "v"), (out, "out"), (lse, "lse"), (dout, "dout"), (dq, "dq"), (dk, "dk"),
-                 (dv, "dv"), (ws, "ws"))
-    scale = D ** -0.5 if scale is None else float(scale)
-    st, L, B = _stream(dev), lib(), cu.numel() - 1
+    grads, ld = [], []
+    for g, H, name in ((dq, Hq, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv")):
+        if g is None:
+            g = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        elif g.shape[0] != T:
+            raise ValueError(f"{name}: expected {T} tokens, got {tuple(g.shape)}")
+        grads.append(g)
+        ld.append(_rows_ld(g, at, H, D, name))
+    if ws is not None and ws.get_device() != at:
+        raise ValueError(f"ws: on {ws.device}, expected CUDA device {at}")
+    dq, dk, dv = grads
+    scale = D ** -0.5 if scale is None else scale
+    L = lib()
+    with _On(at):
+        st = _stream(dev)
 
-    def call(ws):
-        return L.qlin_attn_bwd(q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, out.data_ptr(), lse.data_ptr(),
-                               dout.data_ptr(), cu.data_ptr(), B, T, Hq, Hkv, D, scale, dq.data_ptr(), ld[0],
-                               dk.data_ptr(), ld[1], dv.data_ptr(), ld[2], ws.data_ptr(), ws.numel(), st)
+        def call(ws):
+            return L.qlin_attn_bwd(q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, out.data_ptr(),
+                                   lse.data_ptr(), dout.data_ptr(), cu.data_ptr(), n - 1, T, Hq, Hkv, D, scale,
+                                   dq.data_ptr(), ld[0], dk.data_ptr(), ld[1], dv.data_ptr(), ld[2], ws.data_ptr(),
+                                   ws.numel(), st)
 
-    check(_on(dev, lambda: _call_with_workspace(call, lambda: L.qlin_attn_bwd_workspace_bytes(B, T, Hq, Hkv, D), dev, st,
-                                                ws)), "qlin_attn_bwd")
+        check(_call_with_workspace(call, lambda: L.qlin_attn_bwd_workspace_bytes(n - 1, T, Hq, Hkv, D), dev, st, ws),
+              "qlin_attn_bwd")
     return dq, dk, dv
 
 
@@ -738,57 +752,59 @@ class KVBatch:
 
 
 def _kv_structs(cache: KVCache, batch: KVBatch, tokens: int):
+    """The C structs of a cache and a batch, checked, and their device's index."""
     torch = _torch()
     k, v, ks, vs = cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale
-    if k.dim() != 4:
-        raise ValueError(f"cache: expected codes [pages][heads][page][dim], got {tuple(k.shape)}")
-    shape, dev = k.shape, k.device
-    for t, dt, sh, name in ((k, torch.int8, shape, "k_codes"), (v, torch.int8, shape, "v_codes"),
-                            (ks, torch.float32, shape[:3], "k_scale"), (vs, torch.float32, shape[:3], "v_scale")):
-        _need(t, dt, sh, "cache." + name)
-        if t.device != dev:
-            raise ValueError(f"cache.{name}: on {t.device}, expected {dev}")
+    shape, at = k.shape, k.get_device()
+    if len(shape) != 4 or at < 0:
+        raise ValueError(f"cache: expected codes [pages][heads][page][dim] on a CUDA device, got {tuple(shape)} on {k.device}")
+    pages, heads, page, dim = shape
+    rows = (pages, heads, page)
+    _dense(k, torch.int8, shape, at, "cache.k_codes")
+    _dense(v, torch.int8, shape, at, "cache.v_codes")
+    _dense(ks, torch.float32, rows, at, "cache.k_scale")
+    _dense(vs, torch.float32, rows, at, "cache.v_scale")
     cu, lens, table = batch.cu, batch.lens, batch.table
-    B = cu.numel() - 1
+    n = cu.numel() - 1
     if table.dim() != 2:
         raise ValueError(f"batch.table: expected [sequences][pages], got {tuple(table.shape)}")
-    _i32(cu, (B + 1,), dev, "batch.cu")
-    _i32(lens, (B,), dev, "batch.lens")
-    _i32(table, (B, table.shape[1]), dev, "batch.table")
-    return (KVCacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2], shape[3]),
-            KVBatchStruct(cu.data_ptr(), lens.data_ptr(), table.data_ptr(), B, table.shape[1], tokens), dev)
+    held = table.shape[1]
+    _dense(cu, torch.int32, (n + 1,), at, "batch.cu")
+    _dense(lens, torch.int32, (n,), at, "batch.lens")
+    _dense(table, torch.int32, (n, held), at, "batch.table")
+    return (KVCacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, heads, page, dim),
+            KVBatchStruct(cu.data_ptr(), lens.data_ptr(), table.data_ptr(), n, held, tokens), at)
 
 
 def qlin_kv_write_q8(cache: KVCache, batch: KVBatch, k, v) -> None:
     """New tokens' keys and values (bf16 [tokens][heads][dim]) into the cache, in
     8-bit rows."""
-    _, heads, _, dim = cache.k_codes.shape
-    k_ld, v_ld = _rows_ld(k, heads, dim, "k"), _rows_ld(v, heads, dim, "v")
-    if k.shape[0] != v.shape[0]:
+    c, s, at = _kv_structs(cache, batch, k.shape[0])
+    k_ld, v_ld = _rows_ld(k, at, c.heads, c.dim, "k"), _rows_ld(v, at, c.heads, c.dim, "v")
+    if v.shape[0] != k.shape[0]:
         raise ValueError(f"k, v: {k.shape[0]} and {v.shape[0]} tokens")
-    c, s, dev = _kv_structs(cache, batch, k.shape[0])
-    _same_device(dev, (k, "k"), (v, "v"))
-    check(_on(dev, lambda: lib().qlin_kv_write_q8(ctypes.byref(c), ctypes.byref(s), k.data_ptr(), k_ld, v.data_ptr(), v_ld,
-                                                  _stream(dev))), "qlin_kv_write_q8")
+    with _On(at):
+        check(lib().qlin_kv_write_q8(ctypes.byref(c), ctypes.byref(s), k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+                                     _stream(k.device)), "qlin_kv_write_q8")
 
 
 def qlin_kv_read_q8(cache: KVCache, batch: KVBatch, tokens: int, k=None, v=None):
     """The last cu[b + 1] - cu[b] tokens of each sequence read back: (k, v), bf16
     [tokens][heads][dim].  Rows that belong to no sequence are not written."""
     torch = _torch()
-    c, s, dev = _kv_structs(cache, batch, tokens)
-    shape = (tokens, c.heads, c.dim)
+    c, s, at = _kv_structs(cache, batch, tokens)
+    shape, dev = (tokens, c.heads, c.dim), cache.k_codes.device
     if k is None:
         k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
-        _need(k, torch.bfloat16, shape, "k")
+        _dense(k, torch.bfloat16, shape, at, "k")
     if v is None:
         v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
-        _need(v, torch.bfloat16, shape, "v")
-    _same_device(dev, (k, "k"), (v, "v"))
-    check(_on(dev, lambda: lib().qlin_kv_read_q8(ctypes.byref(c), ctypes.byref(s), k.data_ptr(), v.data_ptr(),
-                                                 _stream(dev))), "qlin_kv_read_q8")
+        _dense(v, torch.bfloat16, shape, at, "v")
+    with _On(at):
+        check(lib().qlin_kv_read_q8(ctypes.byref(c), ctypes.byref(s), k.data_ptr(), v.data_ptr(), _stream(dev)),
+              "qlin_kv_read_q8")
     return k, v
 
 
@@ -801,25 +817,30 @@ def qlin_attn_q8(q, cache: KVCache, batch: KVBatch, scale: Optional[float] = Non
     bf16 [tokens][heads_q][dim]; rows that belong to no sequence are not
     written."""
     torch = _torch()
-    dim = cache.k_codes.shape[-1]
-    q_ld = _rows_ld(q, None, dim, "q")
-    T, Hq, _ = q.shape
-    c, s, dev = _kv_structs(cache, batch, T)
+    T = q.shape[0]
+    c, s, at = _kv_structs(cache, batch, T)
+    dim = c.dim
+    q_ld = _rows_ld(q, at, None, dim, "q")
+    Hq, dev = q.shape[1], q.device
     if out is None:
         out = torch.empty((T, Hq, dim), dtype=torch.bfloat16, device=dev)
     else:
-        _need(out, torch.bfloat16, (T, Hq, dim), "out")
-    _same_device(dev, (q, "q"), (out, "out"), (ws, "ws"))
-    scale = dim ** -0.5 if scale is None else float(scale)
+        _dense(out, torch.bfloat16, (T, Hq, dim), at, "out")
+    if ws is not None and ws.get_device() != at:
+        raise ValueError(f"ws: on {ws.device}, expected CUDA device {at}")
+    scale = dim ** -0.5 if scale is None else scale
     held = s.table_len * c.page
     max_len = held if max_len is None else min(int(max_len), held)
-    st, L, cr, sr = _stream(dev), lib(), ctypes.byref(c), ctypes.byref(s)
+    L, cr, sr = lib(), ctypes.byref(c), ctypes.byref(s)
+    with _On(at):
+        st = _stream(dev)
 
-    def call(ws):
-        return L.qlin_attn_q8(cr, sr, q.data_ptr(), q_ld, Hq, scale, max_len, out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+        def call(ws):
+            return L.qlin_attn_q8(cr, sr, q.data_ptr(), q_ld, Hq, scale, max_len, out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                  st)
 
-    check(_on(dev, lambda: _call_with_workspace(call, lambda: L.qlin_attn_q8_workspace_bytes(cr, sr, Hq, max_len), dev,
-                                                st, ws)), "qlin_attn_q8")
+        check(_call_with_workspace(call, lambda: L.qlin_attn_q8_workspace_bytes(cr, sr, Hq, max_len), dev, st, ws),
+              "qlin_attn_q8")
     return out
 
 

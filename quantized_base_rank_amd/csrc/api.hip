@@ -1356,6 +1356,11 @@ int qlin_kv_read_q8(const qlin_kv_cache* cache, const qlin_kv_batch* batch, uint
 
 namespace {
 
+// Rows of query heads a sequence (on average) up to which 32 of them are taken
+// at a time by waves that stream the cache on their own; beyond, 256 at a time.
+// At 16, 32, 64, 128, 256 rows, us with the join: 16384 tokens, 64 query heads
+// over 8: 20, 30, 47, 80, 148 and 38, 39, 40, 44, 53; 16 sequences of 4096, 32
+// over 8: 48, 53, 88, 163 and (32 rows on) 106, 108, 120.
 constexpr int64_t kFewChunkRows = 64;
 
 // How attention over the cache is split.
@@ -1370,13 +1375,20 @@ ChunkPlan make_chunk_plan(const qlin_kv_cache* c, const qlin_kv_batch* s, int32_
   const int64_t T = s->tokens, g = heads_q / c->heads;
   const int64_t len = std::min<int64_t>(max_len, static_cast<int64_t>(s->table_len) * c->page);
   p.few = T * g <= kFewChunkRows * static_cast<int64_t>(s->batch);
-  const int64_t tiles = std::max<int64_t>(s->batch, ceil_div(T * g, 256)) * c->heads;
-  const int64_t want = p.few ? 1536 : 256, unit = p.few ? 128 : 64, least = p.few ? 128 : 512;
-  if (tiles < want) {
-    p.per = static_cast<int32_t>(std::max<int64_t>(least, unit * ceil_div(ceil_div(len * tiles, want), unit)));
-    p.splits = static_cast<int32_t>(ceil_div(len, p.per));
+  // One round of workgroups (two to a compute unit, or one of the wide ones),
+  // if that leaves each keys enough, and no share so long that one long
+  // sequence holds up the others.  Few rows, us with the join, in shares for
+  // 256, 512, 1024, 1536 workgroups (64 query heads over 8): 1 x 16384 tokens
+  // 18.9, 20.1, 27.9, 27.8; 4 x 4096 16.9, 17.1, 21.8, 22.1; 16 x up to 4096
+  // 44.7, 31.6, 34.9, 34.4; 32 x up to 8192 135, 91, 100, 95; 1 x 65536 39.3,
+  // 37.3, 44.5, 53.2.
+  const int64_t tiles = std::max<int64_t>(s->batch, ceil_div(T * g, p.few ? 32 : 256)) * c->heads;
+  const int64_t want = p.few ? 512 : 256, unit = p.few ? 128 : 64, least = p.few ? 128 : 512;
+  const int64_t per = clamp64(unit * ceil_div(ceil_div(len * tiles, want), unit), least, p.few ? 8192 : 1 << 30);
+  if (per < len) {
+    p.per = static_cast<int32_t>(per);
+    p.splits = static_cast<int32_t>(ceil_div(len, per));
   }
-  if (p.splits == 1) p.per = 1 << 30;
   size_t off = kCounterBytes;
   if (p.splits > 1) {
     const size_t rows = static_cast<size_t>(p.splits) * T * heads_q;

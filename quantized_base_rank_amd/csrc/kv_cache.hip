@@ -78,8 +78,9 @@ __global__ __launch_bounds__(256) void k_kv_write(KvWriteArgs a) {
 }
 
 __global__ __launch_bounds__(256) void k_kv_read(KvReadArgs a) {
+  // (lanes past D stay: the whole wave looks the token up)
   const int lane = threadIdx.x & 15, sub = (threadIdx.x & 63) >> 4, H = a.c.H, D = a.c.D;
-  if (8 * lane >= D) return;
+  const bool in = 8 * lane < D;
   each_part(a.s.T, H, [&](int t, int r0) {
     const Place p = place_of(a.s, a.c, t);
     if (!p.known) return;
@@ -89,14 +90,14 @@ __global__ __launch_bounds__(256) void k_kv_read(KvReadArgs a) {
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + 4 * i + sub, head = r < H ? r : r - H;
       const int64_t row = ((static_cast<int64_t>(p.page) * H + head) << a.c.page_shift) + p.row;
-      const bool there = p.page >= 0 && r < 2 * H;
+      const bool there = in && p.page >= 0 && r < 2 * H;
       c[i] = there ? *reinterpret_cast<const u32x2*>((r < H ? a.c.k : a.c.v) + row * D + 8 * lane) : u32x2{0u, 0u};
       s[i] = there ? (r < H ? a.c.ks : a.c.vs)[row] : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + 4 * i + sub, head = r < H ? r : r - H;
-      if (r < 2 * H)
+      if (in && r < 2 * H)
         *reinterpret_cast<u32x4*>((r < H ? a.k : a.v) + (static_cast<int64_t>(t) * H + head) * D + 8 * lane) = values8(c[i], s[i]);
     }
   });

@@ -228,7 +228,8 @@ def test_longer_than_said(qb):
 
 
 @pytest.mark.parametrize("Hkv,D,page,new,lens", [(1, 64, 16, [1, 1, 1], [1, 33, 100]), (8, 128, 64, [5, 0, 200], [5, 7, 260]),
-                                                 (3, 80, 32, [17, 40], [90, 40]), (2, 16, 16, [9, 3], [4, 300])])
+                                                 (3, 80, 32, [17, 40], [90, 40]), (2, 16, 16, [9, 3], [4, 300]),
+                                                 (5, 48, 16, [3] * 9 + [0, 1, 70], [40] * 12), (9, 96, 16, [1] * 200, list(range(1, 201)))])
 def test_cache_write_and_read(qb, Hkv, D, page, new, lens):
     """Codes and scales bit for bit as the oracle rounds them, all other rows of
     the cache as they were, and the rows read back."""
