@@ -4,7 +4,10 @@
 //     ds_ij = p_ij (do_i . v_j - delta_i),  dv_j = sum_i p_ij do_i,
 //     dk_j = c sum_i ds_ij q_i,             dq_i = c sum_j ds_ij k_j.
 // Two launches: dq, a workgroup for 128 query rows, which forms their delta and
-// walks the keys; then dk and dv, a workgroup for 128 keys, which walks the
+// walks the keys (the sum of a row's ds, which ought to be nothing, is the
+// error that delta has from the roundings of o; with the sum of p k, one more
+// product from operands at hand, dq is put right for it at the end, and delta
+// for the other launch); then dk and dv, a workgroup for 128 keys, which walks the
 // query rows of all heads that share them.  Scores are formed twice; in return
 // no sum needs atomics, so the results are the same from run to run.
 //
@@ -132,22 +135,17 @@ __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
   }
   delta += swap_halves(delta);
   const float lse2 = a.lse[o_row] * kLog2e;
-  if (in && h == 0) {  // for dk and dv, with their signs
-    const int64_t at = (static_cast<int64_t>(kvh) * a.T + t_row) * g + hg;
-    a.lse2[at] = -lse2;
-    a.delta[at] = -delta;
-  }
-
   const TileAt<DP> at = tile_at<DP>(lane);
-  f32x16 dq[DB];
+  f32x16 dq[DB], mean[DB];  // sums of ds k and of p k
+  float off = 0.0f;         // sum of ds
 #pragma unroll
-  for (int d = 0; d < DB; ++d) dq[d] = f32x16{};
-  // scores and do . v - delta of a tile's first and second 32 keys, then ds
+  for (int d = 0; d < DB; ++d) dq[d] = mean[d] = f32x16{};
+  // scores and do . v - delta of a tile's first and second 32 keys, then p and ds
   f32x16 s0, p0, s1, p1;
-  u32x4 d0[2], d1[2];
+  u32x4 e0[2], d0[2], e1[2], d1[2];
   // Operands of a tile's products in their order: X(second), Z(first),
   // Z(second), X(first of the next tile), and X(second) of that one again
-  constexpr int NX = 2 * KS, NZ = 2 * DB, kAll = 2 * NX + 2 * NZ, kAhead = 8;
+  constexpr int NX = 2 * KS, NZ = 2 * DB, kAll = 2 * NX + 2 * NZ, kAhead = 4;
   static_assert(kAll % kAhead == 0 && NX >= kAhead, "the ring goes on into the next tile");
   u32x4 ring[kAhead];
   auto operand = [&](int buf, int n) __attribute__((always_inline)) {
@@ -156,12 +154,14 @@ __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
     const int m = n - NX - 2 * NZ;
     return row_operand<DP>(m % 2 == 0 ? sk(buf + 1) : sv(buf + 1), at, m < NX ? 0 : 1, m % NX / 2);
   };
-  auto value = [&](auto cut, int j0, f32x16& s, const f32x16& dp, int i) __attribute__((always_inline)) {
+  auto value = [&](auto cut, int j0, f32x16& s, f32x16& dp, int i) __attribute__((always_inline)) {
     const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.c2, -lse2));
-    s[i] = decltype(cut)::value && j0 + acc_row(i, h) >= seen ? 0.0f : p * dp[i];
+    s[i] = decltype(cut)::value && j0 + acc_row(i, h) >= seen ? 0.0f : p;
+    dp[i] *= s[i];
+    off += dp[i];
   };
-  auto pack = [&](const f32x16& s, u32x4 (&ds)[2], int i) __attribute__((always_inline)) {  // values i, i + 1
-    ds[i / 8][i % 8 / 2] = pack_bf16x2(s[i], s[i + 1]);
+  auto pack = [&](const f32x16& s, u32x4 (&p)[2], int i) __attribute__((always_inline)) {  // values i, i + 1
+    p[i / 8][i % 8 / 2] = pack_bf16x2(s[i], s[i + 1]);
   };
   auto step = [&](auto cut, int tile, int buf) __attribute__((always_inline)) {
     const int j0 = tile * kBT;
@@ -180,6 +180,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
       } else if constexpr (n < NX + 2 * NZ) {
         constexpr int m = n - NX, kg = m / DB;
         dq[m % DB] = mfma32(f, kg < 2 ? d0[kg & 1] : d1[kg & 1], dq[m % DB]);
+        mean[m % DB] = mfma32(f, kg < 2 ? e0[kg & 1] : e1[kg & 1], mean[m % DB]);
       } else {
         constexpr int m = n - NX - 2 * NZ;
         if (m % 2 == 0)
@@ -197,13 +198,13 @@ __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
 #pragma unroll
         for (int i = 16 * n / NX; i < 16 * (n + 1) / NX; ++i) {
           value(cut, j0, s0, p0, i);
-          if (i % 2 == 1) pack(s0, d0, i - 1);
+          if (i % 2 == 1) pack(s0, e0, i - 1), pack(p0, d0, i - 1);
         }
       } else if constexpr (n < NX + NZ) {
 #pragma unroll
         for (int i = 16 * (n - NX) / NZ; i < 16 * (n - NX + 1) / NZ; ++i) {
           value(cut, j0 + 32, s1, p1, i);
-          if (i % 2 == 1) pack(s1, d1, i - 1);
+          if (i % 2 == 1) pack(s1, e1, i - 1), pack(p1, d1, i - 1);
         }
       } else if constexpr (n < NX + 2 * NZ) {
 #pragma unroll
@@ -243,6 +244,16 @@ __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnBwdArgs a) {
   if (t < tiles_end) step(cut, t, 0);
   if (t + 1 < tiles_end) step(cut, t + 1, 1);
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (loads into LDS end before the workgroup does)
+  off += swap_halves(off);
+  if (in && h == 0) {  // for dk and dv, with their signs
+    const int64_t at = (static_cast<int64_t>(kvh) * a.T + t_row) * g + hg;
+    a.lse2[at] = -lse2;
+    a.delta[at] = -(delta + off);
+  }
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dq[d][i] -= off * mean[d][i];
   store_row<DB>(dq, a.scale, a.dq + t_row * a.dq_ld + hq * D, D, in, h);
 }
 
