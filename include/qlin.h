@@ -517,8 +517,9 @@ int qlin_bwd_q8(const qlin_qweight *w, const int8_t *xq, const float *x_scale, i
  * for the sums of the backward pass; sums and statistics are fp32, taken in an
  * order that depends on the sizes only.
  * Limits (QLIN_E_SHAPE): dim a multiple of 16, 16 .. 128; heads_q a multiple
- * of heads_kv, at most 128 times it, heads_q <= 4096; tokens * heads_q < 2^31 -
- * 2^16; 1 <= batch <= 2^20; ld < 2^23; scale finite and > 0.  No tokens: nothing is done.
+ * of heads_kv, at most 128 times it, heads_q <= 4096; tokens * heads_q < 2^30;
+ * 1 <= batch <= 2^20; batch * heads_kv <= 2^22; ld < 2^23; scale finite and
+ * > 0.  No tokens: nothing is done.
  * int32 arrays (cu, lens, table) need 4-byte alignment only.  Outputs must
  * overlap neither inputs nor one another nor the workspace
  * (QLIN_E_OVERLAP; parts of one buffer with the same ld may alternate).
@@ -644,7 +645,8 @@ int qlin_dequant_bf16(const qlin_qweight *w, uint16_t *W_out, hipStream_t stream
  * "k_quant_q8", "k_rmsnorm_q8", "k_rmsnorm_bwd" (both of its launches),
  * "k_w8a8_few", "k_w8a8_gemm" (with the join of its shares), "k_du",
  * "k_tokens" (8-bit rows), "k_kv_write", "k_kv_read", "k_attn_fwd",
- * "k_attn_q8", "k_attn_bwd" (all launches of a call).  `start` and `stop` are HIP events created by the caller; the elapsed time between them is the
+ * "k_attn_q8", "k_attn_bwd" (all launches of a call).  `start` and `stop` are
+ * HIP events created by the caller; the elapsed time between them is the
  * kernel's duration on the device.  kernel = NULL disarms.  One hook per
  * process (a later call replaces an armed one).  Host only; QLIN_E_NULL for
  * a missing event, QLIN_E_SHAPE for a name of 64 or more characters.

@@ -1201,7 +1201,9 @@ int check_heads(int32_t batch, int64_t tokens, int32_t heads_q, int32_t heads_kv
   if (batch < 1 || batch > (1 << 20) || tokens < 0) return QLIN_E_SHAPE;
   if (heads_kv < 1 || heads_q < heads_kv || heads_q > 4096 || heads_q % heads_kv != 0) return QLIN_E_SHAPE;
   if (heads_q / heads_kv > kMaxShare) return QLIN_E_SHAPE;
-  if (tokens >= (int64_t{1} << 31) || tokens * heads_q >= (int64_t{1} << 31) - (1 << 16)) return QLIN_E_SHAPE;
+  // launches of 256 threads for every 128 rows, and one more for each sequence and key head, stay below 2^32 threads
+  if (tokens >= (int64_t{1} << 30) || tokens * heads_q >= (int64_t{1} << 30)) return QLIN_E_SHAPE;
+  if (static_cast<int64_t>(batch) * heads_kv > (int64_t{1} << 22)) return QLIN_E_SHAPE;
   if (dim < 16 || dim > 128 || dim % 16 != 0) return QLIN_E_SHAPE;
   return QLIN_OK;
 }
@@ -1363,6 +1365,10 @@ namespace {
 // over 8: 48, 53, 88, 163 and (32 rows on) 106, 108, 120.
 constexpr int64_t kFewChunkRows = 64;
 
+// Launches of 256 threads stay below 2^32 threads: of the shares, and of their
+// join, which takes four rows at a time.
+constexpr int64_t kMaxChunkBlocks = (int64_t{1} << 24) - 1, kMaxJoinRows = int64_t{1} << 25;
+
 // How attention over the cache is split.
 struct ChunkPlan {
   bool few = false;           // rows of 32 at a time (attn_few.hip)
@@ -1384,7 +1390,10 @@ ChunkPlan make_chunk_plan(const qlin_kv_cache* c, const qlin_kv_batch* s, int32_
   // 37.3, 44.5, 53.2.
   const int64_t tiles = std::max<int64_t>(s->batch, ceil_div(T * g, p.few ? 32 : 256)) * c->heads;
   const int64_t want = p.few ? 512 : 256, unit = p.few ? 128 : 64, least = p.few ? 128 : 512;
-  const int64_t per = clamp64(unit * ceil_div(ceil_div(len * tiles, want), unit), least, p.few ? 8192 : 1 << 30);
+  int64_t per = clamp64(unit * ceil_div(ceil_div(len * tiles, want), unit), least, p.few ? 8192 : 1 << 30);
+  const int64_t launched = (T * g / (p.few ? 32 : 256) + s->batch) * c->heads;
+  const int64_t most = T * heads_q > kMaxJoinRows ? 1 : std::max<int64_t>(1, kMaxChunkBlocks / launched);
+  per = std::max(per, unit * ceil_div(ceil_div(len, most), unit));
   if (per < len) {
     p.per = static_cast<int32_t>(per);
     p.splits = static_cast<int32_t>(ceil_div(len, per));

@@ -196,16 +196,8 @@ __device__ __forceinline__ void store_row(const f32x16 (&x)[DB], float f, uint16
     }
 }
 
-// The page that holds place j of sequence b, or -1: a table entry outside the
-// cache, or a place outside the table, is a page that is not there.
-__device__ __forceinline__ int page_of(const int32_t* table, int table_len, int pages, int page_shift, int b, int j) {
-  const int at = j >> page_shift;
-  if (j < 0 || at >= table_len) return -1;
-  const int p = table[static_cast<int64_t>(b) * table_len + at];
-  return p < 0 || p >= pages ? -1 : p;
-}
-
-// The same for a place that is the wave's.
+// The page that holds place j of sequence b (the wave's), or -1: a table entry
+// outside the cache, or a place outside the table, is a page that is not there.
 __device__ __forceinline__ int uniform_page(const int32_t* table, int table_len, int pages, int page_shift, int b, int j) {
   const int at = j >> page_shift;
   if (j < 0 || at >= table_len) return -1;

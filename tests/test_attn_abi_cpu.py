@@ -201,3 +201,28 @@ def test_cache_overlaps():
                          *((getattr(c, y), k) for y, k in memory.items() if y != x)):
             bad = cache(**{x: other + (m - 1) // 16 * 16})
             assert L.qlin_kv_write_q8(ctypes.byref(bad), ctypes.byref(s), far(7), HKV * D, far(8), HKV * D, None) == OVERLAP
+
+
+def test_launch_limits():
+    """Sizes whose launches would pass 2^32 threads are refused, or not split further."""
+    L = _lib.lib()
+    n = L.qlin_attn_bwd_workspace_bytes
+    assert n(1 << 20, 1 << 20, 4, 4, 64) > 0 and n(1 << 20, 1 << 20, 5, 5, 64) == 0
+    assert n(1, (1 << 24) - 1, 64, 8, 64) > 0 and n(1, 1 << 24, 64, 8, 64) == 0
+    assert L.qlin_attn_fwd(*swap(swap(fwd_args(), 7, 1 << 20), 10, HQ)) == SHAPE
+    w = L.qlin_attn_q8_workspace_bytes
+
+    def shares(b, tokens, heads, hq, length):
+        c, s = cache(heads=heads, page=256), batch(batch=b, table_len=1 << 22, tokens=tokens)
+        one = w(ctypes.byref(c), ctypes.byref(s), hq, 1)  # (not in shares)
+        rest = w(ctypes.byref(c), ctypes.byref(s), hq, length) - one
+        assert one > 0 and rest >= 0
+        return max(1, rest // (tokens * hq * (D + 2) * 4))
+
+    assert shares(1, 1, 1, 1, 1 << 30) > 1
+    for b, tokens, heads, hq in ((32, 32, 8, 8), (1 << 10, 1 << 10, 8, 64), (1 << 17, 1 << 17, 8, 32), (1 << 20, 1 << 20, 4, 16),
+                                 (1 << 20, 1 << 20, 4, 64), (1, 20000, 2, 64), (3, 1, 1, 128)):
+        n = shares(b, tokens, heads, hq, 1 << 30)
+        few = tokens * (hq // heads) <= 64 * b
+        launched = (tokens * (hq // heads) // (32 if few else 256) + b) * heads * n
+        assert launched < 1 << 24 and (n == 1 or (tokens * hq + 3) // 4 < 1 << 24), (b, tokens, n)
