@@ -400,10 +400,10 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
       for (int n = 0; n < 2 * kLoads; ++n) load_part(buf + 3, n);
     }
     if constexpr (PAGED) {
-      if (on) {
+      if (on) {  // (fetched in each branch: once behind both takes 279 spills)
 #pragma unroll
-      for (int n = 0; n < 2 * kHold; ++n) fetch(j + 3, page_now, n);
-}
+        for (int n = 0; n < 2 * kHold; ++n) fetch(j + 3, page_now, n);
+      }
       queue = queue >> 4 | blocks(page_k) << 12;
       page_now = page_k;
       page_k = pages_of(j + 5);
