@@ -128,17 +128,29 @@ __device__ __forceinline__ void load_word_to_lds(const void* base, uint32_t byte
   __builtin_amdgcn_raw_ptr_buffer_load_lds(uniform_rsrc(base, bytes), (lds_ptr_t)dst, 4, at, 0, 0, 0);
 }
 
-// Sets the elements that are not finite to zero; 0 if there were none.
-__device__ __forceinline__ uint32_t clear_nonfinite(u32x4& v) {
-  uint32_t any = 0;
+// Whether a lane's elements are not all finite: an exponent of all ones.
+template <int N>
+__device__ __forceinline__ bool any_nonfinite(const u32x4 (&v)[N]) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 top = {0, 0};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u16x2 e = __builtin_bit_cast(u16x2, v[i][j] & 0x7FFF7FFFu);
+      top = __builtin_elementwise_max(top, e);
+    }
+  return top.x >= 0x7F80 || top.y >= 0x7F80;
+}
+
+// Sets the elements that are not finite to zero.
+__device__ __forceinline__ void clear_nonfinite(u32x4& v) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     // an exponent of all ones carries into its half's top bit
     const uint32_t m = ((v[j] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-    any |= m;
     v[j] &= ~((m >> 15) * 0xFFFFu);
   }
-  return any;
 }
 
 // The other half's value, and the larger of both, in each lane.

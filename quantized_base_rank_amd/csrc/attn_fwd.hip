@@ -78,7 +78,9 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t sv2[kTile];
   __shared__ __attribute__((aligned(16))) uint8_t sv3[kTile];
   __shared__ __attribute__((aligned(16))) float s_scale[PAGED ? R * 2 * kBN : 1];
-  __shared__ int s_odd[R];  // 1 + the step whose values in this buffer were not finite
+  // 1 + the step whose values in this buffer were not finite, a wave's part each
+  // (a wave sets its own up, so that none waits for another)
+  __shared__ __attribute__((aligned(16))) uint32_t s_odd[R * 4];
   auto sk = [&](int buf) { return buf % R == 0 ? sk0 : buf % R == 1 ? sk1 : R == 3 || buf % R == 2 ? sk2 : sk3; };
   auto sv = [&](int buf) { return buf % R == 0 ? sv0 : buf % R == 1 ? sv1 : R == 3 || buf % R == 2 ? sv2 : sv3; };
 
@@ -97,7 +99,7 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   const int base = PAGED ? share * a.per : 0, until = PAGED ? base + a.per : 0x7FFFFFFF;
   if (base > 0 && base >= len) return;  // (k_attn_join counts a sequence's shares alike)
   auto inside = [&](int v) { return v < until ? v : until; };
-  if (tid < R) s_odd[tid] = 0;
+  if (lane < R) s_odd[lane * 4 + wave] = 0;
 
   // this lane's query rows, one of each 32 of the wave's
   const int tok0 = rt.row0 / a.g, rem0 = rt.row0 - tok0 * a.g;
@@ -236,22 +238,25 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   for (int n = 0; n < 2 * DB; ++n) vf[n] = u32x4{0, 0, 0, 0};
 
   // Values of step j that are not finite, where the mask cuts the step: set to
-  // zero in LDS, by each wave in the part that it loaded, and noted ..
+  // zero in LDS, by each wave in the part that it loaded, and noted (the part
+  // is read two units before it is looked at) ..
+  u32x4 mine[kLoads];
+  auto read_values = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      mine[i] = *reinterpret_cast<const u32x4*>(sv(buf) + (wave * kLoads + i) * 1024 + lane * 16);
+  };
   auto clear_values = [&](int j, int buf) __attribute__((always_inline)) {
-    uint32_t odd = 0;
+    if (__ballot(any_nonfinite(mine)) == 0) return;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      u32x4* const at = reinterpret_cast<u32x4*>(sv(buf) + (wave * kLoads + i) * 1024 + lane * 16);
-      u32x4 v = *at;
-      const uint32_t bad = clear_nonfinite(v);
-      if (bad != 0) *at = v;
-      odd |= bad;
+      clear_nonfinite(mine[i]);
+      *reinterpret_cast<u32x4*>(sv(buf) + (wave * kLoads + i) * 1024 + lane * 16) = mine[i];
     }
-    if (odd != 0) s_odd[buf % R] = j + 1;
+    s_odd[buf % R * 4 + wave] = j + 1;
   };
   // .. and, as they are, added to the rows that see them
-  auto add_nonfinite = [&](int j, int buf) {
-    if (PAGED || s_odd[buf % R] != j + 1) return;
+  auto add_nonfinite = [&](int j) {
     const int j0 = base + j * kBN;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
@@ -372,6 +377,12 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   const bool active = wave * 64 <= last_in;
   auto step = [&](auto cut, int j, int buf) __attribute__((always_inline)) {
     const bool on = active && (!decltype(cut)::value || base + j * kBN < w_end);
+    u32x4 odd = {0, 0, 0, 0};
+    if constexpr (decltype(cut)::value && !PAGED) {
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+      read_values(buf + 1);
+      odd = *reinterpret_cast<const u32x4*>(s_odd + buf % R * 4);
+    }
     if (on) {
       unit(cut, std::integral_constant<int, 0>{}, j, buf);
       unit(cut, std::integral_constant<int, 1>{}, j, buf);
@@ -379,17 +390,17 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
     if constexpr (PAGED) {
       barrier<63>();
     } else {
-      if constexpr (decltype(cut)::value) {
-        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
-        clear_values(j + 1, buf + 1);
-      }
+      if constexpr (decltype(cut)::value) clear_values(j + 1, buf + 1);
       barrier<2 * kLoads>();
     }
     pin();
     if (on) {
       unit(cut, std::integral_constant<int, 2>{}, j, buf);
       unit(cut, std::integral_constant<int, 3>{}, j, buf);
-      if constexpr (decltype(cut)::value && !PAGED) add_nonfinite(j, buf);
+      if constexpr (decltype(cut)::value && !PAGED) {
+        const uint32_t now = static_cast<uint32_t>(j) + 1;
+        if (__ballot(odd.x == now || odd.y == now || odd.z == now || odd.w == now) != 0) add_nonfinite(j);
+      }
     } else if constexpr (PAGED) {
 #pragma unroll
       for (int n = 0; n < 4 * kHold; ++n) put(buf + 2, n);
@@ -433,6 +444,7 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
 #pragma unroll
         for (int n = 0; n < 2 * kLoads; ++n) load_part(i, n);
       __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * kLoads) : "memory");
+      read_values(0);
       clear_values(0, 0);
     }
     barrier<63>();
