@@ -242,3 +242,27 @@ def test_many_heads(qb, Hq, Hkv):
     T.check_gradient(lens, Hq, Hkv, D, q, k, v, do, *qb.qlin_attn_bwd(q, k, v, o, lse, do, cu), 0.25)
     c = T.Paged(qb, 2, [9, 40], lens, Hkv, D, 256)
     c.check(q, qb.qlin_attn_q8(q, c.cache, c.batch), 0.25)
+
+
+@pytest.mark.parametrize("lens,new,Hq,Hkv,D,page", [
+    ([3000], [150], 4, 2, 128, 64),             # many rows in shares
+    ([3000], [150], 4, 2, 64, 16),
+    ([1500], [300], 128, 128, 16, 32),          # many rows, every key in one workgroup
+    ([1500], [300], 128, 128, 80, 128),
+    ([20000, 40, 1, 700], [1, 1, 1, 1], 64, 64, 16, 64),  # few rows, the longest shares there are
+])
+def test_holes_in_long_sequences(qb, lens, new, Hq, Hkv, D, page):
+    """Pages that are not there between whole steps, and steps that nothing cuts
+    again behind them; NaN in every page of nobody."""
+    c = T.Paged(qb, 11, lens, new, Hkv, D, page, spare=9)
+    for b in range(len(lens)):
+        held = -(-lens[b] // page)
+        for i in [held // 3, held // 3 + 1, *range(held // 2, held, 13)]:
+            if 0 < i < held - 1:
+                c.table[b, i] = -1 if i % 2 else 1 << 30
+    used = {int(p) for p in c.table.flatten() if 0 <= int(p) < c.cache.k_codes.shape[0]}
+    for p in set(range(c.cache.k_codes.shape[0])) - used:
+        c.cache.k_scale[p] = c.cache.v_scale[p] = float("nan")
+    q = T.heads(3, sum(new), Hq, D)
+    o = qb.qlin_attn_q8(q, c.cache, qb.KVBatch(c.batch.cu, c.batch.lens, c.table.cuda()), max_len=max(lens))
+    c.check(q, o, D ** -0.5)
