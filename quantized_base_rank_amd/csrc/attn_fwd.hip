@@ -33,15 +33,15 @@
 // not finite are set to zero for the product (0 times them is not 0) and added
 // to the rows that see them.
 //
-// Measured, heads of 128.  8192 tokens, 64 query heads over 8: 1087 us, 1.01
+// Measured, heads of 128.  8192 tokens, 64 query heads over 8: 1100 us, 1.00
 // PFLOP/s (a library product of 8192^3 reaches 1.20), matrix cores busy 49 % of
 // the cycles, 6.8 vector instructions to one of theirs; 2048 tokens behind
 // 30000 in the cache, 32 over 8: 1540 us, 0.68 PFLOP/s, busy 26 %, 11.1 to one
 // with the scales and the codes' conversion.  Heads of 64, 32 over 8, 8192
 // tokens: 340 us, 0.81 PFLOP/s: half the products to the same softmax.  4 x
-// 1024 tokens, 32 heads: 82 us, where 28 of a head's 40 steps take the form for
-// cut steps (whole steps go in turns of the ring; choosing for each step alone
-// moves O about, 1193 spills).  32 rows a wave in place of 64, the products not
+// 1024 tokens, 32 heads: 77 us, where 16 of a head's 40 steps take the form for
+// cut steps (the form chosen for each step in the ring moves O about: 1193
+// spills).  32 rows a wave in place of 64, the products not
 // between the parts of the softmax: 437 us (heads of 64), 1850 (cache).  Loads
 // in a burst behind the barrier: 1222 and 1676 where these take 1154 and 1559.
 #include "attn_common.hpp"
@@ -135,7 +135,12 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   const int w_end = wave * 64 > last_in ? 0 : inside(first + token(w_last) + 1);
   const int sees_all = inside(first + tok0 + 1) - base;
   const int steps = end > base ? (end - base + kBN - 1) / kBN : 0;
-  const int whole = sees_all >= 2 * kBN ? (sees_all / kBN - 1) / R * R : 0;  // steps that nothing cuts, nor the next
+  // Steps, in turns of the ring, that nothing cuts.  The last step of a turn
+  // takes the next one's first scores as if it were cut where keys are packed
+  // (4 x 1024 tokens, 32 heads: 82 -> 77 us; 8192 tokens, eight heads to a key
+  // head: 1090 -> 1100); over the cache turns end a step sooner (2048 tokens
+  // behind 30000: 1560, the other way 1600).
+  const int whole = sees_all >= kBN ? (sees_all / kBN - (PAGED ? 1 : 0)) / R * R : 0;
 
   // ---- packed keys and values, straight into LDS: load i of a wave fills
   // kRowsPer rows; rows past the sequence and elements past D lie outside the
@@ -326,7 +331,7 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
   uint32_t queue = 0xFFFF;  // blocks of 16 keys that are there, four bits a step from step j on
 
   // Unit u of step j: Y(u) between X(next) and Z(last)
-  auto unit = [&](auto cut, auto number, int j, int buf) __attribute__((always_inline)) {
+  auto unit = [&](auto cut, auto next_cut, auto number, int j, int buf) __attribute__((always_inline)) {
     constexpr int u = decltype(number)::value, b = u & 1, nb = b ^ 1, half = u >> 1, next_half = (u + 1 & 3) >> 1;
     constexpr int NS = KS + 2 * DB;  // slots
     constexpr bool reload = b == 0;
@@ -363,7 +368,7 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
       }
       constexpr int kFirst = NS - 6 > KS + 1 ? NS - 6 : NS - 4;  // (the scores are there by then)
       if constexpr (n >= kFirst && n < kFirst + 4)
-        score4(cut, s[nb], base + next_j * kBN, next_buf, next_half, nb, u == 3 ? queue >> 4 : queue, 4 * (n - kFirst));
+        score4(next_cut, s[nb], base + next_j * kBN, next_buf, next_half, nb, u == 3 ? queue >> 4 : queue, 4 * (n - kFirst));
       if constexpr (n == NS - 1) {
         settle(15);
         whole_top();
@@ -387,28 +392,31 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
     pin();
   };
   const bool active = wave * 64 <= last_in;
-  auto step = [&](auto cut, int j, int buf) __attribute__((always_inline)) {
+  // (next_cut: the next step may be cut)
+  auto step = [&](auto cut, auto next_cut, int j, int buf) __attribute__((always_inline)) {
     const bool on = active && (!decltype(cut)::value || base + j * kBN < w_end);
     u32x4 odd = {0, 0, 0, 0};
-    if constexpr (decltype(cut)::value && !PAGED) {
+    if constexpr (decltype(next_cut)::value && !PAGED) {
       __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
       read_values(buf + 1);
+    }
+    if constexpr (decltype(cut)::value && !PAGED) {
       odd = *reinterpret_cast<const u32x4*>(s_odd + buf % R * 4);
     }
     if (on) {
-      unit(cut, std::integral_constant<int, 0>{}, j, buf);
-      unit(cut, std::integral_constant<int, 1>{}, j, buf);
+      unit(cut, cut, std::integral_constant<int, 0>{}, j, buf);
+      unit(cut, cut, std::integral_constant<int, 1>{}, j, buf);
     }
     if constexpr (PAGED) {
       barrier<63>();
     } else {
-      if constexpr (decltype(cut)::value) clear_values(j + 1, buf + 1);
+      if constexpr (decltype(next_cut)::value) clear_values(j + 1, buf + 1);
       barrier<2 * kLoads>();
     }
     pin();
     if (on) {
-      unit(cut, std::integral_constant<int, 2>{}, j, buf);
-      unit(cut, std::integral_constant<int, 3>{}, j, buf);
+      unit(cut, cut, std::integral_constant<int, 2>{}, j, buf);
+      unit(cut, next_cut, std::integral_constant<int, 3>{}, j, buf);
       if constexpr (decltype(cut)::value && !PAGED) {
         const uint32_t now = static_cast<uint32_t>(j) + 1;
         if (__ballot(odd.x == now || odd.y == now || odd.z == now || odd.w == now) != 0) add_nonfinite(j);
@@ -474,10 +482,12 @@ __global__ __launch_bounds__(256, 1) void k_attn(AttnArgs a) {
     pin();
     int j = 0;
     for (; j < whole && (!PAGED || (queue & 0xFFFFu) == 0xFFFFu); j += R)
-      each<R>([&](auto i) __attribute__((always_inline)) { step(uncut, j + i, i); });
+      each<R>([&](auto i) __attribute__((always_inline)) {
+        step(uncut, std::integral_constant<bool, !PAGED && decltype(i)::value == R - 1>{}, j + i, i);
+      });
     for (; j < steps; j += R)
       each<R>([&](auto i) __attribute__((always_inline)) {
-        if (j + i < steps) step(cut, j + i, i);
+        if (j + i < steps) step(cut, cut, j + i, i);
       });
     // the last unit's share of O
 #pragma unroll
